@@ -487,6 +487,131 @@ int cache_lru_plan(moe_cache* c, const moe_ws* ws, int layer, int K, moe_swap* p
 int moe_cache_apply_lru(moe_cache* c, const moe_swap* plan_dev, const int32_t* n_dev, moe_stream_t compute,
                         moe_stream_t copy);
 
+/* ------------------------------------------ the attention half of a layer
+ * The pages keep a request's context beside the MoE path (Strata expert paths,
+ * "KV" reuse and verify windows) without giving its kernels; the calls below
+ * are this library's own: keys and values in a paged cache, the position
+ * rotation on the way in, attention of the newest tokens over the pages, and
+ * the norms around a block on the fp32 residual stream.
+ *
+ * A call serves B requests at once.  Request b's new tokens are rows
+ * q_start[b] .. q_start[b+1] - 1 of the call's T token rows; kv_len[b] counts
+ * its tokens in the cache with the new ones, so token i of the n_b new ones is
+ * at position p = kv_len[b] - n_b + i.  Position p lives in page
+ * page_table[b * table_stride + p / page], place p % page.  n_b = 0 is allowed;
+ * q_start is non-decreasing with q_start[0] >= 0 and q_start[B] <= T; rows
+ * outside [q_start[0], q_start[B]) are neither read nor written. */
+
+/* The page pools of one layer's keys and values (device memory of the caller).
+ * Element (page, head, place, column) is at page * page_stride + head *
+ * head_stride + place * tok_stride + column, in both pools.  The strides are
+ * in elements, positive, at least D and multiples of 16 bytes; the pools are
+ * 16-byte aligned. */
+typedef struct {
+  void* k;
+  void* v;
+  int e4m3;              /* 0: bf16 elements; 1: FP8-E4M3 elements                     */
+  int Hkv, D;            /* key heads 1..1024; columns 64, 128 or 256                  */
+  int page, npages;      /* tokens in a page (a power of two, 1..65536), pages in a pool */
+  long long page_stride, head_stride, tok_stride;
+  const float* k_scale;  /* fp32 [Hkv] device: a stored code c stands for c * scale;   */
+  const float* v_scale;  /*   NULL: 1.  Read only for E4M3 pools                       */
+} moe_kv_pages;
+
+typedef struct {
+  const int32_t* q_start;    /* int32 [B + 1] device                                       */
+  const int32_t* kv_len;     /* int32 [B] device                                           */
+  const int32_t* page_table; /* int32 [B][table_stride] device                             */
+  int B, T;                  /* requests; token rows                                       */
+  int max_n;                 /* about the largest n_b: picks a tile size, never the result */
+  int table_stride;          /* entries of a row: a request holds at most page times this  */
+} moe_kv_batch;
+
+typedef struct moe_rope moe_rope;       /* the rotation's frequencies */
+typedef struct moe_attn_ws moe_attn_ws; /* scratch of the attention calls, error word */
+
+/* Rotation of the first `rot` columns of a head by position p: pair i is columns
+ * (i, i + rot/2), or (2i, 2i + 1) when interleaved, turned by the angle
+ * p * f_i: (u, w) -> (u cos - w sin, w cos + u sin).  f_i = inv_freq_host[i]
+ * (double [rot/2], finite) or, with NULL, theta^(-2i/rot).  The angle is kept
+ * as a 64-bit fixed-point fraction of a turn: exact to 2^-33 turn at every
+ * 32-bit position.  rot a multiple of 16 in [16, 256]; theta > 0 and finite.
+ * Synchronous (allocates the table). */
+int moe_rope_create(moe_rope** out, int rot, int interleaved, double theta, const double* inv_freq_host);
+int moe_rope_destroy(moe_rope* r);
+
+/* Append the call's new keys and values to the cache, keys rotated by position,
+ * and rotate the queries.  q bf16 [T][Hq][D] -> q_out (may be q), k and v bf16
+ * [T][Hkv][D]; *_stride: elements between tokens (heads are D apart), multiples
+ * of 8, at least heads * D (not checked for T <= 1); all pointers 16-byte
+ * aligned.  q may be NULL (Hq 0), rope NULL (nothing turns).  Rotation in fp32, one rounding to the stored type: bf16 to
+ * nearest even; E4M3(x / scale) to nearest even, saturating at 448, NaN kept.
+ * A position outside [0, page * table_stride), or a page id outside
+ * [0, npages), records MOE_ERANGE in err_dev (int32[1], may be NULL) and
+ * nothing is stored for that token.  Two tokens must not share a place.
+ * Asynchronous on `stream`. */
+int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q,
+                  long long q_stride, uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k,
+                  long long k_stride, const uint16_t* v, long long v_stride, int32_t* err_dev, moe_stream_t stream);
+
+/* Scratch for moe_paged_attention with Hq query heads on Hkv key heads of D
+ * columns (Hq a multiple of Hkv, at most 64 times it): the parts of requests
+ * split over their length, and the device error word.  Independent of batch
+ * and lengths. */
+int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D);
+int moe_attn_ws_destroy(moe_attn_ws* ws);
+typedef struct {
+  int32_t* error; /* int32[1] device error word (first error wins) */
+} moe_attn_ws_view;
+int moe_attn_ws_get_view(const moe_attn_ws* ws, moe_attn_ws_view* out);
+/* Synchronise `stream`, return the workspace's device error word and reset it. */
+int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
+
+/* Attention of every new token over its request's pages.  With group
+ * g = Hq / Hkv, token at position p, query head h reads key head h / g:
+ *   s_j = scale * q . k_j over the keys j <= p (and j > p - window if window > 0),
+ *   o = sum_j exp(s_j) v_j / sum_j exp(s_j).
+ * A token that sees no key (p < 0) gets zeros.  What lies in the pages outside
+ * a request's kv_len keys is never used, whatever it holds, and pages wholly
+ * before every window of a call need no valid table entry.
+ *   q, o  bf16 [T][Hq][D]; strides between tokens as in moe_kv_append; o must not
+ *         overlap q.
+ * Scores, softmax sums and outputs accumulate in fp32; the weights exp(s - m)
+ * are rounded to 16 bits for the product with v.  A key in a page whose id is
+ * outside [0, npages) reads as zeros and records MOE_ERANGE in the workspace's
+ * error word; so does kv_len beyond page * table_stride, cut there.  The result
+ * does not vary between runs.  scale finite; window >= 0, 0 for none.
+ * Asynchronous on `stream`; one stream drives a workspace at a time. */
+int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const uint16_t* q, long long q_stride, int Hq,
+                        uint16_t* o, long long o_stride, float scale, int window, moe_attn_ws* ws,
+                        moe_stream_t stream);
+
+/* The norms around a block, its gate and its residual add in one pass:
+ *   z  = post_norm ? w_post * y / sqrt(mean(y^2) + eps) : y
+ *   x_out = x + res_scale * g * z,   g = gate, sigmoid(gate) or 1
+ *   xn = w_pre * x_out / sqrt(mean(x_out^2) + eps).
+ * moe_residual_rmsnorm is the case without weights, gate, scale and post-norm. */
+typedef struct {
+  const uint16_t* y;       /* bf16 [T][H] the block's output, or NULL: x_out = x       */
+  long long y_stride;      /* elements between tokens                                  */
+  int post_norm;           /* normalise y first                                        */
+  const uint16_t* w_post;  /* bf16 [H] or NULL: ones                                   */
+  const uint16_t* gate;    /* bf16 [T][H], or NULL: none                               */
+  long long gate_stride;   /* elements between tokens; 0: one row for every token      */
+  int gate_sigmoid;        /* the gate is sigmoid(gate)                                */
+  float res_scale;
+  const uint16_t* w_pre;   /* bf16 [H] or NULL: ones                                   */
+  float eps;               /* > 0                                                      */
+} moe_block_norm_desc;
+
+/* x, x_out: fp32 [T][H] (x_out may be x, and may be NULL when x_out is not
+ * wanted); xn: bf16 [T][H] or NULL; strides in elements between tokens, at least
+ * H (not checked for T <= 1).  fp32 arithmetic, one rounding of xn.  1 <= H <=
+ * 16384.  Natural alignment suffices; 16-byte aligned rows of a multiple of 8
+ * columns take wider accesses.  Asynchronous on `stream`. */
+int moe_block_norm(const moe_block_norm_desc* d, const float* x, long long x_stride, float* x_out,
+                   long long x_out_stride, uint16_t* xn, long long xn_stride, int T, int H, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

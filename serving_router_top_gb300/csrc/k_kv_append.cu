@@ -1,0 +1,239 @@
+// New keys and values into a paged cache, with the position rotation on the way.
+//
+// The expert-path pages give no kernel for this step; the mathematics is the
+// rotation of column pairs (u, w) by a = p * f_i for a token at position p:
+//   u' = u cos a - w sin a,   w' = w cos a + u sin a.
+// p * f_i in fp32 is off by p * 2^-24 (0.06 rad at a million tokens), and fp64
+// runs at a small fraction of the fp32 rate here.  So f_i is kept as a 64-bit
+// fixed-point fraction of a turn: p times it, modulo 2^64, is the angle's
+// fraction of a turn with an error of at most p * 2^-65 (plus the 53 bits of
+// the given f_i), and only its top bits become a float, for sincospif.
+#include <math.h>
+
+#include <vector>
+
+#include "paged.cuh"
+
+struct moe_rope {
+  int rot, interleaved;
+  uint64_t* turns;  // device [rot/2]
+};
+
+namespace moe {
+namespace append {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 128;  // rot <= 256
+
+struct Args {
+  KvView kv;
+  const uint64_t* turns;
+  int rot, interleaved;
+  const uint16_t *q, *k, *v;
+  uint16_t* qo;
+  long long qs, qos, ks, vs;
+  int Hq;
+  int32_t* err;
+};
+
+__device__ __forceinline__ void unpack8(uint4 u, float f[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float f[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Two values -> two E4M3 bytes (low byte first), to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight columns of one head to where they belong: head < Hq is a query, then keys, then values.
+template <bool E4M3>
+__device__ __forceinline__ void store8(const Args& a, int t, int head, int col, const float f[8], int D, long long at) {
+  if (head < a.Hq) {
+    *reinterpret_cast<uint4*>(a.qo + (long long)t * a.qos + head * D + col) = pack8(f);
+    return;
+  }
+  if (at < 0) return;
+  const bool is_v = head >= a.Hq + a.kv.Hkv;
+  const int h = head - a.Hq - (is_v ? a.kv.Hkv : 0);
+  uint8_t* dst = (is_v ? a.kv.v : a.kv.k) + at + h * a.kv.head_stride;
+  if (!E4M3) {
+    *reinterpret_cast<uint4*>(dst + 2 * col) = pack8(f);
+  } else {
+    const float* sc = is_v ? a.kv.v_scale : a.kv.k_scale;
+    const float s = sc ? sc[h] : 1.0f;
+    uint2 u;
+    u.x = e4m3x2(f[0] / s, f[1] / s) | (e4m3x2(f[2] / s, f[3] / s) << 16);
+    u.y = e4m3x2(f[4] / s, f[5] / s) | (e4m3x2(f[6] / s, f[7] / s) << 16);
+    *reinterpret_cast<uint2*>(dst + col) = u;
+  }
+}
+
+// One CTA per token.
+template <bool E4M3, int D>
+__global__ void __launch_bounds__(kThreads) k_kv_append(const __grid_constant__ Args a) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ float2 cs[kMaxPairs];  // cos, sin of each pair's angle
+  const int t = blockIdx.x;
+  const int b = request_of(a.kv, t);
+  if (b < 0) return;
+  const long long pos = position_of(a.kv, b, t);
+  const int pairs = a.rot / 2;
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    // a signed fraction of a turn in [-1/2, 1/2); sincospif takes half turns
+    const long long frac = (long long)(uint64_t(pos) * a.turns[i]);
+    float c, s;
+    sincospif(float(frac) * 0x1p-63f, &s, &c);
+    cs[i] = make_float2(c, s);
+  }
+  long long at = -1;  // byte offset of (page, place) in the pools
+  const long long entry = pos >> a.kv.page_shift;
+  if (pos >= 0 && entry < a.kv.table_stride) {
+    const int id = a.kv.page_table[(long long)b * a.kv.table_stride + entry];
+    if (id >= 0 && id < a.kv.npages)
+      at = id * a.kv.page_stride + (pos & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
+  }
+  if (at < 0 && threadIdx.x == 0) set_error(a.err, MOE_ERANGE);
+  __syncthreads();
+  // an item is 16 columns of a head: the two halves' vectors of eight pairs, or two neighbours
+  constexpr int kItems = D / 16;
+  const int n = (a.Hq + 2 * a.kv.Hkv) * kItems;
+  for (int it = threadIdx.x; it < n; it += kThreads) {
+    const int head = it / kItems, j = it - head * kItems;
+    const bool turn = head < a.Hq + a.kv.Hkv && 16 * j < a.rot;
+    const int c0 = turn && !a.interleaved ? 8 * j : 16 * j;
+    const int c1 = turn && !a.interleaved ? pairs + 8 * j : 16 * j + 8;
+    const uint16_t* src = head < a.Hq ? a.q + (long long)t * a.qs + head * D
+                          : head < a.Hq + a.kv.Hkv ? a.k + (long long)t * a.ks + (head - a.Hq) * D
+                                                   : a.v + (long long)t * a.vs + (head - a.Hq - a.kv.Hkv) * D;
+    float x0[8], x1[8];
+    unpack8(*reinterpret_cast<const uint4*>(src + c0), x0);
+    unpack8(*reinterpret_cast<const uint4*>(src + c1), x1);
+    if (turn) {
+      if (!a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 r = cs[8 * j + i];
+          const float u = x0[i], w = x1[i];
+          x0[i] = u * r.x - w * r.y;
+          x1[i] = w * r.x + u * r.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 r = cs[8 * j + i], r2 = cs[8 * j + 4 + i];
+          float u = x0[2 * i], w = x0[2 * i + 1];
+          x0[2 * i] = u * r.x - w * r.y;
+          x0[2 * i + 1] = w * r.x + u * r.y;
+          u = x1[2 * i], w = x1[2 * i + 1];
+          x1[2 * i] = u * r2.x - w * r2.y;
+          x1[2 * i + 1] = w * r2.x + u * r2.y;
+        }
+      }
+    }
+    store8<E4M3>(a, t, head, c0, x0, D, at);
+    store8<E4M3>(a, t, head, c1, x1, D, at);
+  }
+}
+
+template <bool E4M3>
+cudaError_t launch(int D, int T, cudaStream_t s, const Args& a) {
+  switch (D) {
+    case 64: return launch_pdl(k_kv_append<E4M3, 64>, dim3(T), dim3(kThreads), 0, s, a);
+    case 128: return launch_pdl(k_kv_append<E4M3, 128>, dim3(T), dim3(kThreads), 0, s, a);
+    default: return launch_pdl(k_kv_append<E4M3, 256>, dim3(T), dim3(kThreads), 0, s, a);
+  }
+}
+
+}  // namespace append
+}  // namespace moe
+
+extern "C" int moe_rope_create(moe_rope** out, int rot, int interleaved, double theta, const double* inv_freq_host) {
+  using namespace moe;
+  if (!out || rot < 16 || rot > 2 * append::kMaxPairs || rot % 16) return MOE_EINVAL;
+  *out = nullptr;
+  if (!inv_freq_host && !(theta > 0.0 && isfinite(theta))) return MOE_EINVAL;
+  uint64_t turns[append::kMaxPairs];
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = inv_freq_host ? inv_freq_host[i] : pow(theta, -2.0 * i / rot);
+    if (!isfinite(f)) return MOE_EINVAL;
+    // the fraction of a turn in [0, 1): whole turns do nothing at whole positions
+    const double turn = f / 6.283185307179586476925286766559;
+    const double frac = turn - floor(turn);
+    const double scaled = ldexp(frac, 64);
+    turns[i] = scaled >= 18446744073709551616.0 ? 0 : uint64_t(scaled);
+  }
+  moe_rope* r = static_cast<moe_rope*>(calloc(1, sizeof(moe_rope)));
+  if (!r) return MOE_ENOMEM;
+  r->rot = rot;
+  r->interleaved = interleaved ? 1 : 0;
+  if (cudaMalloc(&r->turns, sizeof(turns)) != cudaSuccess) {
+    cudaGetLastError();
+    free(r);
+    return MOE_ENOMEM;
+  }
+  if (cudaMemcpy(r->turns, turns, size_t(rot / 2) * 8, cudaMemcpyHostToDevice) != cudaSuccess) {
+    cudaGetLastError();
+    moe_rope_destroy(r);
+    return MOE_ECUDA;
+  }
+  *out = r;
+  return MOE_OK;
+}
+
+extern "C" int moe_rope_destroy(moe_rope* r) {
+  if (!r) return MOE_OK;
+  cudaFree(r->turns);
+  free(r);
+  return MOE_OK;
+}
+
+extern "C" int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q,
+                             long long q_stride, uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k,
+                             long long k_stride, const uint16_t* v, long long v_stride, int32_t* err_dev,
+                             moe_stream_t stream) {
+  using namespace moe;
+  append::Args a = {};
+  const int rc = kv_view(kv, b, &a.kv);
+  if (rc) return rc;
+  const int T = b->T, D = kv->D;
+  if (Hq < 0 || Hq > 1024 * kMaxGroup || (Hq > 0) != (q != nullptr) || (rope && rope->rot > D)) return MOE_EINVAL;
+  if (T == 0 || b->B == 0) return MOE_OK;
+  if (q && (!rows_ok(q, q_stride, T, (long long)Hq * D) || !rows_ok(q_out, q_out_stride, T, (long long)Hq * D)))
+    return MOE_EINVAL;
+  if (!rows_ok(k, k_stride, T, (long long)kv->Hkv * D) || !rows_ok(v, v_stride, T, (long long)kv->Hkv * D))
+    return MOE_EINVAL;
+  a.turns = rope ? rope->turns : nullptr;
+  a.rot = rope ? rope->rot : 0;
+  a.interleaved = rope ? rope->interleaved : 0;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qo = q_out;
+  a.qs = q_stride;
+  a.qos = q_out_stride;
+  a.ks = k_stride;
+  a.vs = v_stride;
+  a.Hq = Hq;
+  a.err = err_dev;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((kv->e4m3 ? append::launch<true>(D, T, s, a) : append::launch<false>(D, T, s, a)) != cudaSuccess) return MOE_ECUDA;
+  return MOE_OK;
+}

@@ -29,7 +29,9 @@ EXPORTED = (
     "cache_plan_swaps", "moe_cache_apply_swaps", "moe_ws_set_profiling", "moe_ws_kernel_times",
     "cache_plan_swaps_noalloc", "moe_residual_rmsnorm", "moe_layer_forward_streamed", "moe_ws_set_tail_skip",
     "moe_ws_set_fused_heat", "cache_lru_plan", "moe_cache_apply_lru", "moe_ws_set_decode_path",
-    "moe_ws_set_wait_test", "moe_nvfp4_split", "moe_layers_forward_streamed",
+    "moe_ws_set_wait_test", "moe_nvfp4_split", "moe_layers_forward_streamed", "moe_rope_create", "moe_rope_destroy",
+    "moe_kv_append", "moe_attn_ws_create", "moe_attn_ws_destroy", "moe_attn_ws_get_view", "moe_attn_sync_status",
+    "moe_paged_attention", "moe_block_norm",
 )
 
 
@@ -69,6 +71,27 @@ class moe_policy_cfg(C.Structure):
     _fields_ = [("threshold", C.c_float), ("max_swaps", C.c_int), ("decay", C.c_float)]
 
 
+class moe_kv_pages(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("e4m3", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+                ("page", C.c_int), ("npages", C.c_int), ("page_stride", C.c_longlong), ("head_stride", C.c_longlong),
+                ("tok_stride", C.c_longlong), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
+class moe_kv_batch(C.Structure):
+    _fields_ = [("q_start", C.c_void_p), ("kv_len", C.c_void_p), ("page_table", C.c_void_p), ("B", C.c_int),
+                ("T", C.c_int), ("max_n", C.c_int), ("table_stride", C.c_int)]
+
+
+class moe_attn_ws_view(C.Structure):
+    _fields_ = [("error", C.c_void_p)]
+
+
+class moe_block_norm_desc(C.Structure):
+    _fields_ = [("y", C.c_void_p), ("y_stride", C.c_longlong), ("post_norm", C.c_int), ("w_post", C.c_void_p),
+                ("gate", C.c_void_p), ("gate_stride", C.c_longlong), ("gate_sigmoid", C.c_int),
+                ("res_scale", C.c_float), ("w_pre", C.c_void_p), ("eps", C.c_float)]
+
+
 SWAP_DTYPE = np.dtype([("layer", "<i4"), ("hot_expert", "<i4"), ("cold_expert", "<i4"), ("slot", "<i4"),
                        ("diff", "<f4")])
 
@@ -83,7 +106,7 @@ def load() -> C.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"libmoe.so not built ({LIB_PATH}); run python -m serving_router_top_gb300.build")
     lib = C.CDLL(LIB_PATH)
-    P, I, Z, F = C.c_void_p, C.c_int, C.c_size_t, C.c_float
+    P, I, Z, F, Q, D = C.c_void_p, C.c_int, C.c_size_t, C.c_float, C.c_longlong, C.c_double
     sig = {
         "moe_blob_bytes": (Z, [I, I]),
         "moe_pack_expert": (I, [P, P, P, I, I, F, F, F, P]),
@@ -117,6 +140,15 @@ def load() -> C.CDLL:
         "cache_lru_plan": (I, [P, P, I, I, P, P, P]),
         "moe_cache_apply_lru": (I, [P, P, P, P, P]),
         "moe_ws_kernel_times": (I, [P, I, P, P, C.POINTER(C.c_int)]),
+        "moe_rope_create": (I, [C.POINTER(P), I, I, D, P]),
+        "moe_rope_destroy": (I, [P]),
+        "moe_kv_append": (I, [P, P, P, P, Q, P, Q, I, P, Q, P, Q, P, P]),
+        "moe_attn_ws_create": (I, [C.POINTER(P), I, I, I]),
+        "moe_attn_ws_destroy": (I, [P]),
+        "moe_attn_ws_get_view": (I, [P, C.POINTER(moe_attn_ws_view)]),
+        "moe_attn_sync_status": (I, [P, P]),
+        "moe_paged_attention": (I, [P, P, P, Q, I, P, Q, F, I, P, P]),
+        "moe_block_norm": (I, [P, P, Q, P, Q, P, Q, I, I, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -415,3 +447,173 @@ def moe_cache_apply_lru(cache: Cache, plan_dev, n_dev, compute=None, copy=None) 
 def moe_cache_apply_swaps(cache: Cache, plan_dev, n_dev, compute=None, copy=None) -> None:
     _check(load().moe_cache_apply_swaps(cache.handle, _ptr(plan_dev), _ptr(n_dev), _stream(compute),
                                         _stream(copy)), "moe_cache_apply_swaps")
+
+
+# ------------------------------------------------- the attention half of a layer
+
+class KvPages:
+    """A layer's key and value page pools: torch tensors [npages, Hkv, page, D], bf16 (or their
+    bits as int16) or float8_e4m3fn with the scales of each head (fp32 [Hkv]); any strides with
+    contiguous columns, the same in both."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype or k.stride(3) != 1:
+            raise ValueError("KvPages: k and v are [npages, Hkv, page, D] of one shape, type and layout, columns contiguous")
+        if k.dtype not in (torch.bfloat16, torch.int16, torch.float8_e4m3fn):
+            raise ValueError(f"KvPages: bf16 or float8_e4m3fn pools, not {k.dtype}")
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or t.numel() != k.shape[1] or not t.is_contiguous()):
+                raise ValueError("KvPages: the scales are contiguous float32 [Hkv]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        npages, self.Hkv, page, self.D = k.shape
+        self.c = moe_kv_pages(k.data_ptr(), v.data_ptr(), 1 if k.dtype == torch.float8_e4m3fn else 0, self.Hkv, self.D,
+                              page, npages, k.stride(0), k.stride(1), k.stride(2), _ptr(k_scale), _ptr(v_scale))
+        self.ref = C.addressof(self.c)
+
+
+class KvBatch:
+    """The requests of one call: q_start int32 [B+1], kv_len int32 [B], page_table int32 [B, pages]
+    (device tensors, read when the kernels run), T token rows, about max_n new tokens a request."""
+
+    def __init__(self, q_start, kv_len, page_table, T: int, max_n: int):
+        import torch
+        B = kv_len.numel()
+        if (any(t.dtype != torch.int32 for t in (q_start, kv_len, page_table)) or q_start.numel() != B + 1
+                or page_table.dim() != 2 or page_table.shape[0] != B or not q_start.is_contiguous()
+                or not kv_len.is_contiguous() or (page_table.numel() and page_table.stride(1) != 1)):
+            raise ValueError("KvBatch: int32 q_start [B+1], kv_len [B] and page_table [B, pages], rows contiguous")
+        if B > 1 and page_table.stride(0) != page_table.shape[1]:
+            raise ValueError("KvBatch: the rows of page_table follow one another")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.c = moe_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B, T, max_n,
+                              page_table.shape[1])
+        self.ref = C.addressof(self.c)
+
+
+class Rope:
+    """Rotation frequencies: theta^(-2i/rot), or inv_freq (float64 [rot/2])."""
+
+    def __init__(self, rot: int, theta: float = 10000.0, inv_freq: Optional[np.ndarray] = None,
+                 interleaved: bool = False):
+        f = None
+        if inv_freq is not None:
+            f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+            if f.shape != (rot // 2,):
+                raise ValueError("Rope: inv_freq is [rot/2]")
+        h = C.c_void_p()
+        _check(load().moe_rope_create(C.byref(h), rot, 1 if interleaved else 0, float(theta),
+                                      None if f is None else f.ctypes.data), "moe_rope_create")
+        self.handle, self.rot = h, rot
+
+    def close(self):
+        if self.handle:
+            load().moe_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class AttnWorkspace:
+    def __init__(self, Hq: int, Hkv: int, D: int):
+        h = C.c_void_p()
+        _check(load().moe_attn_ws_create(C.byref(h), Hq, Hkv, D), "moe_attn_ws_create")
+        self.handle = h
+        self.Hq, self.Hkv, self.D = Hq, Hkv, D
+        v = moe_attn_ws_view()
+        _check(load().moe_attn_ws_get_view(h, C.byref(v)), "moe_attn_ws_get_view")
+        self.view = v
+
+    def close(self):
+        if self.handle:
+            load().moe_attn_ws_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def error_ptr(self) -> int:
+        return self.view.error
+
+
+def _heads(t, T: int, H: int, D: int, what: str):
+    """Address and token stride of [T, H, D] bf16 rows whose heads follow one another."""
+    if t.dim() != 3 or tuple(t.shape) != (T, H, D) or t.element_size() != 2 or t.stride(2) != 1 or (
+            H > 1 and t.stride(1) != D):
+        raise ValueError(f"{what}: bf16 [{T}, {H}, {D}] with heads {D} apart, got {tuple(t.shape)} {t.dtype} "
+                         f"strides {t.stride()}")
+    return t.data_ptr(), t.stride(0)
+
+
+def moe_kv_append(pages: KvPages, batch: KvBatch, rope: Optional[Rope], q, q_out, k, v, err=None, stream=None) -> None:
+    """Rotate q into q_out and the keys by position; write keys and values into their pages."""
+    T, Hkv, D = batch.c.T, pages.Hkv, pages.D
+    Hq = 0 if q is None else q.shape[1]
+    qp, qs = (None, 0) if q is None else _heads(q, T, Hq, D, "q")
+    op, os_ = (None, 0) if q is None else _heads(q_out, T, Hq, D, "q_out")
+    kp, ks = _heads(k, T, Hkv, D, "k")
+    vp, vs = _heads(v, T, Hkv, D, "v")
+    _check(load().moe_kv_append(pages.ref, batch.ref, None if rope is None else rope.handle, qp, qs, op, os_, Hq, kp, ks,
+                                vp, vs, _ptr(err), _stream(stream)), "moe_kv_append")
+
+
+def moe_paged_attention(pages: KvPages, batch: KvBatch, q, o, ws: AttnWorkspace, scale: float, window: int = 0,
+                        stream=None) -> None:
+    """o (bf16 [T, Hq, D]) = attention of every new token over its request's pages."""
+    T, D = batch.c.T, pages.D
+    qp, qs = _heads(q, T, ws.Hq, D, "q")
+    op, os_ = _heads(o, T, ws.Hq, D, "o")
+    _check(load().moe_paged_attention(pages.ref, batch.ref, qp, qs, ws.Hq, op, os_, scale, window, ws.handle,
+                                      _stream(stream)), "moe_paged_attention")
+
+
+def moe_attn_sync_status(ws: AttnWorkspace, stream=None) -> int:
+    return int(load().moe_attn_sync_status(ws.handle, _stream(stream)))
+
+
+class BlockNormDesc:
+    """Owner of a moe_block_norm_desc and references to its tensors (bf16 or their bits)."""
+
+    def __init__(self, **kw):
+        self.tensors = kw
+        y, gate = kw["y"], kw["gate"]
+        self.T = None if y is None else y.shape[0]
+        widths = {t.shape[-1] for t in (y, gate, kw["w_post"], kw["w_pre"]) if t is not None}
+        if len(widths) > 1 or (gate is not None and gate.shape[0] not in (1, self.T)):
+            raise ValueError("block_norm_desc: y, gate and the weights differ in size")
+        self.H = widths.pop() if widths else None
+        for t in (y, gate):
+            if t is not None and (t.dim() != 2 or t.element_size() != 2 or t.stride(1) != 1):
+                raise ValueError("block_norm_desc: y is bf16 [T, H], gate bf16 [T, H] or [1, H], columns contiguous")
+        for t in (kw["w_post"], kw["w_pre"]):
+            if t is not None and (t.dim() != 1 or t.element_size() != 2 or not t.is_contiguous()):
+                raise ValueError("block_norm_desc: the weights are contiguous bf16 [H]")
+        self.c = moe_block_norm_desc(
+            _ptr(y), 0 if y is None else y.stride(0), 1 if kw["post_norm"] else 0, _ptr(kw["w_post"]), _ptr(gate),
+            0 if gate is None or gate.shape[0] == 1 else gate.stride(0), 1 if kw["gate_sigmoid"] else 0,
+            kw["res_scale"], _ptr(kw["w_pre"]), kw["eps"])
+        self.ref = C.addressof(self.c)
+
+
+def block_norm_desc(y=None, post_norm: bool = False, w_post=None, gate=None, gate_sigmoid: bool = False,
+                    res_scale: float = 1.0, w_pre=None, eps: float = 1e-6) -> BlockNormDesc:
+    return BlockNormDesc(y=y, post_norm=post_norm, w_post=w_post, gate=gate, gate_sigmoid=gate_sigmoid,
+                         res_scale=res_scale, w_pre=w_pre, eps=eps)
+
+
+def moe_block_norm(desc: BlockNormDesc, x, x_out, xn, T: int, H: int, stream=None) -> None:
+    """x_out (fp32) = x + res_scale * gate * post-norm(y); xn (bf16) = pre-norm of the next block of x_out."""
+    if x.dtype.itemsize != 4 or tuple(x.shape) != (T, H) or desc.H not in (None, H) or desc.T not in (None, T) or any(
+            t is not None and (tuple(t.shape) != (T, H) or t.element_size() != size)
+            for t, size in ((x_out, 4), (xn, 2))):
+        raise ValueError(f"moe_block_norm: x, x_out fp32 and xn bf16 are [{T}, {H}], as are y, gate and the weights")
+    _check(load().moe_block_norm(desc.ref, _ptr(x), x.stride(0), _ptr(x_out), 0 if x_out is None else x_out.stride(0),
+                                 _ptr(xn), 0 if xn is None else xn.stride(0), T, H, _stream(stream)), "moe_block_norm")
