@@ -595,7 +595,7 @@ typedef struct {
   const uint16_t* y;       /* bf16 [T][H] the block's output, or NULL: x_out = x       */
   long long y_stride;      /* elements between tokens                                  */
   int post_norm;           /* normalise y first                                        */
-  const uint16_t* w_post;  /* bf16 [H] or NULL: ones                                   */
+  const uint16_t* w_post;  /* bf16 [H] or NULL: ones; read only with post_norm         */
   const uint16_t* gate;    /* bf16 [T][H], or NULL: none                               */
   long long gate_stride;   /* elements between tokens; 0: one row for every token      */
   int gate_sigmoid;        /* the gate is sigmoid(gate)                                */

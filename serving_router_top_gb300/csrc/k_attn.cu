@@ -1,127 +1,22 @@
-// Attention of the newest tokens of each request over a paged cache.
-//
-// For a token at position p, query head h and its key head:
-//   s_j = scale * q . k_j,  j <= p (and j > p - window);  o = sum exp(s_j) v_j / sum exp(s_j)
-// in one pass over the keys with the running maximum and sum of the softmax.
-// One CTA per (token, query head): its warps take the keys in turn and their
-// parts are joined at the end.
-#include "paged.cuh"
+// moe_paged_attention: checks, workspace and launch (the kernels are in attn.cuh).
+#include "attn.cuh"
 
 struct moe_attn_ws {
-  int Hq, Hkv, D;
+  int Hq, Hkv, D, ctas;
   int32_t* error;
+  float *part, *ml;
+  int4* head;
+  long long* cut;
 };
 
 namespace moe {
 namespace attn {
-
-constexpr int kWarps = 8;
-
-struct Args {
-  KvView kv;
-  const uint16_t* q;
-  uint16_t* o;
-  long long qs, os;
-  int Hq, G, window;
-  float scale;
-  int32_t* err;
-};
-
-// Lane's D/32 neighbouring elements of a cache row.
-template <bool E4M3, int N>
-__device__ __forceinline__ void load_row(const uint8_t* p, int lane, float f[N]) {
-  if (E4M3) {
-    const uint8_t* e = p + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 v = f16x2_to_f32x2(e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(e + i)));
-      f[i] = v.x;
-      f[i + 1] = v.y;
-    }
-  } else {
-    const uint16_t* e = reinterpret_cast<const uint16_t*>(p) + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = bf16_bits_to_f32(e[i]);
-  }
-}
-
-template <bool E4M3, int D>
-__global__ void __launch_bounds__(32 * kWarps) k_attn(const __grid_constant__ Args a) {
-  constexpr int N = D / 32;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int t = blockIdx.x, head = blockIdx.y, h = head / a.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = request_of(a.kv, t);
-  if (b < 0) return;
-  const long long pos = position_of(a.kv, b, t), cap = (long long)a.kv.table_stride << a.kv.page_shift;
-  if (threadIdx.x == 0 && a.kv.kv_len[b] > cap) set_error(a.err, MOE_ERANGE);
-  const long long end = pos + 1 < cap ? pos + 1 : cap;
-  const long long first = a.window > 0 && pos + 1 > a.window ? pos + 1 - a.window : 0;
-  float q[N], o[N];
-  const float qk = a.scale * (a.kv.k_scale ? a.kv.k_scale[h] : 1.f);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = qk * bf16_bits_to_f32(a.q[(long long)t * a.qs + head * D + lane * N + i]);
-    o[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (long long j = first + warp; j < end; j += kWarps) {
-    const int id = a.kv.page_table[(long long)b * a.kv.table_stride + (j >> a.kv.page_shift)];
-    float k[N], v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) k[i] = v[i] = 0.f;
-    if (id >= 0 && id < a.kv.npages) {
-      const long long at = id * a.kv.page_stride + h * a.kv.head_stride +
-                           (j & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
-      load_row<E4M3, N>(a.kv.k + at, lane, k);
-      load_row<E4M3, N>(a.kv.v + at, lane, v);
-    } else if (lane == 0) {
-      set_error(a.err, MOE_ERANGE);
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s);
-    const float c = mn == -INFINITY ? 1.f : __expf(m - mn), w = mn == -INFINITY ? 0.f : __expf(s - mn);
-    m = mn;
-    l = l * c + w;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * c + w * v[i];
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) s_o[warp][lane * N + i] = o[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float mx = -INFINITY, lt = 0.f, ot = 0.f;
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float c = s_m[w] == -INFINITY ? 0.f : __expf(s_m[w] - mx);
-      lt += c * s_l[w];
-      ot += c * s_o[w][threadIdx.x];
-    }
-    const float vs = a.kv.v_scale ? a.kv.v_scale[h] : 1.f;
-    const float r = end > first ? ot / lt * vs : 0.f;
-    a.o[(long long)t * a.os + head * D + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
-  }
-}
-
-template <bool E4M3>
-cudaError_t launch(int D, dim3 grid, cudaStream_t s, const Args& a) {
-  const dim3 block(32 * kWarps);
-  switch (D) {
-    case 64: k_attn<E4M3, 64><<<grid, block, 0, s>>>(a); break;
-    case 128: k_attn<E4M3, 128><<<grid, block, 0, s>>>(a); break;
-    default: k_attn<E4M3, 256><<<grid, block, 0, s>>>(a);
-  }
-  return cudaGetLastError();
-}
-
+int launch_d64(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
+int launch_d128(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
+int launch_d256(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
+int opt_in_d64();
+int opt_in_d128();
+int opt_in_d256();
 }  // namespace attn
 }  // namespace moe
 
@@ -135,12 +30,30 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
   w->Hq = Hq;
   w->Hkv = Hkv;
   w->D = D;
-  if (cudaMalloc(&w->error, 256) != cudaSuccess) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1 ||
+      (D == 64 ? attn::opt_in_d64() : D == 128 ? attn::opt_in_d128() : attn::opt_in_d256()) != MOE_OK) {
+    cudaGetLastError();
+    free(w);
+    return MOE_ECUDA;
+  }
+  w->ctas = sms < attn::kMaxRuns ? sms : attn::kMaxRuns;  // one CTA per SM
+  const size_t rows = 2 * size_t(w->ctas) * (D == 256 ? 64 : 128);
+  const size_t o_part = 256, o_ml = o_part + rows * D * 4, o_head = o_ml + rows * 8, o_cut = o_head + size_t(w->ctas) * 16;
+  const size_t bytes = o_cut + (2 * size_t(w->ctas) + 1) * 8;
+  uint8_t* base = nullptr;
+  if (cudaMalloc(&base, bytes) != cudaSuccess) {
     cudaGetLastError();
     free(w);
     return MOE_ENOMEM;
   }
-  if (cudaMemset(w->error, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  w->error = reinterpret_cast<int32_t*>(base);
+  w->part = reinterpret_cast<float*>(base + o_part);
+  w->ml = reinterpret_cast<float*>(base + o_ml);
+  w->head = reinterpret_cast<int4*>(base + o_head);
+  w->cut = reinterpret_cast<long long*>(base + o_cut);
+  if (cudaMemset(base, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     moe_attn_ws_destroy(w);
     return MOE_ECUDA;
@@ -151,7 +64,7 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
 
 extern "C" int moe_attn_ws_destroy(moe_attn_ws* w) {
   if (!w) return MOE_OK;
-  cudaFree(w->error);
+  cudaFree(w->error);  // the start of the single allocation
   free(w);
   return MOE_OK;
 }
@@ -187,14 +100,20 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.o = o;
   a.qs = q_stride;
   a.os = o_stride;
-  a.Hq = Hq;
   a.G = Hq / kv->Hkv;
   a.window = window;
   a.scale = scale;
   a.err = ws->error;
+  a.part = ws->part;
+  a.ml = ws->ml;
+  a.head = ws->head;
+  a.cut = ws->cut;
+  a.total = ws->cut + 2 * ws->ctas;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(T, Hq);
-  if ((kv->e4m3 ? attn::launch<true>(kv->D, grid, s, a) : attn::launch<false>(kv->D, grid, s, a)) != cudaSuccess)
-    return MOE_ECUDA;
-  return MOE_OK;
+  const int nr = attn::row_tile(kv->D, (long long)a.G * (b->max_n > 1 ? b->max_n : 1));
+  switch (kv->D) {
+    case 64: return attn::launch_d64(a, kv->e4m3, nr, ws->ctas, s);
+    case 128: return attn::launch_d128(a, kv->e4m3, nr, ws->ctas, s);
+    default: return attn::launch_d256(a, kv->e4m3, nr, ws->ctas, s);
+  }
 }

@@ -150,8 +150,7 @@ extern "C" int moe_block_norm(const moe_block_norm_desc* d, const float* x, long
                               moe_stream_t stream) {
   using namespace moe;
   if (!d || !x || T < 0 || H < 1 || H > bnorm::kMaxH || !(d->eps > 0.f)) return MOE_EINVAL;
-  if (!d->y && (d->post_norm || d->w_post || d->gate)) return MOE_EINVAL;
-  if (d->w_post && !d->post_norm) return MOE_EINVAL;
+  if (!d->y && (d->post_norm || d->gate)) return MOE_EINVAL;
   auto ok = [&](const void* p, long long stride, int size, bool may_be_0) {
     return !p || (!(reinterpret_cast<uintptr_t>(p) % size) && (T <= 1 || stride >= H || (may_be_0 && stride == 0)));
   };

@@ -106,7 +106,7 @@ def norm(lib, x=P16, xs=64, xo=P16, xos=64, xn=P16, xns=64, T=2, H=64, **kw):
 
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(T=-1), dict(H=0), dict(H=16385), dict(eps=0.0), dict(eps=-1.0),
-                                dict(eps=float("nan")), dict(y=None), dict(post_norm=0), dict(x=P16 + 2),
+                                dict(eps=float("nan")), dict(y=None), dict(x=P16 + 2),
                                 dict(xo=P16 + 1), dict(xn=P16 + 1), dict(y=P16 + 1), dict(gate=P16 + 1),
                                 dict(w_post=P16 + 1), dict(w_pre=P16 + 1), dict(xs=63), dict(xos=0), dict(xns=32),
                                 dict(y_stride=0), dict(gate_stride=63), dict(gate_stride=-64)])
