@@ -505,14 +505,15 @@ int moe_cache_apply_lru(moe_cache* c, const moe_swap* plan_dev, const int32_t* n
 /* The page pools of one layer's keys and values (device memory of the caller).
  * Element (page, head, place, column) is at page * page_stride + head *
  * head_stride + place * tok_stride + column, in both pools.  The strides are
- * in elements, positive, at least D and multiples of 16 bytes; the pools are
+ * in elements, below 2^38, at least D and multiples of 16 bytes; the pools are
  * 16-byte aligned. */
 typedef struct {
   void* k;
   void* v;
   int e4m3;              /* 0: bf16 elements; 1: FP8-E4M3 elements                     */
   int Hkv, D;            /* key heads 1..1024; columns 64, 128 or 256                  */
-  int page, npages;      /* tokens in a page (a power of two, 1..65536), pages in a pool */
+  int page, npages;      /* tokens in a page (a power of two, 1..65536; at least 2 for E4M3
+                            with 64 columns), pages in a pool                          */
   long long page_stride, head_stride, tok_stride;
   const float* k_scale;  /* fp32 [Hkv] device: a stored code c stands for c * scale;   */
   const float* v_scale;  /*   NULL: 1.  Read only for E4M3 pools                       */

@@ -23,6 +23,11 @@
 // 2^-8 relative to each weight however small (f16 would keep three bits more
 // of the large weights and lose those 2^-32 below the largest).
 //
+// Movement.  One warp asks the copy engine for the tiles (a page, or 128 keys of
+// a larger one, by 64 columns a box, swizzled for the tensor core); pages that
+// are not there are asked for past the pool's end and read as zeros.  E4M3
+// tiles land as they are and are turned into bf16 by four warps of their own.
+//
 // Split.  Every (request, key head, row tile) is a unit of tiles; all tiles of
 // a call are laid end to end and cut into equal runs, one per SM, whatever the
 // lengths.  A run takes its units in pieces; a piece that is not its whole unit
@@ -30,6 +35,7 @@
 // unit in their order.
 #pragma once
 
+#include <cuda.h>
 #include <limits.h>
 
 #include "paged.cuh"
@@ -42,21 +48,21 @@ constexpr float kUnset = -1e30f;              // m of a row that has seen no key
 constexpr float kGrow = 8.0f;                 // m is set again when a score passes it by this (log2)
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr int kSmem = 232448;
-constexpr int kMisc = 6144;                   // barriers, row statistics, schedule
+constexpr int kMisc = 5120;                   // barriers, row statistics, schedule
 
 struct Args {
+  CUtensorMap mk, mv, mq;  // pools [page][head][place][column], query rows [token][head][column]
   KvView kv;
-  const uint16_t* q;
   uint16_t* o;
-  long long qs, os;
-  int G, window;
+  long long os;
+  int G, window, tokens;   // query heads a key head; visible keys (0: all); tokens in a row tile
   float scale;
   int32_t* err;
   float* part;  // [2 * CTAs][NR][D] pieces: head piece of CTA c at 2c, tail piece at 2c + 1
   float* ml;    // [2 * CTAs][NR][2] their m and sums
   int4* head;   // [CTAs] head piece: request, key head, row tile; w = 1 when it starts inside its unit
-  long long* cut;  // [CTAs][2] that unit's tiles, first and last + 1, in the call's order of tiles
-  long long* total;  // [1] tiles of the call
+  int2* cut;    // [CTAs] that unit's tiles, first and last + 1, in the call's order of tiles
+  int* total;   // [1] tiles of the call
 };
 
 template <int D, int NR, bool E4M3>
@@ -64,18 +70,23 @@ struct Cfg {
   static constexpr int DS = D < 128 ? D : 128;       // columns in a slot
   static constexpr int H = D / DS;                   // slots of a key or value tile
   static constexpr int SLOT = kKeys * DS * 2;
+  static constexpr int RAW = E4M3 ? kKeys * DS : 0;  // a slot's codes
   static constexpr int QBYTES = NR * D * 2;
   static constexpr int PBYTES = kKeys * NR * 2;
   static constexpr int FREE = kSmem - kMisc - 2 * PBYTES;
-  static constexpr int QB = (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
-  static constexpr int NS = (FREE - QB * QBYTES) / SLOT;
-  static constexpr int CW = NR < 32 ? NR : 32;       // rows a softmax warp holds
-  static constexpr int SW = 4 * (NR / CW);           // softmax warps
-  static constexpr int PW = NR > 64 ? 4 : 8;         // producer warps
-  static constexpr int THREADS = 32 * (SW + 1 + PW);
+  // E4M3: three tiles' worth of bf16, all other room for codes on their way
+  static constexpr int NSV = D < 128 ? 6 : 3;
+  static constexpr int QB = E4M3 ? ((FREE - NSV * SLOT - 2 * QBYTES) / (RAW + 1) >= 4 ? 2 : 1)
+                                 : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
+  static constexpr int NS0 = E4M3 ? NSV : (FREE - QB * QBYTES) / SLOT, NS = NS0 > 16 ? 16 : NS0;
+  static constexpr int NRAW0 = E4M3 ? (FREE - QB * QBYTES - NS * SLOT) / (RAW + 1) : 0, NRAW = NRAW0 > 16 ? 16 : NRAW0;
+  static constexpr int CW = NR < 32 ? NR : NR < 128 ? 32 : 64;  // rows a softmax warp holds
+  static constexpr int SW = 4 * (NR / CW);                      // softmax warps
+  static constexpr int VW = E4M3 ? 4 : 0;                       // converting warps
+  static constexpr int THREADS = 32 * (SW + 2 + VW);
   static constexpr int COLS0 = (2 + H) * NR;
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
-  static_assert(COLS0 <= 512 && NS >= 3 && NS <= 16, "resources of an SM");
+  static_assert(COLS0 <= 512 && NS >= 3 && (!E4M3 || NRAW >= 3), "resources of an SM");
 };
 
 // ------------------------------------------------------------------ schedule
@@ -92,63 +103,65 @@ __device__ __forceinline__ Req load_req(const KvView& kv, int b) {
   r.pos0 = r.kv - r.n;
   return r;
 }
-struct Span {  // the keys that a row tile's rows see between them: [lo, hi), in nt tiles from tile0
+struct Span {  // the keys that a row tile's tokens i0 .. i1 see between them: [lo, hi), in nt tiles from tile0
   int i0, i1, lo, hi, tile0, nt;
 };
-template <int NR>
-__device__ __forceinline__ Span span_of(const Req& r, int rt, int G, int window, int cap) {
+__device__ __forceinline__ Span span_of(const Req& r, int rt, int tokens, int window, int cap) {
   Span s;
-  s.i0 = rt * NR / G;
-  s.i1 = (min((rt + 1) * NR, r.n * G) - 1) / G;
+  s.i0 = rt * tokens;
+  s.i1 = min(s.i0 + tokens, r.n) - 1;
   s.hi = min(max(r.pos0 + s.i1 + 1, 0), cap);
   s.lo = window > 0 ? min(max(r.pos0 + s.i0 - window + 1, 0), s.hi) : 0;
   s.tile0 = s.lo / kKeys;
-  s.nt = max(s.hi / kKeys + (s.hi % kKeys != 0) - s.tile0, 1);  // a tile even where nothing is seen: its rows get zeros
+  s.nt = max((s.hi + kKeys - 1) / kKeys - s.tile0, 1);  // a tile even where nothing is seen: its rows get zeros
   return s;
 }
 __device__ __forceinline__ int cap_of(const KvView& kv) {
   return int(min((long long)kv.table_stride << kv.page_shift, (long long)INT_MAX - kKeys));
 }
-template <int NR>
-__device__ __forceinline__ long long head_tiles(const Req& r, int G, int window, int cap) {
+__device__ __forceinline__ long long head_tiles(const Req& r, int tokens, int window, int cap) {
   long long w = 0;
-  for (int rt = 0; rt * NR < r.n * G; ++rt) w += span_of<NR>(r, rt, G, window, cap).nt;
+  for (int rt = 0; rt * tokens < r.n; ++rt) w += span_of(r, rt, tokens, window, cap).nt;
   return w;
+}
+// First tile of run c: `total` tiles in `runs` runs whose lengths differ by one at most.
+__device__ __forceinline__ int cut_at(int total, int runs, int c) {
+  const int q = total / runs;
+  return q * c + min(c, total - q * runs);
 }
 
 // A walk over the tiles of a run: the same in every role.
-template <int NR>
 struct Walk {
   Req r;
   Span s;
   int b, h, rt, j, jbeg, jend;
-  long long left;  // tiles after this one
-  __device__ __forceinline__ void unit(const Args& a, int cap, int from, long long count) {
-    s = span_of<NR>(r, rt, a.G, a.window, cap);
+  int left;  // tiles after this one
+  __device__ __forceinline__ void unit(const Args& a, int cap, int from, int count) {
+    s = span_of(r, rt, a.tokens, a.window, cap);
     jbeg = j = from;
-    jend = int(min((long long)s.nt, from + count));
+    jend = min(s.nt, from + count);
     left = count - 1;
   }
   // The run's first tile: tile `off` of request b.
-  __device__ __forceinline__ void start(const Args& a, int cap, int b_, long long off, long long count) {
+  __device__ __forceinline__ void start(const Args& a, int cap, int b_, int off, int count) {
     b = b_;
     r = load_req(a.kv, b);
-    const long long per = head_tiles<NR>(r, a.G, a.window, cap);
-    h = int(off / per);
+    const int per = int(head_tiles(r, a.tokens, a.window, cap));
+    h = off / per;
     off -= h * per;
     for (rt = 0;; ++rt) {
-      const int nt = span_of<NR>(r, rt, a.G, a.window, cap).nt;
+      const int nt = span_of(r, rt, a.tokens, a.window, cap).nt;
       if (off < nt) break;
       off -= nt;
     }
-    unit(a, cap, int(off), count);
+    unit(a, cap, off, count);
   }
   __device__ __forceinline__ void next(const Args& a, int cap) {  // left > 0
     if (++j < jend) {
       --left;
       return;
     }
-    if ((rt + 1) * NR < r.n * a.G) {
+    if ((rt + 1) * a.tokens < r.n) {
       ++rt;
     } else {
       rt = 0;
@@ -173,6 +186,9 @@ __device__ __forceinline__ void bar_init(uint64_t* b, int n) {
 __device__ __forceinline__ void arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
 }
+__device__ __forceinline__ void expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ unsigned long long now_ns() {
   unsigned long long t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -182,6 +198,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // the CTA gave up: every role then runs through its loop without waiting, and the call reports it.
 __device__ __forceinline__ void wait(uint64_t* b, uint32_t par, volatile int* fail) {
   unsigned long long t0 = 0;
+#pragma unroll 1
   for (uint32_t i = 0;; ++i) {
     uint32_t ok;
     asm volatile(
@@ -190,26 +207,55 @@ __device__ __forceinline__ void wait(uint64_t* b, uint32_t par, volatile int* fa
         : "r"(su32(b)), "r"(par)
         : "memory");
     if (ok) return;
+    if ((i & 15) != 15) continue;
     if (*fail) return;
-    if (i == 0) t0 = now_ns();
-    else if ((i & 63) == 0 && now_ns() - t0 > kWaitNs) *fail = 1;
+    if (i == 15) t0 = now_ns();
+    else if (now_ns() - t0 > kWaitNs) *fail = 1;
   }
 }
-__device__ __forceinline__ void commit_to(uint64_t* b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b))
-               : "memory");
-}
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// A box of 64 columns (or a slot's codes) of a page from its place `tok` on -> dst, counted on b.
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* tm, int col, int tok, int head, int page,
+                                         uint64_t* b) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(su32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(col), "r"(tok), "r"(head), "r"(page), "r"(su32(b))
+      : "memory");
+}
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* tm, int col, int head, int token, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(su32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(col), "r"(head), "r"(token), "r"(su32(b))
+      : "memory");
+}
+// The tensor core's instructions are issued by one lane of a converged warp.
+__device__ __forceinline__ void commit_to(uint64_t* b) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(su32(b))
+      : "memory");
+}
+// Four steps of 16 along the contracted dimension; the descriptors advance by A and B (16-byte units).
+template <int A, int B>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "add.u64 a1, %1, %5;\n\tadd.u64 b1, %2, %6;\n\t"
+      "add.u64 a2, %1, %7;\n\tadd.u64 b2, %2, %8;\n\t"
+      "add.u64 a3, %1, %9;\n\tadd.u64 b3, %2, %10;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A), "n"(B), "n"(2 * A), "n"(2 * B), "n"(3 * A), "n"(3 * B)
       : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void ld16(uint32_t t, float v[16]) {
+__device__ __forceinline__ void ld16(uint32_t t, float* v) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -220,7 +266,7 @@ __device__ __forceinline__ void ld16(uint32_t t, float v[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void st16(uint32_t t, const float v[16]) {
+__device__ __forceinline__ void st16(uint32_t t, const float* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
       "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
@@ -258,6 +304,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// Two E4M3 codes (low byte first) -> bf16x2, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
+  const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(two));
+  return pack2(f.x, f.y);
+}
 
 // Shared-memory descriptors (start, leading and stride offsets in 16-byte units, version 1).
 __device__ __forceinline__ uint64_t desc(uint32_t start, uint32_t lbo, uint32_t sbo, uint64_t swizzle) {
@@ -266,71 +317,32 @@ __device__ __forceinline__ uint64_t desc(uint32_t start, uint32_t lbo, uint32_t 
 }
 
 struct Misc {
-  uint64_t full[16], empty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree, drain;
+  uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree, drain;
   uint32_t taddr;
   int fail;
-  int b;          // the run's first request
-  long long off;  // its first tile in it
+  int b, off;  // the run's first request, its first tile in it
   long long scan[32];
   float m[128], alpha[128];
   float red[4][128];
+  int page[2][kKeys];  // pages of a tile's boxes
   int nbad;
-  uint8_t bad[128];  // keys of a tile with values that are not finite
+  uint8_t bad[kKeys];  // keys of a tile with values that are not finite
 };
 static_assert(sizeof(Misc) <= kMisc, "misc");
 
-// ------------------------------------------------------------------ roles
-
-// Byte offset of each of a thread's keys in a pool (-1: nothing there, read as zeros).
-template <int RPT>
-struct Rows {
-  long long off[RPT];
+// A place in a ring of N slots.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t phase;
+  __device__ __forceinline__ explicit Ring(uint32_t ph) : phase(ph) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
 };
-template <int RPT, int STEP, int NR>
-__device__ __forceinline__ void find_rows(const Args& a, const Walk<NR>& w, int r0, int lane_col, Rows<RPT>& out,
-                                          bool report) {
-  const KvView& kv = a.kv;
-  const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
-  int id[RPT];
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int key = (w.s.tile0 + w.j) * kKeys + r0 + i * STEP;
-    id[i] = key >= w.s.lo && key < w.s.hi ? row[key >> kv.page_shift] : -2;
-  }
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int key = (w.s.tile0 + w.j) * kKeys + r0 + i * STEP;
-    if (id[i] >= 0 && id[i] < kv.npages) {
-      out.off[i] = id[i] * kv.page_stride + w.h * kv.head_stride +
-                   (long long)(key & ((1 << kv.page_shift) - 1)) * kv.tok_stride;
-    } else {
-      out.off[i] = -1;
-      if (report && id[i] != -2) set_error(a.err, MOE_ERANGE);
-    }
-  }
-}
-
-// Two E4M3 codes (low byte first) -> bf16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(two));
-  return pack2(f.x, f.y);
-}
-
-// The query rows of a piece, K-major with the 128-byte swizzle, one 64-column chunk after another.
-template <int D, int NR, int THREADS>
-__device__ __forceinline__ void load_q(const Args& a, const Walk<NR>& w, uint8_t* dst, int tid) {
-  constexpr int CH = D / 8;  // 16-byte pieces of a row
-  const int rows = w.r.n * a.G - w.rt * NR;
-  for (int p = tid; p < NR * CH; p += THREADS) {
-    const int row = p / CH, c = p % CH;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int rr = w.rt * NR + row, i = rr / a.G, g = rr - i * a.G;
-      u = *reinterpret_cast<const uint4*>(a.q + (w.r.s0 + i) * a.qs + (long long)(w.h * a.G + g) * D + c * 8);
-    }
-    *reinterpret_cast<uint4*>(dst + (c / 8) * (NR * 128) + sw128(row, c % 8)) = u;
-  }
-}
 
 // Sum of each of W values over the warp's lanes: lane i of every group of W gets value i's.
 template <int W>
@@ -357,19 +369,28 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   uint8_t* ring = smem;
   uint8_t* sq = ring + C::NS * C::SLOT;
   uint8_t* sp = sq + C::QB * C::QBYTES;
-  Misc& ms = *reinterpret_cast<Misc*>(sp + 2 * C::PBYTES);
+  uint8_t* raw = sp + 2 * C::PBYTES;
+  Misc& ms = *reinterpret_cast<Misc*>(raw + C::NRAW * C::RAW);
   volatile int* fail = &ms.fail;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kMmaWarp = C::SW, kProd0 = 32 * (C::SW + 1), kProd = 32 * C::PW, kSoft = 32 * C::SW;
+  constexpr int kMmaWarp = C::SW, kLoadWarp = C::SW + 1, kSoft = 32 * C::SW;
 
   pdl_trigger();
-  if (tid == 0) {
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ms.taddr)),
+                 "n"(C::COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else if (tid == 32 * kLoadWarp) {
     for (int i = 0; i < C::NS; ++i) {
-      bar_init(&ms.full[i], C::PW);
+      bar_init(&ms.full[i], E4M3 ? C::VW : 1);
       bar_init(&ms.empty[i], 1);
     }
+    for (int i = 0; i < C::NRAW; ++i) {
+      bar_init(&ms.rfull[i], 1);
+      bar_init(&ms.rempty[i], C::VW);
+    }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&ms.qfull[i], C::PW);
+      bar_init(&ms.qfull[i], 1);
       bar_init(&ms.qfree[i], 1);
       bar_init(&ms.sfull[i], 1);
       bar_init(&ms.pfull[i], C::SW);
@@ -380,11 +401,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ms.fail = 0;
     ms.nbad = 0;
-  }
-  if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ms.taddr)),
-                 "n"(C::COLS));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   pdl_wait();
 
@@ -397,7 +413,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
     if (b < B) {
       const Req r = load_req(a.kv, b);
       if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
-      mine += a.kv.Hkv * head_tiles<NR>(r, a.G, a.window, cap);
+      mine += a.kv.Hkv * head_tiles(r, a.tokens, a.window, cap);
     }
   }
   long long incl = mine;
@@ -411,321 +427,283 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   __syncthreads();
   tc_after();
   const uint32_t taddr = ms.taddr;
-  long long total = 0, before = incl - mine;
+  long long all = 0, before = incl - mine;
+#pragma unroll 4
   for (int w = 0; w < C::THREADS / 32; ++w) {
-    if (w < warp) before += ms.scan[w];
-    total += ms.scan[w];
+    const long long v = ms.scan[w];
+    if (w < warp) before += v;
+    all += v;
   }
-  const int runs = int(min((long long)gridDim.x, total)), run = blockIdx.x;  // no run is empty
-  const long long w0 = run < runs ? total * run / runs : 0, w1 = run < runs ? total * (run + 1) / runs : 0;
-  const long long count = w1 - w0;
+  const int run = blockIdx.x;
+  const int total = all < INT_MAX ? int(all) : 0;  // more tiles than that are refused
+  const int runs = min(int(gridDim.x), total);     // no run is empty
+  const int w0 = run < runs ? cut_at(total, runs, run) : 0;
+  const int count = run < runs ? cut_at(total, runs, run + 1) - w0 : 0;
   if (tid == 0) {
     a.head[run].w = 0;
     if (run == 0) *a.total = total;
+    if (run == 0 && all >= INT_MAX) set_error(a.err, MOE_ERANGE);
   }
   if (count > 0 && w0 >= before && w0 < before + mine) {
-    long long off = w0 - before;
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      const long long n = a.kv.Hkv * head_tiles<NR>(load_req(a.kv, b), a.G, a.window, cap);
-      if (off < n) {
-        ms.b = b;
-        ms.off = off;
-        break;
-      }
+    int off = w0 - int(before), b = tid * per;
+    while (per > 1) {
+      const int n = int(a.kv.Hkv * head_tiles(load_req(a.kv, b), a.tokens, a.window, cap));
+      if (off < n) break;
       off -= n;
+      ++b;
     }
+    ms.b = b;
+    ms.off = off;
   }
   __syncthreads();
 
   if (count > 0) {
-    Walk<NR> w;
+    Walk w;
     w.start(a, cap, ms.b, ms.off, count);
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- tensor cores
-      if (lane == 0) {
-        // D f32, A and B bf16, N = NR, M = 128; the second product's operands are both MN-major
-        constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(NR >> 3) << 17) | (8u << 24);
-        constexpr uint32_t kIdescS = kBase, kIdescO = kBase | (1u << 15) | (1u << 16);
-        int slot = 0, qn = -1;  // ring position, pieces begun
-        uint32_t sph = 0;       // its phase
-        auto take = [&]() {
-          wait(&ms.full[slot], sph, fail);
-          tc_after();
-        };
-        auto pass = [&]() {
-          if (++slot == C::NS) {
-            slot = 0;
-            sph ^= 1;
+      // D f32, A and B bf16, N = NR, M = 128; the second product's operands are both MN-major
+      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(NR >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdescS = kBase, kIdescO = kBase | (1u << 15) | (1u << 16);
+      Ring<C::NS> rg(0);
+      int qn = -1;             // pieces begun, less one
+      int pieces = 0;          // pieces whose O has been begun
+      bool first_prev = false;
+      for (int n = 0; n <= count; ++n) {
+        bool first = false;
+        if (n < count) {
+          // S^T(n) = K(n) Q^T
+          first = w.j == w.jbeg;
+          if (first) {
+            ++qn;
+            wait(&ms.qfull[qn % C::QB], (qn / C::QB) & 1, fail);
           }
-        };
-        bool first_prev = false;
-        int pieces_done = 0;
-        for (long long n = 0; n <= count; ++n) {
-          bool first = false;
-          if (n < count) {
-            // S^T(n) = K(n) Q^T
-            first = w.j == w.jbeg;
-            if (first) {
-              ++qn;
-              wait(&ms.qfull[qn % C::QB], (qn / C::QB) & 1, fail);
-            }
-            const uint32_t d = taddr + uint32_t(n & 1) * NR;
-            for (int hh = 0; hh < C::H; ++hh) {
-              take();
-              const uint32_t ka = su32(ring + slot * C::SLOT);
-              const uint32_t qa = su32(sq + (qn % C::QB) * C::QBYTES) + hh * (C::DS / 64) * (NR * 128);
-              if (!*fail) {
+          const uint32_t d = taddr + uint32_t(n & 1) * NR;
+          const uint64_t qd = desc(su32(sq + (qn % C::QB) * C::QBYTES), 16, 1024, 2);
 #pragma unroll
-                for (int k = 0; k < C::DS / 16; ++k) {
-                  const uint32_t ko = (k / 4) * (kKeys * 128) + (k % 4) * 32, qo = (k / 4) * (NR * 128) + (k % 4) * 32;
-                  mma(d, desc(ka + ko, 16, 1024, 2), desc(qa + qo, 16, 1024, 2), kIdescS, hh + k > 0);
-                }
-                commit_to(&ms.empty[slot]);
-              }
-              pass();
-            }
+          for (int hh = 0; hh < C::H; ++hh) {
+            wait(&ms.full[rg.slot], rg.phase, fail);
+            tc_after();
             if (!*fail) {
-              commit_to(&ms.sfull[n & 1]);
-              if (w.j + 1 == w.jend) commit_to(&ms.qfree[qn % C::QB]);
-            }
-          }
-          if (n > 0) {
-            // O^T += V(n-1)^T P(n-1)^T
-            const int p = int((n - 1) & 1);
-            wait(&ms.pfull[p], ((n - 1) >> 1) & 1, fail);
-            if (first_prev && pieces_done > 0) wait(&ms.ofree, (pieces_done - 1) & 1, fail);
-            if (first_prev) ++pieces_done;
-            const uint32_t pa = su32(sp + p * C::PBYTES);
-            for (int hh = 0; hh < C::H; ++hh) {
-              take();
-              const uint32_t va = su32(ring + slot * C::SLOT);
-              if (!*fail) {
+              const uint64_t kd = desc(su32(ring + rg.slot * C::SLOT), 16, 1024, 2);
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k) {
-                  // D = 64: the upper 64 rows of M read the same columns again and are not used
-                  mma(taddr + uint32_t(2 + hh) * NR, desc(va + k * 2048, D < 128 ? 0 : kKeys * 128, 1024, 2),
-                      desc(pa + k * 256, 128, 2048, 0), kIdescO, !first_prev || k > 0);
-                }
-                commit_to(&ms.empty[slot]);
-              }
-              pass();
+              for (int k = 0; k < C::DS / 64; ++k)
+                mma4<2, 2>(d, kd + k * (kKeys * 128 >> 4), qd + (hh * (C::DS / 64) + k) * (NR * 128 >> 4), kIdescS,
+                           hh + k > 0);
+              commit_to(&ms.empty[rg.slot]);
             }
-            if (!*fail) commit_to(&ms.pvdone[p]);
+            rg.next();
           }
-          first_prev = first;
-          if (n + 1 < count) w.next(a, cap);
+          if (!*fail) {
+            commit_to(&ms.sfull[n & 1]);
+            if (w.j + 1 == w.jend) commit_to(&ms.qfree[qn % C::QB]);
+          }
         }
-        commit_to(&ms.drain);
-        unsigned long long t0 = now_ns();
-        for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
-          asm volatile(
-              "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-              : "=r"(ok)
-              : "r"(su32(&ms.drain))
-              : "memory");
+        if (n > 0) {
+          // O^T += V(n-1)^T P(n-1)^T
+          const int p = (n - 1) & 1;
+          wait(&ms.pfull[p], ((n - 1) >> 1) & 1, fail);
+          if (first_prev) {
+            if (pieces > 0) wait(&ms.ofree, (pieces - 1) & 1, fail);
+            ++pieces;
+          }
+          const uint64_t pd = desc(su32(sp + p * C::PBYTES), 128, 2048, 0);
+#pragma unroll
+          for (int hh = 0; hh < C::H; ++hh) {
+            wait(&ms.full[rg.slot], rg.phase, fail);
+            tc_after();
+            if (!*fail) {
+              // D = 64: the upper 64 rows of M read the same columns again and are not used
+              const uint64_t vd = desc(su32(ring + rg.slot * C::SLOT), D < 128 ? 0 : kKeys * 128, 1024, 2);
+#pragma unroll
+              for (int k = 0; k < kKeys / 64; ++k)
+                mma4<128, 16>(taddr + uint32_t(2 + hh) * NR, vd + k * 512, pd + k * 64, kIdescO, !first_prev || k > 0);
+              commit_to(&ms.empty[rg.slot]);
+            }
+            rg.next();
+          }
+          if (!*fail) commit_to(&ms.pvdone[p]);
+        }
+        first_prev = first;
+        if (n + 1 < count) w.next(a, cap);
       }
-      __syncwarp();
-    } else if (warp > kMmaWarp) {
-      // -------------------------------------------------------- producers
-      const int pt = tid - kProd0;
-      int slot = 0, qn = -1;
-      uint32_t sph = 1;  // a fresh slot is empty
-      auto pass = [&]() {
-        if (++slot == C::NS) {
-          slot = 0;
-          sph ^= 1;
+      commit_to(&ms.drain);
+      const unsigned long long t0 = now_ns();
+      for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(&ms.drain))
+            : "memory");
+    } else if (warp == kLoadWarp) {
+      // -------------------------------------------------------- loads
+      const KvView& kv = a.kv;
+      const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
+      // pages of a tile's boxes: up to four a lane
+      auto pages_of = [&](const Walk& k, int id[4]) {
+        const int32_t* row = kv.page_table + (long long)k.b * kv.table_stride;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = lane + 32 * i, key = (k.s.tile0 + k.j) * kKeys + (x << box_shift);
+          id[i] = -2;
+          if (x < boxes && key < k.s.hi && key + (1 << box_shift) > k.s.lo) id[i] = row[key >> kv.page_shift];
         }
       };
-      auto give = [&](uint64_t* b) {  // this warp's part of a slot is in shared memory
-        proxy_fence();
+      auto put_pages = [&](const int id[4], int* out) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = lane + 32 * i;
+          if (x < boxes) {
+            const bool ok = id[i] >= 0 && id[i] < kv.npages;
+            if (!ok && id[i] != -2) set_error(a.err, MOE_ERANGE);
+            out[x] = ok ? id[i] : kv.npages;  // past the end: zeros
+          }
+        }
+      };
+      Ring<E4M3 ? C::NRAW : C::NS> rg(1);  // a fresh slot is empty
+      auto load = [&](const CUtensorMap* tm, const int* page, int h, int key0) {
+        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
+#pragma unroll 1
+        for (int hh = 0; hh < C::H; ++hh) {
+          uint64_t* full = E4M3 ? &ms.rfull[rg.slot] : &ms.full[rg.slot];
+          wait(E4M3 ? &ms.rempty[rg.slot] : &ms.empty[rg.slot], rg.phase, fail);
+          if (*fail) break;
+          if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
+          __syncwarp();
+          constexpr int CHUNKS = E4M3 ? 1 : C::DS / 64;
+#pragma unroll 1
+          for (int x = lane; x < boxes * CHUNKS; x += 32) {
+            const int p = x & (boxes - 1), c = x >> (7 - box_shift);
+            uint8_t* dst = E4M3 ? raw + rg.slot * C::RAW + (p << box_shift) * C::DS
+                                : ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
+            load_box(dst, tm, hh * C::DS + c * 64, tok, h, page[p], full);
+          }
+          rg.next();
+        }
+      };
+      int qn = -1, id[4], hv = 0, key0v = 0;
+      pages_of(w, id);
+      for (int n = 0; n <= count; ++n) {
+        if (n < count) {
+          if (w.j == w.jbeg) {
+            ++qn;
+            if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
+            if (lane == 0 && !*fail) {
+              uint64_t* b = &ms.qfull[qn % C::QB];
+              expect(b, uint32_t(a.tokens * a.G * D * 2));
+              for (int c = 0; c < D / 64; ++c)
+                load_rows(sq + (qn % C::QB) * C::QBYTES + c * (NR * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0, b);
+            }
+            __syncwarp();
+          }
+          put_pages(id, ms.page[n & 1]);
+          __syncwarp();
+        }
+        const int h = w.h, key0 = (w.s.tile0 + w.j) * kKeys;
+        const bool more = n + 1 < count;
+        if (more) {
+          w.next(a, cap);
+          pages_of(w, id);  // on their way while this tile is asked for
+        }
+        if (n < count) load(&a.mk, ms.page[n & 1], h, key0);
+        if (n > 0) load(&a.mv, ms.page[(n - 1) & 1], hv, key0v);
+        hv = h;
+        key0v = key0;
         __syncwarp();
-        if (lane == 0) arrive(b);
-      };
-      auto queries = [&](const Walk<NR>& wk, auto&& before_wait) {
-        ++qn;
-        if (qn >= C::QB) before_wait();
-        if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
-        load_q<D, NR, kProd>(a, wk, sq + (qn % C::QB) * C::QBYTES, pt);
-        give(&ms.qfull[qn % C::QB]);
-      };
-      if constexpr (!E4M3) {
-        // cp.async, 16 bytes a thread; a slot is handed over when kLag newer ones are on their way
-        constexpr int CH = C::DS / 8, STEP = kProd / CH, RPT = kKeys / STEP;
-        constexpr int kLag = C::NS / 2;
-        const int r0 = pt / CH, c = pt % CH;
-        Rows<RPT> rk, rv;
-        int given = 0, made = 0;  // slots handed over, slots begun
-        int gslot = 0;
-        auto hand = [&]() {
+      }
+    } else if (warp > kLoadWarp) {
+      // -------------------------------------------------------- E4M3 codes -> bf16
+      if constexpr (E4M3) {
+        const int vt = tid - 32 * (kLoadWarp + 1);
+        constexpr int CH = C::DS / 8, STEP = 32 * C::VW / CH;  // 8 codes a thread make one 16-byte piece
+        const int r0 = vt / CH, c = vt % CH;
+        Ring<C::NRAW> in(0);
+        Ring<C::NS> out(1);
+        for (long long x = 0; x < 2ll * C::H * count; ++x) {
+          wait(&ms.rfull[in.slot], in.phase, fail);
+          wait(&ms.empty[out.slot], out.phase, fail);
+          const uint8_t* src = raw + in.slot * C::RAW + c * 8;
+          uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
+#pragma unroll 8
+          for (int r = r0; r < kKeys; r += STEP) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src + r * C::DS);
+            *reinterpret_cast<uint4*>(dst + sw128(r, c % 8)) =
+                make_uint4(e4m3x2_to_bf16x2(v.x & 0xffffu), e4m3x2_to_bf16x2(v.x >> 16),
+                           e4m3x2_to_bf16x2(v.y & 0xffffu), e4m3x2_to_bf16x2(v.y >> 16));
+          }
           proxy_fence();
           __syncwarp();
-          if (lane == 0) arrive(&ms.full[gslot]);
-          if (++gslot == C::NS) gslot = 0;
-          ++given;
-        };
-        // what has been begun is handed over before a wait that depends on it
-        auto flush = [&]() {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          while (given < made) hand();
-        };
-        auto load = [&](const uint8_t* pool, const Rows<RPT>& r) {
-          for (int hh = 0; hh < C::H; ++hh) {
-            wait(&ms.empty[slot], sph, fail);
-            uint8_t* dst = ring + slot * C::SLOT + (c / 8) * (kKeys * 128);
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-              const bool ok = r.off[i] >= 0;
-              const uint8_t* src = pool + (ok ? r.off[i] + hh * (C::DS * 2) + c * 16 : 0);
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst) + sw128(r0 + i * STEP, c % 8)),
-                           "l"(src), "r"(ok ? 16 : 0)
-                           : "memory");
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            pass();
-            ++made;
-            if (made - given > kLag) {
-              asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-              hand();
-            }
+          if (lane == 0) {
+            arrive(&ms.full[out.slot]);
+            arrive(&ms.rempty[in.slot]);
           }
-        };
-        for (long long n = 0; n <= count; ++n) {
-          if (n < count) {
-            if (w.j == w.jbeg) queries(w, flush);
-            find_rows<RPT, STEP>(a, w, r0, c, rk, c == 0);
-            load(a.kv.k, rk);
-          }
-          if (n > 0) load(a.kv.v, rv);
-          rv = rk;
-          if (n + 1 < count) w.next(a, cap);
-        }
-        flush();
-      } else {
-        // 16 codes a load, turned into bf16 on the way; the loads of kDepth tiles are in flight
-        constexpr int CH = C::DS / 16, STEP = kProd / CH, RPT = kKeys / STEP;
-        constexpr int kRegs = NR > 16 ? 32 : 64, kTile = C::H * RPT * 8;  // registers for loads, of one tile
-        constexpr int kDepth = 4 * kTile <= kRegs ? 4 : 2 * kTile <= kRegs ? 2 : 1;
-        const int r0 = pt / CH, c = pt % CH;
-        uint4 kb[kDepth][C::H][RPT], vb[kDepth][C::H][RPT];
-        Rows<RPT> rk, rv;
-        auto load = [&](const uint8_t* pool, const Rows<RPT>& r, uint4 (&buf)[C::H][RPT]) {
-#pragma unroll
-          for (int hh = 0; hh < C::H; ++hh)
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-              buf[hh][i] = make_uint4(0, 0, 0, 0);
-              if (r.off[i] >= 0)
-                buf[hh][i] = __ldg(reinterpret_cast<const uint4*>(pool + r.off[i] + hh * C::DS + c * 16));
-            }
-        };
-        auto store = [&](const uint4 (&buf)[C::H][RPT]) {
-#pragma unroll
-          for (int hh = 0; hh < C::H; ++hh) {
-            wait(&ms.empty[slot], sph, fail);
-            uint8_t* dst = ring + slot * C::SLOT + (c / 4) * (kKeys * 128);
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) {
-              const uint32_t v[4] = {buf[hh][i].x, buf[hh][i].y, buf[hh][i].z, buf[hh][i].w};
-              uint32_t f[8];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                f[2 * x] = e4m3x2_to_bf16x2(v[x] & 0xffffu);
-                f[2 * x + 1] = e4m3x2_to_bf16x2(v[x] >> 16);
-              }
-              const int r = r0 + i * STEP;
-              *reinterpret_cast<uint4*>(dst + sw128(r, (c % 4) * 2)) = make_uint4(f[0], f[1], f[2], f[3]);
-              *reinterpret_cast<uint4*>(dst + sw128(r, (c % 4) * 2 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
-            }
-            give(&ms.full[slot]);
-            pass();
-          }
-        };
-        Walk<NR> ahead = w;  // kDepth tiles ahead of w
-        long long an = 0;    // its tile
-#pragma unroll
-        for (int u = 0; u < kDepth; ++u) {
-          if (an < count) {
-            find_rows<RPT, STEP>(a, ahead, r0, c, rk, c == 0);
-            load(a.kv.k, rk, kb[u]);
-            if (u < kDepth - 1) load(a.kv.v, rk, vb[u]);
-            rv = rk;
-            ++an;
-            if (an < count) ahead.next(a, cap);
-          }
-        }
-        for (long long n0 = 0; n0 <= count; n0 += kDepth) {
-#pragma unroll
-          for (int u = 0; u < kDepth; ++u) {
-            const long long n = n0 + u;
-            constexpr int kBack = kDepth - 1;
-            if (n < count) {
-              if (w.j == w.jbeg) queries(w, [] {});
-              store(kb[u]);
-            }
-            // rv: tile n + kDepth - 1, whose values follow; then the keys of tile n + kDepth
-            if (n > 0 && n <= count) store(vb[(u + kBack) % kDepth]);
-            if (n + kDepth - 1 < count) load(a.kv.v, rv, vb[(u + kBack) % kDepth]);
-            if (n + kDepth < count) {
-              find_rows<RPT, STEP>(a, ahead, r0, c, rk, c == 0);
-              load(a.kv.k, rk, kb[u]);
-              rv = rk;
-              if (++an < count) ahead.next(a, cap);
-            }
-            if (n + 1 < count) w.next(a, cap);
-          }
+          in.next();
+          out.next();
         }
       }
     } else {
       // -------------------------------------------------------- softmax
-      constexpr int CW = C::CW;
+      constexpr int CW = C::CW, CK = CW == 16 || (E4M3 && NR > 32) ? 16 : 32;  // rows of a warp, and at a time
       const int quad = warp & 3, c0 = (warp >> 2) * CW;
       const int krow = quad * 32 + lane;  // this thread's key in a tile, and its column of v
       const uint32_t tl = taddr + (uint32_t(quad * 32) << 16);
       float l[CW];
       float factor = 0.f;  // of the scores, in log2 units
-      for (long long n = 0; n < count; ++n) {
+      for (int n = 0; n < count; ++n) {
         const bool first = w.j == w.jbeg;
         if (first) {
 #pragma unroll
           for (int i = 0; i < CW; ++i) l[i] = 0.f;
           factor = a.scale * 1.4426950408889634f * (E4M3 && a.kv.k_scale ? a.kv.k_scale[w.h] : 1.f);
         }
-        const int p = int(n & 1);
+        const int p = n & 1;
         const uint32_t ph = (n >> 1) & 1;
         const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
         // every row of the tile sees every key of it
         const bool whole = key0 + kKeys <= min(w.r.pos0 + w.s.i0 + 1, cap) &&
                            (a.window <= 0 || key0 > w.r.pos0 + w.s.i1 - a.window);
+        // rows x .. x + CK - 1: scores in log2 units, hidden ones -inf
+        auto scores = [&](int x0, float* s) {
+#pragma unroll
+          for (int i = 0; i < CK; i += 16) ld16(tl + p * NR + c0 + x0 + i, s + i);
+          ld_wait();
+#pragma unroll
+          for (int x = 0; x < CK; ++x) s[x] *= factor;
+          if (!whole) {
+            // rows are in order of their tokens: those from `from` on and before `to` see this key
+            const int t_from = max(key - w.r.pos0, 0) - w.s.i0;
+            const int from = key >= cap ? INT_MAX : t_from > a.tokens ? INT_MAX : t_from * a.G;
+            const int t_to = a.window > 0 ? key - w.r.pos0 + a.window - w.s.i0 : a.tokens;
+            const int to = t_to >= a.tokens ? INT_MAX : t_to * a.G;
+#pragma unroll
+            for (int x = 0; x < CK; ++x)
+              if (c0 + x0 + x < from || c0 + x0 + x >= to) s[x] = -INFINITY;
+          }
+        };
         wait(&ms.sfull[p], ph, fail);
         tc_after();
-        float s[CW];
+        float s[CK];
+        bool set = first;
+        if (!first) {
+          float over = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < CW; i += 16) ld16(tl + p * NR + c0 + i, s + i);
-        ld_wait();
-        float over = -INFINITY;
-        {
-          int i = (w.rt * NR + c0) / a.G, g = (w.rt * NR + c0) - i * a.G;
+          for (int x0 = 0; x0 < CW; x0 += CK) {
+            scores(x0, s);
 #pragma unroll
-          for (int x = 0; x < CW; ++x) {
-            s[x] *= factor;
-            if (!whole) {
-              const int pos = w.r.pos0 + i;
-              if (key > pos || key >= cap || (a.window > 0 && key <= pos - a.window)) s[x] = -INFINITY;
-              if (++g == a.G) {
-                g = 0;
-                ++i;
-              }
-            }
-            if (!first) over = fmaxf(over, s[x] - ms.m[c0 + x]);
+            for (int x = 0; x < CK; ++x) over = fmaxf(over, s[x] - ms.m[c0 + x0 + x]);
           }
+          set = vote_any<kSoft>(over > kGrow);
         }
-        if (vote_any<kSoft>(first || over > kGrow)) {
+        if (set) {
           // set m: the rows' maxima over the 128 keys
 #pragma unroll
-          for (int x = 0; x < CW; ++x) {
-            const float v = warp_max(s[x]);
-            if (lane == (x & 31)) ms.red[quad][c0 + x] = v;
+          for (int x0 = 0; x0 < CW; x0 += CK) {
+            scores(x0, s);
+#pragma unroll
+            for (int x = 0; x < CK; ++x) {
+              const float v = warp_max(s[x]);
+              if (lane == (x & 31)) ms.red[quad][c0 + x0 + x] = v;
+            }
           }
           softmax_sync<kSoft>();
           if (tid < NR) {
@@ -740,61 +718,74 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
             for (int x = 0; x < CW; ++x) l[x] *= ms.alpha[c0 + x];
             wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
             tc_after();
-            for (int hh = 0; hh < C::H; ++hh)
+#pragma unroll 1
+            for (int x = 0; x < C::H * CW; x += 16) {
+              const int hh = x / CW, y0 = x % CW;
+              float o[16];
+              ld16(tl + (2 + hh) * NR + c0 + y0, o);
+              ld_wait();
 #pragma unroll
-              for (int x = 0; x < CW; x += 16) {
-                float o[16];
-                ld16(tl + (2 + hh) * NR + c0 + x, o);
-                ld_wait();
-#pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] *= ms.alpha[c0 + x + y];
-                st16(tl + (2 + hh) * NR + c0 + x, o);
-              }
+              for (int y = 0; y < 16; ++y) o[y] *= ms.alpha[c0 + y0 + y];
+              st16(tl + (2 + hh) * NR + c0 + y0, o);
+            }
             st_wait();
           }
         }
         if (n >= 2) wait(&ms.pvdone[p], ((n - 2) >> 1) & 1, fail);  // P(n - 2) has been read
         uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
 #pragma unroll
-        for (int x = 0; x < CW; x += 8) {
-          uint32_t u[4];
+        for (int x0 = 0; x0 < CW; x0 += CK) {
+          if (CW > CK) scores(x0, s);
 #pragma unroll
-          for (int y = 0; y < 8; y += 2) {
-            const float e0 = ex2(s[x + y] - ms.m[c0 + x + y]);
-            const float e1 = ex2(s[x + y + 1] - ms.m[c0 + x + y + 1]);
-            l[x + y] += e0;
-            l[x + y + 1] += e1;
-            u[y / 2] = pack2(e0, e1);
+          for (int x = 0; x < CK; x += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int y = 0; y < 8; y += 2) {
+              const float e0 = ex2(s[x + y] - ms.m[c0 + x0 + x + y]);
+              const float e1 = ex2(s[x + y + 1] - ms.m[c0 + x0 + x + y + 1]);
+              l[x0 + x + y] += e0;
+              l[x0 + x + y + 1] += e1;
+              u[y / 2] = pack2(e0, e1);
+            }
+            *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
           }
-          *reinterpret_cast<uint4*>(dst + ((c0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        // A value that is not finite must not reach a row that does not see its key (0 times it is
-        // NaN): where rows differ in what they see, such values are taken out of the tile and added
-        // to the rows that do see them.
+        // Values at hidden keys may hold anything, and 0 times what is not finite is NaN.  Those that
+        // no row sees become zeros; where rows differ in what they see, values that are not finite
+        // are taken out of the tile and added to the rows that do see them.
         bool spoiled = false;
-        if (!whole && w.s.i1 > w.s.i0) {
-          const long long at = (n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
+        if (!whole) {
+          const bool gone = key < w.s.lo || key >= w.s.hi, mixed = w.s.i1 > w.s.i0;
+          const int at = (n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
           bool bad = false;
+#pragma unroll 1
           for (int hh = 0; hh < C::H; ++hh) {
-            const int slot = int((at + hh) % C::NS);
+            const int slot = (at + hh) % C::NS;
             wait(&ms.full[slot], uint32_t((at + hh) / C::NS) & 1, fail);
-            constexpr uint32_t kExp = 0x7f80u;
+            uint8_t* row = ring + slot * C::SLOT;
+            if (c0 == 0 && (gone || mixed)) {
 #pragma unroll 4
-            for (int c = 0; c < C::DS / 8; ++c) {
-              uint4* v = reinterpret_cast<uint4*>(ring + slot * C::SLOT + (c / 8) * (kKeys * 128) + sw128(krow, c % 8));
-              uint32_t x[4] = {v->x, v->y, v->z, v->w};
-              bool here = false;
+              for (int c = 0; c < C::DS / 8; ++c) {
+                uint4* v = reinterpret_cast<uint4*>(row + (c / 8) * (kKeys * 128) + sw128(krow, c % 8));
+                uint32_t x[4] = {0, 0, 0, 0};
+                bool here = gone;
+                if (!gone) {
+                  x[0] = v->x, x[1] = v->y, x[2] = v->z, x[3] = v->w;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if ((x[i] & kExp) == kExp) x[i] &= 0xffff0000u, here = true;
-                if ((x[i] >> 16 & kExp) == kExp) x[i] &= 0xffffu, here = true;
+                  for (int i = 0; i < 4; ++i) {
+                    if ((x[i] & 0x7f80u) == 0x7f80u) x[i] &= 0xffff0000u, here = true;
+                    if ((x[i] & 0x7f800000u) == 0x7f800000u) x[i] &= 0xffffu, here = true;
+                  }
+                  bad |= here;
+                }
+                if (here) *v = make_uint4(x[0], x[1], x[2], x[3]);
               }
-              if (here) *v = make_uint4(x[0], x[1], x[2], x[3]);
-              bad |= here;
             }
           }
-          if (bad && c0 == 0) ms.bad[atomicAdd(&ms.nbad, 1)] = uint8_t(krow);
-          spoiled = vote_any<kSoft>(bad);
+          if (mixed) {
+            if (bad) ms.bad[atomicAdd(&ms.nbad, 1)] = uint8_t(krow);
+            spoiled = vote_any<kSoft>(bad);
+          }
         }
         proxy_fence();
         tc_before();
@@ -804,36 +795,29 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
           wait(&ms.pvdone[p], ph, fail);
           tc_after();
           const int nbad = *const_cast<volatile int*>(&ms.nbad);
-          for (int e = 0; e < nbad; ++e) {
-            const int k = key0 + ms.bad[e];
+#pragma unroll 1
+          for (int e = 0; e < nbad * C::H; ++e) {
+            const int k = key0 + ms.bad[e / C::H], hh = e % C::H, col = hh * 128 + krow;
             const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (k >> a.kv.page_shift)];
             const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
                                (long long)(k & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
-            for (int hh = 0; hh < C::H; ++hh) {
-              const int col = hh * 128 + krow;
-              float add = 0.f;
-              if (col < D) {
-                if (E4M3) add = f16x2_to_f32x2(e4m3x2_to_f16x2(v[col])).x;
-                else add = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[col]);
-              }
-              if (isfinite(add)) add = 0.f;
-              int i = (w.rt * NR + c0) / a.G, g = (w.rt * NR + c0) - i * a.G;
+            float add = 0.f;
+            if (col < D) {
+              if (E4M3) add = f16x2_to_f32x2(e4m3x2_to_f16x2(v[col])).x;
+              else add = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[col]);
+            }
+            if (isfinite(add)) add = 0.f;
+#pragma unroll 1
+            for (int x = 0; x < CW; x += 16) {
+              float o[16];
+              ld16(tl + (2 + hh) * NR + c0 + x, o);
+              ld_wait();
 #pragma unroll
-              for (int x = 0; x < CW; x += 16) {
-                float o[16];
-                ld16(tl + (2 + hh) * NR + c0 + x, o);
-                ld_wait();
-#pragma unroll
-                for (int y = 0; y < 16; ++y) {
-                  const int pos = w.r.pos0 + i;
-                  if (k <= pos && (a.window <= 0 || k > pos - a.window)) o[y] += add;
-                  if (++g == a.G) {
-                    g = 0;
-                    ++i;
-                  }
-                }
-                st16(tl + (2 + hh) * NR + c0 + x, o);
+              for (int y = 0; y < 16; ++y) {
+                const int pos = w.r.pos0 + w.s.i0 + (c0 + x + y) / a.G;
+                if (k <= pos && (a.window <= 0 || k > pos - a.window)) o[y] += add;
               }
+              st16(tl + (2 + hh) * NR + c0 + x, o);
             }
           }
           st_wait();
@@ -855,52 +839,51 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
           }
           softmax_sync<kSoft>();
           const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
-          const int rows = min(NR, w.r.n * a.G - w.rt * NR);
-          const long long part = 2ll * blockIdx.x + (head ? 0 : 1);
-          if (split) {
-            if (tid < rows) {
-              float2 v = make_float2(ms.m[tid], ms.red[0][tid] + ms.red[1][tid] + ms.red[2][tid] + ms.red[3][tid]);
-              reinterpret_cast<float2*>(a.ml)[part * NR + tid] = v;
-            }
-            if (head && tid == 0) {
-              a.head[blockIdx.x] = make_int4(w.b, w.h, w.rt, 1);
-              a.cut[2 * blockIdx.x] = w0 - w.jbeg;
-              a.cut[2 * blockIdx.x + 1] = w0 - w.jbeg + w.s.nt;
-            }
+          const int rows = (w.s.i1 - w.s.i0 + 1) * a.G;
+          const long long part = 2ll * run + (head ? 0 : 1);
+          if (tid < NR) {
+            const float t = ms.red[0][tid] + ms.red[1][tid] + ms.red[2][tid] + ms.red[3][tid];
+            const float vs = E4M3 && a.kv.v_scale ? a.kv.v_scale[w.h] : 1.f;
+            if (split && tid < rows) reinterpret_cast<float2*>(a.ml)[part * NR + tid] = make_float2(ms.m[tid], t);
+            ms.alpha[tid] = t == 0.f ? 0.f : vs / t;
           }
-          const float vs = E4M3 && a.kv.v_scale ? a.kv.v_scale[w.h] : 1.f;
+          if (split && head && tid == 0) {
+            a.head[run] = make_int4(w.b, w.h, w.rt, 1);
+            a.cut[run] = make_int2(w0 - w.jbeg, w0 - w.jbeg + w.s.nt);
+          }
+          softmax_sync<kSoft>();
           wait(&ms.pvdone[p], ph, fail);
           tc_after();
-          for (int hh = 0; hh < C::H; ++hh) {
-            const int col = hh * 128 + krow;
-            int i = (w.rt * NR + c0) / a.G, g = (w.rt * NR + c0) - i * a.G;
+#pragma unroll 1
+          for (int x = 0; x < C::H * CW; x += 16) {
+            const int hh = x / CW, row0 = c0 + x % CW, col = hh * 128 + krow;
+            if (row0 >= rows) continue;
+            float o[16];
+            ld16(tl + (2 + hh) * NR + row0, o);
+            ld_wait();
+            if (split) {
+              float* to = a.part + (part * NR + row0) * D + col;
 #pragma unroll
-            for (int x = 0; x < CW; x += 16) {
-              float o[16];
-              ld16(tl + (2 + hh) * NR + c0 + x, o);
-              ld_wait();
+              for (int y = 0; y < 16; ++y)
+                if (row0 + y < rows && col < D) to[y * D] = o[y];
+            } else {
+              int i = row0 / a.G, g = row0 - i * a.G;
+              uint16_t* to = a.o + (long long)(w.r.s0 + w.s.i0 + i) * a.os + (long long)(w.h * a.G + g) * D + col;
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
-                const int row = c0 + x + y;
-                if (row < rows && col < D) {
-                  if (split) {
-                    a.part[(part * NR + row) * D + col] = o[y];
-                  } else {
-                    const float t = ms.red[0][row] + ms.red[1][row] + ms.red[2][row] + ms.red[3][row];
-                    const float v = t == 0.f ? 0.f : o[y] / t * vs;
-                    a.o[(w.r.s0 + i) * a.os + (long long)(w.h * a.G + g) * D + col] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(v));
-                  }
-                }
+                // a sum of zero is a row that sees no key; its O is zeros
+                if (row0 + y < rows && col < D)
+                  *to = __bfloat16_as_ushort(__float2bfloat16_rn(o[y] * ms.alpha[row0 + y]));
+                to += D;
                 if (++g == a.G) {
                   g = 0;
-                  ++i;
+                  to += a.os - (long long)a.G * D;
                 }
               }
             }
           }
           tc_before();
-          softmax_sync<kSoft>();  // m, red and O are free
+          softmax_sync<kSoft>();  // m, alpha, red and O are free
           if (lane == 0) arrive(&ms.ofree);
         }
         if (n + 1 < count) w.next(a, cap);
@@ -926,16 +909,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
   __shared__ float4 acc[kJoinThreads];
   pdl_trigger();
   pdl_wait();
-  const long long total = *a.total;
-  const int runs = int(min((long long)gridDim.x, total)), c = blockIdx.x, tid = threadIdx.x;
+  const int total = *a.total;
+  const int runs = min(int(gridDim.x), total), c = blockIdx.x, tid = threadIdx.x;
   if (c < 1 || c >= runs) return;
   const int4 hd = a.head[c];
-  const long long u0 = a.cut[2 * c], u1 = a.cut[2 * c + 1];
-  if (!hd.w || total * (c - 1) / runs > u0) return;
+  const int2 unit = a.cut[c];
+  if (!hd.w || cut_at(total, runs, c - 1) > unit.x) return;
   const Req r = load_req(a.kv, hd.x);
-  const int rows = min(NR, r.n * a.G - hd.z * NR);
+  const int i0 = hd.z * a.tokens, rows = min(a.tokens, r.n - i0) * a.G;
   int np = 1;  // pieces: the tail of run c - 1, then the heads of the runs that begin before the unit's end
-  while (c - 1 + np < runs && total * (c - 1 + np) / runs < u1) ++np;
+  while (c - 1 + np < runs && cut_at(total, runs, c - 1 + np) < unit.y) ++np;
   auto place = [&](int k) { return 2ll * (c - 1 + k) + (k == 0 ? 1 : 0); };
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     float m = kUnset;
@@ -980,18 +963,21 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
       }
       const float vs = a.kv.v_scale ? a.kv.v_scale[hd.y] : 1.f;
       const float x = l == 0.f ? 0.f : vs / l;
-      const int rr = hd.z * NR + row, i = rr / a.G, g = rr - i * a.G;
+      const int i = row / a.G, g = row - i * a.G;
       uint2 u;
       u.x = pack2(o.x * x, o.y * x);
       u.y = pack2(o.z * x, o.w * x);
-      *reinterpret_cast<uint2*>(a.o + (r.s0 + i) * a.os + (long long)(hd.y * a.G + g) * D + col * 4) = u;
+      *reinterpret_cast<uint2*>(a.o + (long long)(r.s0 + i0 + i) * a.os + (long long)(hd.y * a.G + g) * D + col * 4) = u;
     }
     __syncthreads();
   }
 }
 
-// Tile of rows for calls of about `rows` query rows per request and key head.
-inline int row_tile(int D, long long rows) { return rows <= 16 ? 16 : rows <= 64 || D == 256 ? 64 : 128; }
+// Tile of rows for calls of about n new tokens a request and G query heads a key head: the smallest
+// that holds a request's rows, else the largest.  A tile holds the heads of NR / G whole tokens.
+inline int row_tile(int D, int e4m3, int G, int n) {
+  return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || e4m3 || D > 128 ? 64 : 128;
+}
 
 template <int D, int NR, bool E4M3>
 int launch_one(const Args& a, int ctas, cudaStream_t s) {
@@ -1000,11 +986,11 @@ int launch_one(const Args& a, int ctas, cudaStream_t s) {
   if (launch_pdl(k_join<D, NR>, dim3(ctas, 16), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
   return MOE_OK;
 }
-template <int D, int NR>
+template <int D, int NR, bool E4M3>
 int opt_in() {
-  return cudaFuncSetAttribute(k_attn<D, NR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
-                 cudaFuncSetAttribute(k_attn<D, NR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
-                     cudaSuccess
+  // the join keeps the split of L1 and shared memory that the kernel before it had
+  return cudaFuncSetAttribute(k_join<D, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
+                 cudaFuncSetAttribute(k_attn<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
              ? MOE_OK
              : MOE_ECUDA;
 }

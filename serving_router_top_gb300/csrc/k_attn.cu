@@ -1,4 +1,6 @@
 // moe_paged_attention: checks, workspace and launch (the kernels are in attn.cuh).
+#include <cudaTypedefs.h>
+
 #include "attn.cuh"
 
 struct moe_attn_ws {
@@ -6,7 +8,7 @@ struct moe_attn_ws {
   int32_t* error;
   float *part, *ml;
   int4* head;
-  long long* cut;
+  int2* cut;
 };
 
 namespace moe {
@@ -17,6 +19,31 @@ int launch_d256(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
 int opt_in_d64();
 int opt_in_d128();
 int opt_in_d256();
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Tiles of a pool or of the query rows; what lies outside reads as zeros.
+bool encode(CUtensorMap* m, void* base, int e4m3, int rank, const cuuint64_t* dims, const cuuint64_t* pitches,
+            const cuuint32_t* box) {
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  return fn && fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base, dims, pitches,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace attn
 }  // namespace moe
 
@@ -41,7 +68,7 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
   w->ctas = sms < attn::kMaxRuns ? sms : attn::kMaxRuns;  // one CTA per SM
   const size_t rows = 2 * size_t(w->ctas) * (D == 256 ? 64 : 128);
   const size_t o_part = 256, o_ml = o_part + rows * D * 4, o_head = o_ml + rows * 8, o_cut = o_head + size_t(w->ctas) * 16;
-  const size_t bytes = o_cut + (2 * size_t(w->ctas) + 1) * 8;
+  const size_t bytes = o_cut + size_t(w->ctas) * 8 + 4;
   uint8_t* base = nullptr;
   if (cudaMalloc(&base, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -52,7 +79,7 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
   w->part = reinterpret_cast<float*>(base + o_part);
   w->ml = reinterpret_cast<float*>(base + o_ml);
   w->head = reinterpret_cast<int4*>(base + o_head);
-  w->cut = reinterpret_cast<long long*>(base + o_cut);
+  w->cut = reinterpret_cast<int2*>(base + o_cut);
   if (cudaMemset(base, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     moe_attn_ws_destroy(w);
@@ -96,21 +123,33 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   if (T == 0 || b->B == 0) return MOE_OK;
   const long long width = (long long)Hq * kv->D;
   if (!rows_ok(q, q_stride, T, width) || !rows_ok(o, o_stride, T, width)) return MOE_EINVAL;
-  a.q = q;
+  const int nr = attn::row_tile(kv->D, kv->e4m3, Hq / kv->Hkv, b->max_n > 1 ? b->max_n : 1);
   a.o = o;
-  a.qs = q_stride;
-  a.os = o_stride;
+  a.os = T > 1 ? o_stride : width;
   a.G = Hq / kv->Hkv;
   a.window = window;
+  a.tokens = nr / a.G;
+  const int size = kv->e4m3 ? 1 : 2, box = kv->page < attn::kKeys ? kv->page : attn::kKeys;
+  // sizes and byte strides of the pools, innermost first; a size of one takes any stride
+  const cuuint64_t dims[4] = {cuuint64_t(kv->D), cuuint64_t(kv->page), cuuint64_t(kv->Hkv), cuuint64_t(kv->npages)};
+  auto pitch = [&](long long bytes) { return cuuint64_t(bytes ? bytes : kv->D * size); };
+  const cuuint64_t pitches[3] = {pitch(a.kv.tok_stride), pitch(a.kv.head_stride), pitch(a.kv.page_stride)};
+  const cuuint32_t boxes[4] = {cuuint32_t(kv->e4m3 ? (kv->D < 128 ? kv->D : 128) : 64), cuuint32_t(box), 1, 1};
+  const cuuint64_t qdims[3] = {cuuint64_t(kv->D), cuuint64_t(Hq), cuuint64_t(T)};
+  const cuuint64_t qpitches[2] = {cuuint64_t(kv->D) * 2, cuuint64_t(T > 1 ? q_stride : width) * 2};
+  const cuuint32_t qbox[3] = {64, cuuint32_t(a.G), cuuint32_t(a.tokens)};
+  if (!attn::encode(&a.mk, kv->k, kv->e4m3, 4, dims, pitches, boxes) ||
+      !attn::encode(&a.mv, kv->v, kv->e4m3, 4, dims, pitches, boxes) ||
+      !attn::encode(&a.mq, const_cast<uint16_t*>(q), 0, 3, qdims, qpitches, qbox))
+    return MOE_EINVAL;
   a.scale = scale;
   a.err = ws->error;
   a.part = ws->part;
   a.ml = ws->ml;
   a.head = ws->head;
   a.cut = ws->cut;
-  a.total = ws->cut + 2 * ws->ctas;
+  a.total = reinterpret_cast<int*>(ws->cut + ws->ctas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int nr = attn::row_tile(kv->D, (long long)a.G * (b->max_n > 1 ? b->max_n : 1));
   switch (kv->D) {
     case 64: return attn::launch_d64(a, kv->e4m3, nr, ws->ctas, s);
     case 128: return attn::launch_d128(a, kv->e4m3, nr, ws->ctas, s);

@@ -5,15 +5,32 @@ namespace moe {
 namespace attn {
 
 int launch_d128(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s) {
-  switch (nr) {
-    case 16: return e4m3 ? launch_one<128, 16, true>(a, ctas, s) : launch_one<128, 16, false>(a, ctas, s);
-    case 64: return e4m3 ? launch_one<128, 64, true>(a, ctas, s) : launch_one<128, 64, false>(a, ctas, s);
-    default: return e4m3 ? launch_one<128, 128, true>(a, ctas, s) : launch_one<128, 128, false>(a, ctas, s);
+  if (e4m3) {
+    switch (nr) {
+      case 16: return launch_one<128, 16, true>(a, ctas, s);
+      case 32: return launch_one<128, 32, true>(a, ctas, s);
+      default: return launch_one<128, 64, true>(a, ctas, s);
+    }
+  } else {
+    switch (nr) {
+      case 16: return launch_one<128, 16, false>(a, ctas, s);
+      case 32: return launch_one<128, 32, false>(a, ctas, s);
+      case 64: return launch_one<128, 64, false>(a, ctas, s);
+      default: return launch_one<128, 128, false>(a, ctas, s);
+    }
   }
 }
 
 int opt_in_d128() {
-  return opt_in<128, 16>() || opt_in<128, 64>() || opt_in<128, 128>() ? MOE_ECUDA : MOE_OK;
+  return opt_in<128, 16, false>() ||
+                 opt_in<128, 32, false>() ||
+                 opt_in<128, 64, false>() ||
+                 opt_in<128, 128, false>() ||
+                 opt_in<128, 16, true>() ||
+                 opt_in<128, 32, true>() ||
+                 opt_in<128, 64, true>()
+             ? MOE_ECUDA
+             : MOE_OK;
 }
 
 }  // namespace attn

@@ -5,14 +5,30 @@ namespace moe {
 namespace attn {
 
 int launch_d256(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s) {
-  switch (nr) {
-    case 16: return e4m3 ? launch_one<256, 16, true>(a, ctas, s) : launch_one<256, 16, false>(a, ctas, s);
-    default: return e4m3 ? launch_one<256, 64, true>(a, ctas, s) : launch_one<256, 64, false>(a, ctas, s);
+  if (e4m3) {
+    switch (nr) {
+      case 16: return launch_one<256, 16, true>(a, ctas, s);
+      case 32: return launch_one<256, 32, true>(a, ctas, s);
+      default: return launch_one<256, 64, true>(a, ctas, s);
+    }
+  } else {
+    switch (nr) {
+      case 16: return launch_one<256, 16, false>(a, ctas, s);
+      case 32: return launch_one<256, 32, false>(a, ctas, s);
+      default: return launch_one<256, 64, false>(a, ctas, s);
+    }
   }
 }
 
 int opt_in_d256() {
-  return opt_in<256, 16>() || opt_in<256, 64>() ? MOE_ECUDA : MOE_OK;
+  return opt_in<256, 16, false>() ||
+                 opt_in<256, 32, false>() ||
+                 opt_in<256, 64, false>() ||
+                 opt_in<256, 16, true>() ||
+                 opt_in<256, 32, true>() ||
+                 opt_in<256, 64, true>()
+             ? MOE_ECUDA
+             : MOE_OK;
 }
 
 }  // namespace attn

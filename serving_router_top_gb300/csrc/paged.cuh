@@ -22,11 +22,11 @@ struct KvView {
 inline int kv_view(const moe_kv_pages* p, const moe_kv_batch* b, KvView* out) {
   if (!p || !b || !p->k || !p->v || (p->e4m3 != 0 && p->e4m3 != 1) || p->Hkv < 1 || p->Hkv > 1024 ||
       (p->D != 64 && p->D != 128 && p->D != 256) || p->page < 1 || p->page > 65536 || (p->page & (p->page - 1)) ||
-      p->npages < 1)
+      p->npages < 1 || (p->e4m3 && p->D * p->page < 128))  // the copy engine writes whole 128-byte lines
     return MOE_EINVAL;
   const int size = p->e4m3 ? 1 : 2;
   auto stride_ok = [&](long long s, int n) {
-    return n <= 1 || (s >= p->D && s < (1ll << 56) && s * size % 16 == 0);
+    return n <= 1 || (s >= p->D && s < (1ll << 38) && s * size % 16 == 0);
   };
   if (!stride_ok(p->page_stride, p->npages) || !stride_ok(p->head_stride, p->Hkv) || !stride_ok(p->tok_stride, p->page))
     return MOE_EINVAL;

@@ -32,7 +32,8 @@ def batch(**kw):
 BAD_PAGES = [dict(k=None), dict(v=None), dict(k=P16 + 8), dict(v=P16 + 2), dict(e4m3=2), dict(e4m3=-1), dict(Hkv=0),
              dict(Hkv=1025), dict(D=0), dict(D=96), dict(D=512), dict(page=0), dict(page=24), dict(page=1 << 17),
              dict(npages=0), dict(page_stride=127), dict(page_stride=-4096), dict(head_stride=64), dict(tok_stride=127),
-             dict(tok_stride=132), dict(e4m3=1, tok_stride=136), dict(tok_stride=1 << 57)]
+             dict(tok_stride=132), dict(e4m3=1, tok_stride=136), dict(tok_stride=1 << 57),
+             dict(e4m3=1, D=64, page=1)]
 BAD_BATCH = [dict(B=-1), dict(T=-1), dict(max_n=-1), dict(table_stride=-1), dict(q_start=None), dict(kv_len=None),
              dict(page_table=None)]
 
