@@ -48,7 +48,7 @@ constexpr float kUnset = -1e30f;              // m of a row that has seen no key
 constexpr float kGrow = 8.0f;                 // m is set again when a score passes it by this (log2)
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr int kSmem = 232448;
-constexpr int kMisc = 5120;                   // barriers, row statistics, schedule
+constexpr int kMisc = 5632;                   // barriers, row statistics, schedule
 
 struct Args {
   CUtensorMap mk, mv, mq;  // pools [page][head][place][column], query rows [token][head][column]
@@ -82,9 +82,9 @@ struct Cfg {
   static constexpr int NRAW0 = E4M3 ? (FREE - QB * QBYTES - NS * SLOT) / (RAW + 1) : 0, NRAW = NRAW0 > 16 ? 16 : NRAW0;
   static constexpr int CW = NR < 32 ? NR : NR < 128 ? 32 : 64;  // rows a softmax warp holds
   static constexpr int SW = 4 * (NR / CW);                      // softmax warps
-  static constexpr int VW = E4M3 ? 4 : 0;                       // converting warps
-  static constexpr int THREADS = 32 * (SW + 2 + VW);
-  static constexpr int COLS0 = (2 + H) * NR;
+  static constexpr int VG = !E4M3 ? 0 : NR > 32 ? 1 : 2;        // groups of four converting warps
+  static constexpr int THREADS = 32 * (SW + 3 + 4 * VG);
+  static constexpr int COLS0 = (2 + 2 * H) * NR;                // two S, two O
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
   static_assert(COLS0 <= 512 && NS >= 3 && (!E4M3 || NRAW >= 3), "resources of an SM");
 };
@@ -119,8 +119,8 @@ __device__ __forceinline__ Span span_of(const Req& r, int rt, int tokens, int wi
 __device__ __forceinline__ int cap_of(const KvView& kv) {
   return int(min((long long)kv.table_stride << kv.page_shift, (long long)INT_MAX - kKeys));
 }
-__device__ __forceinline__ long long head_tiles(const Req& r, int tokens, int window, int cap) {
-  long long w = 0;
+__device__ __forceinline__ int head_tiles(const Req& r, int tokens, int window, int cap) {
+  int w = 0;
   for (int rt = 0; rt * tokens < r.n; ++rt) w += span_of(r, rt, tokens, window, cap).nt;
   return w;
 }
@@ -146,9 +146,8 @@ struct Walk {
   __device__ __forceinline__ void start(const Args& a, int cap, int b_, int off, int count) {
     b = b_;
     r = load_req(a.kv, b);
-    const int per = int(head_tiles(r, a.tokens, a.window, cap));
-    h = off / per;
-    off -= h * per;
+    const int per = head_tiles(r, a.tokens, a.window, cap);
+    for (h = 0; off >= per; ++h) off -= per;
     for (rt = 0;; ++rt) {
       const int nt = span_of(r, rt, a.tokens, a.window, cap).nt;
       if (off < nt) break;
@@ -317,14 +316,16 @@ __device__ __forceinline__ uint64_t desc(uint32_t start, uint32_t lbo, uint32_t 
 }
 
 struct Misc {
-  uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree, drain;
+  uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
   int b, off;  // the run's first request, its first tile in it
-  long long scan[32];
-  float m[128], alpha[128];
+  int scan[32];
+  alignas(16) float m[128];  // of the rows, log2 units
+  alignas(16) float alpha[128];
+  float inv[128];            // 1 / sum of a finished piece's rows
   float red[4][128];
-  int page[2][kKeys];  // pages of a tile's boxes
+  int page[2][kKeys];        // pages of a tile's boxes, for keys and for values
   int nbad;
   uint8_t bad[kKeys];  // keys of a tile with values that are not finite
 };
@@ -372,8 +373,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   uint8_t* raw = sp + 2 * C::PBYTES;
   Misc& ms = *reinterpret_cast<Misc*>(raw + C::NRAW * C::RAW);
   volatile int* fail = &ms.fail;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kMmaWarp = C::SW, kLoadWarp = C::SW + 1, kSoft = 32 * C::SW;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  constexpr int kMmaWarp = C::SW, kLoadWarp = C::SW + 1, kSoft = 32 * C::SW;  // loads: keys, then values
 
   pdl_trigger();
   if (warp == kMmaWarp) {
@@ -382,12 +383,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   } else if (tid == 32 * kLoadWarp) {
     for (int i = 0; i < C::NS; ++i) {
-      bar_init(&ms.full[i], E4M3 ? C::VW : 1);
+      bar_init(&ms.full[i], E4M3 ? 4 : 1);
       bar_init(&ms.empty[i], 1);
     }
     for (int i = 0; i < C::NRAW; ++i) {
       bar_init(&ms.rfull[i], 1);
-      bar_init(&ms.rempty[i], C::VW);
+      bar_init(&ms.rempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&ms.qfull[i], 1);
@@ -395,8 +396,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       bar_init(&ms.sfull[i], 1);
       bar_init(&ms.pfull[i], C::SW);
       bar_init(&ms.pvdone[i], 1);
+      bar_init(&ms.ofree[i], C::SW);
     }
-    bar_init(&ms.ofree, C::SW);
     bar_init(&ms.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ms.fail = 0;
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   // ---- the run: all tiles of the call cut into equal parts
   const int cap = cap_of(a.kv);
   const int B = a.kv.B, per = (B + C::THREADS - 1) / C::THREADS;
-  long long mine = 0;
+  int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b < B) {
@@ -416,38 +417,32 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       mine += a.kv.Hkv * head_tiles(r, a.tokens, a.window, cap);
     }
   }
-  long long incl = mine;
+  int before = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, x);
-    if (lane >= x) incl += y;
+    const int y = __shfl_up_sync(0xffffffffu, before, x);
+    if (lane >= x) before += y;
   }
-  if (lane == 31) ms.scan[warp] = incl;
+  if (lane == 31) ms.scan[warp] = before;
+  before -= mine;
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t taddr = ms.taddr;
-  long long all = 0, before = incl - mine;
-#pragma unroll 4
-  for (int w = 0; w < C::THREADS / 32; ++w) {
-    const long long v = ms.scan[w];
-    if (w < warp) before += v;
-    all += v;
-  }
-  const int run = blockIdx.x;
-  const int total = all < INT_MAX ? int(all) : 0;  // more tiles than that are refused
-  const int runs = min(int(gridDim.x), total);     // no run is empty
+  const int sum = lane < C::THREADS / 32 ? ms.scan[lane] : 0;
+  before += __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
+  const int run = blockIdx.x, total = __reduce_add_sync(0xffffffffu, sum);
+  const int runs = min(int(gridDim.x), total);  // no run is empty
   const int w0 = run < runs ? cut_at(total, runs, run) : 0;
   const int count = run < runs ? cut_at(total, runs, run + 1) - w0 : 0;
   if (tid == 0) {
     a.head[run].w = 0;
     if (run == 0) *a.total = total;
-    if (run == 0 && all >= INT_MAX) set_error(a.err, MOE_ERANGE);
   }
   if (count > 0 && w0 >= before && w0 < before + mine) {
-    int off = w0 - int(before), b = tid * per;
+    int off = w0 - before, b = tid * per;
     while (per > 1) {
-      const int n = int(a.kv.Hkv * head_tiles(load_req(a.kv, b), a.tokens, a.window, cap));
+      const int n = a.kv.Hkv * head_tiles(load_req(a.kv, b), a.tokens, a.window, cap);
       if (off < n) break;
       off -= n;
       ++b;
@@ -467,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       constexpr uint32_t kIdescS = kBase, kIdescO = kBase | (1u << 15) | (1u << 16);
       Ring<C::NS> rg(0);
       int qn = -1;             // pieces begun, less one
-      int pieces = 0;          // pieces whose O has been begun
+      int pieces = -1;         // pieces whose O has been begun, less one
       bool first_prev = false;
       for (int n = 0; n <= count; ++n) {
         bool first = false;
@@ -484,45 +479,40 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
           for (int hh = 0; hh < C::H; ++hh) {
             wait(&ms.full[rg.slot], rg.phase, fail);
             tc_after();
-            if (!*fail) {
-              const uint64_t kd = desc(su32(ring + rg.slot * C::SLOT), 16, 1024, 2);
+            const uint64_t kd = desc(su32(ring + rg.slot * C::SLOT), 16, 1024, 2);
 #pragma unroll
-              for (int k = 0; k < C::DS / 64; ++k)
-                mma4<2, 2>(d, kd + k * (kKeys * 128 >> 4), qd + (hh * (C::DS / 64) + k) * (NR * 128 >> 4), kIdescS,
-                           hh + k > 0);
-              commit_to(&ms.empty[rg.slot]);
-            }
+            for (int k = 0; k < C::DS / 64; ++k)
+              mma4<2, 2>(d, kd + k * (kKeys * 128 >> 4), qd + (hh * (C::DS / 64) + k) * (NR * 128 >> 4), kIdescS,
+                         hh + k > 0);
+            commit_to(&ms.empty[rg.slot]);
             rg.next();
           }
-          if (!*fail) {
-            commit_to(&ms.sfull[n & 1]);
-            if (w.j + 1 == w.jend) commit_to(&ms.qfree[qn % C::QB]);
-          }
+          commit_to(&ms.sfull[n & 1]);
+          if (w.j + 1 == w.jend) commit_to(&ms.qfree[qn % C::QB]);
         }
         if (n > 0) {
           // O^T += V(n-1)^T P(n-1)^T
           const int p = (n - 1) & 1;
           wait(&ms.pfull[p], ((n - 1) >> 1) & 1, fail);
           if (first_prev) {
-            if (pieces > 0) wait(&ms.ofree, (pieces - 1) & 1, fail);
             ++pieces;
+            if (pieces >= 2) wait(&ms.ofree[pieces & 1], ((pieces >> 1) - 1) & 1, fail);
           }
+          const uint32_t od = taddr + uint32_t(2 + (pieces & 1) * C::H) * NR;
           const uint64_t pd = desc(su32(sp + p * C::PBYTES), 128, 2048, 0);
 #pragma unroll
           for (int hh = 0; hh < C::H; ++hh) {
             wait(&ms.full[rg.slot], rg.phase, fail);
             tc_after();
-            if (!*fail) {
-              // D = 64: the upper 64 rows of M read the same columns again and are not used
-              const uint64_t vd = desc(su32(ring + rg.slot * C::SLOT), D < 128 ? 0 : kKeys * 128, 1024, 2);
+            // D = 64: the upper 64 rows of M read the same columns again and are not used
+            const uint64_t vd = desc(su32(ring + rg.slot * C::SLOT), D < 128 ? 0 : kKeys * 128, 1024, 2);
 #pragma unroll
-              for (int k = 0; k < kKeys / 64; ++k)
-                mma4<128, 16>(taddr + uint32_t(2 + hh) * NR, vd + k * 512, pd + k * 64, kIdescO, !first_prev || k > 0);
-              commit_to(&ms.empty[rg.slot]);
-            }
+            for (int k = 0; k < kKeys / 64; ++k)
+              mma4<128, 16>(od + uint32_t(hh) * NR, vd + k * 512, pd + k * 64, kIdescO, !first_prev || k > 0);
+            commit_to(&ms.empty[rg.slot]);
             rg.next();
           }
-          if (!*fail) commit_to(&ms.pvdone[p]);
+          commit_to(&ms.pvdone[p]);
         }
         first_prev = first;
         if (n + 1 < count) w.next(a, cap);
@@ -535,34 +525,63 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
             : "=r"(ok)
             : "r"(su32(&ms.drain))
             : "memory");
-    } else if (warp == kLoadWarp) {
+    } else if (warp == kLoadWarp || warp == kLoadWarp + 1) {
       // -------------------------------------------------------- loads
+      // In the ring, as the products take them: K(0) K(1) V(0) K(2) V(1) .. K(last) V(last - 1) V(last).
+      const bool keys = warp == kLoadWarp;
       const KvView& kv = a.kv;
       const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
+      const CUtensorMap* tm = keys ? &a.mk : &a.mv;
+      int* page = ms.page[keys ? 0 : 1];
       // pages of a tile's boxes: up to four a lane
-      auto pages_of = [&](const Walk& k, int id[4]) {
-        const int32_t* row = kv.page_table + (long long)k.b * kv.table_stride;
+      int id[4];
+      auto find = [&]() {
+        const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int x = lane + 32 * i, key = (k.s.tile0 + k.j) * kKeys + (x << box_shift);
+          const int x = lane + 32 * i, key = (w.s.tile0 + w.j) * kKeys + (x << box_shift);
           id[i] = -2;
-          if (x < boxes && key < k.s.hi && key + (1 << box_shift) > k.s.lo) id[i] = row[key >> kv.page_shift];
+          if (x < boxes && key < w.s.hi && key + (1 << box_shift) > w.s.lo) id[i] = row[key >> kv.page_shift];
         }
       };
-      auto put_pages = [&](const int id[4], int* out) {
+      Ring<E4M3 ? C::NRAW : C::NS> rg(1);  // a fresh slot is empty
+      auto skip = [&]() {
+#pragma unroll
+        for (int hh = 0; hh < C::H; ++hh) rg.next();
+      };
+      int qn = -1;
+      find();
+      if (!keys) {
+        skip();
+        if (count > 1) skip();
+      }
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        if (keys && w.j == w.jbeg) {
+          ++qn;
+          if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
+          if (lane == 0 && !*fail) {
+            uint64_t* b = &ms.qfull[qn % C::QB];
+            expect(b, uint32_t(a.tokens * a.G * D * 2));
+            for (int c = 0; c < D / 64; ++c)
+              load_rows(sq + (qn % C::QB) * C::QBYTES + c * (NR * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0, b);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int x = lane + 32 * i;
           if (x < boxes) {
             const bool ok = id[i] >= 0 && id[i] < kv.npages;
             if (!ok && id[i] != -2) set_error(a.err, MOE_ERANGE);
-            out[x] = ok ? id[i] : kv.npages;  // past the end: zeros
+            page[x] = ok ? id[i] : kv.npages;  // past the end: zeros
           }
         }
-      };
-      Ring<E4M3 ? C::NRAW : C::NS> rg(1);  // a fresh slot is empty
-      auto load = [&](const CUtensorMap* tm, const int* page, int h, int key0) {
-        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
+        __syncwarp();
+        const int h = w.h, tok = ((w.s.tile0 + w.j) * kKeys) & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
+        if (n + 1 < count) {
+          w.next(a, cap);
+          find();  // on their way while this tile is asked for
+        }
 #pragma unroll 1
         for (int hh = 0; hh < C::H; ++hh) {
           uint64_t* full = E4M3 ? &ms.rfull[rg.slot] : &ms.full[rg.slot];
@@ -578,48 +597,26 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
                                 : ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
             load_box(dst, tm, hh * C::DS + c * 64, tok, h, page[p], full);
           }
+          __syncwarp();
           rg.next();
         }
-      };
-      int qn = -1, id[4], hv = 0, key0v = 0;
-      pages_of(w, id);
-      for (int n = 0; n <= count; ++n) {
-        if (n < count) {
-          if (w.j == w.jbeg) {
-            ++qn;
-            if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
-            if (lane == 0 && !*fail) {
-              uint64_t* b = &ms.qfull[qn % C::QB];
-              expect(b, uint32_t(a.tokens * a.G * D * 2));
-              for (int c = 0; c < D / 64; ++c)
-                load_rows(sq + (qn % C::QB) * C::QBYTES + c * (NR * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0, b);
-            }
-            __syncwarp();
-          }
-          put_pages(id, ms.page[n & 1]);
-          __syncwarp();
-        }
-        const int h = w.h, key0 = (w.s.tile0 + w.j) * kKeys;
-        const bool more = n + 1 < count;
-        if (more) {
-          w.next(a, cap);
-          pages_of(w, id);  // on their way while this tile is asked for
-        }
-        if (n < count) load(&a.mk, ms.page[n & 1], h, key0);
-        if (n > 0) load(&a.mv, ms.page[(n - 1) & 1], hv, key0v);
-        hv = h;
-        key0v = key0;
-        __syncwarp();
+        if (keys ? n > 0 : n + 2 != count) skip();
       }
-    } else if (warp > kLoadWarp) {
+    } else if (warp > kLoadWarp + 1) {
       // -------------------------------------------------------- E4M3 codes -> bf16
       if constexpr (E4M3) {
-        const int vt = tid - 32 * (kLoadWarp + 1);
-        constexpr int CH = C::DS / 8, STEP = 32 * C::VW / CH;  // 8 codes a thread make one 16-byte piece
+        const int group = (warp - kLoadWarp - 2) >> 2, vt = tid & 127;
+        static_assert((C::SW + 3) % 4 == 3, "the groups' threads");
+        constexpr int CH = C::DS / 8, STEP = 128 / CH;  // 8 codes a thread make one 16-byte piece
         const int r0 = vt / CH, c = vt % CH;
         Ring<C::NRAW> in(0);
         Ring<C::NS> out(1);
-        for (long long x = 0; x < 2ll * C::H * count; ++x) {
+        if (group) {
+          in.next();
+          out.next();
+        }
+#pragma unroll 1
+        for (int x = group; x < 2 * C::H * count; x += C::VG) {  // the groups take turns
           wait(&ms.rfull[in.slot], in.phase, fail);
           wait(&ms.empty[out.slot], out.phase, fail);
           const uint8_t* src = raw + in.slot * C::RAW + c * 8;
@@ -637,256 +634,290 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
             arrive(&ms.full[out.slot]);
             arrive(&ms.rempty[in.slot]);
           }
-          in.next();
-          out.next();
+#pragma unroll
+          for (int g = 0; g < C::VG; ++g) {
+            in.next();
+            out.next();
+          }
         }
       }
     } else {
       // -------------------------------------------------------- softmax
-      constexpr int CW = C::CW, CK = CW == 16 || (E4M3 && NR > 32) ? 16 : 32;  // rows of a warp, and at a time
+      constexpr int CW = C::CW, CK = CW == 16 || E4M3 ? 16 : 32;  // rows of a warp, and at a time
       const int quad = warp & 3, c0 = (warp >> 2) * CW;
       const int krow = quad * 32 + lane;  // this thread's key in a tile, and its column of v
       const uint32_t tl = taddr + (uint32_t(quad * 32) << 16);
       float l[CW];
       float factor = 0.f;  // of the scores, in log2 units
-      for (int n = 0; n < count; ++n) {
-        const bool first = w.j == w.jbeg;
-        if (first) {
-#pragma unroll
-          for (int i = 0; i < CW; ++i) l[i] = 0.f;
-          factor = a.scale * 1.4426950408889634f * (E4M3 && a.kv.k_scale ? a.kv.k_scale[w.h] : 1.f);
-        }
+      // a finished piece whose O is still to be written
+      int piece = -1, d_token = 0, d_head = 0, d_rows = 0, d_part = -1;
+      bool pending = false;
+#pragma unroll 1
+      for (int n = 0; n <= count; ++n) {
         const int p = n & 1;
         const uint32_t ph = (n >> 1) & 1;
-        const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
-        // every row of the tile sees every key of it
-        const bool whole = key0 + kKeys <= min(w.r.pos0 + w.s.i0 + 1, cap) &&
-                           (a.window <= 0 || key0 > w.r.pos0 + w.s.i1 - a.window);
-        // rows x .. x + CK - 1: scores in log2 units, hidden ones -inf
-        auto scores = [&](int x0, float* s) {
+        if (n < count) {
+          const bool first = w.j == w.jbeg;
+          if (first) {
+            ++piece;
 #pragma unroll
-          for (int i = 0; i < CK; i += 16) ld16(tl + p * NR + c0 + x0 + i, s + i);
-          ld_wait();
-#pragma unroll
-          for (int x = 0; x < CK; ++x) s[x] *= factor;
-          if (!whole) {
-            // rows are in order of their tokens: those from `from` on and before `to` see this key
-            const int t_from = max(key - w.r.pos0, 0) - w.s.i0;
-            const int from = key >= cap ? INT_MAX : t_from > a.tokens ? INT_MAX : t_from * a.G;
-            const int t_to = a.window > 0 ? key - w.r.pos0 + a.window - w.s.i0 : a.tokens;
-            const int to = t_to >= a.tokens ? INT_MAX : t_to * a.G;
-#pragma unroll
-            for (int x = 0; x < CK; ++x)
-              if (c0 + x0 + x < from || c0 + x0 + x >= to) s[x] = -INFINITY;
+            for (int i = 0; i < CW; ++i) l[i] = 0.f;
+            factor = a.scale * 1.4426950408889634f * (E4M3 && a.kv.k_scale ? a.kv.k_scale[w.h] : 1.f);
           }
-        };
-        wait(&ms.sfull[p], ph, fail);
-        tc_after();
-        float s[CK];
-        bool set = first;
-        if (!first) {
-          float over = -INFINITY;
+          const uint32_t to = tl + uint32_t(2 + (piece & 1) * C::H) * NR;  // O of this piece
+          const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
+          const int newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;  // the row tile's tokens
+          // every row of the tile sees every key of it
+          const bool whole = key0 + kKeys <= min(oldest + 1, cap) && (a.window <= 0 || key0 > newest - a.window);
+          // rows x0 .. x0 + CK - 1: scores in log2 units, less m where asked; hidden ones -inf
+          auto scores = [&](int x0, float* s, bool less_m) {
 #pragma unroll
-          for (int x0 = 0; x0 < CW; x0 += CK) {
-            scores(x0, s);
+            for (int i = 0; i < CK; i += 16) ld16(tl + p * NR + c0 + x0 + i, s + i);
+            ld_wait();
 #pragma unroll
-            for (int x = 0; x < CK; ++x) over = fmaxf(over, s[x] - ms.m[c0 + x0 + x]);
-          }
-          set = vote_any<kSoft>(over > kGrow);
-        }
-        if (set) {
-          // set m: the rows' maxima over the 128 keys
-#pragma unroll
-          for (int x0 = 0; x0 < CW; x0 += CK) {
-            scores(x0, s);
-#pragma unroll
-            for (int x = 0; x < CK; ++x) {
-              const float v = warp_max(s[x]);
-              if (lane == (x & 31)) ms.red[quad][c0 + x0 + x] = v;
+            for (int x = 0; x < CK; x += 4) {
+              float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (less_m) m = *reinterpret_cast<const float4*>(&ms.m[c0 + x0 + x]);
+              s[x] = fmaf(s[x], factor, -m.x);
+              s[x + 1] = fmaf(s[x + 1], factor, -m.y);
+              s[x + 2] = fmaf(s[x + 2], factor, -m.z);
+              s[x + 3] = fmaf(s[x + 3], factor, -m.w);
             }
-          }
-          softmax_sync<kSoft>();
-          if (tid < NR) {
-            const float old = first ? kUnset : ms.m[tid];
-            const float v = fmaxf(fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid])), old);
-            ms.m[tid] = v;
-            ms.alpha[tid] = ex2(old - v);
-          }
-          softmax_sync<kSoft>();
+            if (!whole) {
+              // rows are in the order of their tokens: rows from .. to - 1 see this key
+              const int i_from = max(key - oldest, 0), i_to = a.window > 0 ? key - oldest + a.window : a.tokens;
+              const int from = key >= cap || i_from > a.tokens ? INT_MAX : i_from * a.G;
+              const int to_row = i_to >= a.tokens ? INT_MAX : i_to * a.G;
+#pragma unroll
+              for (int x = 0; x < CK; ++x)
+                if (c0 + x0 + x < from || c0 + x0 + x >= to_row) s[x] = -INFINITY;
+            }
+          };
+          wait(&ms.sfull[p], ph, fail);
+          tc_after();
+          float s[CK];
+          bool set = first;
           if (!first) {
+            float over = -INFINITY;
 #pragma unroll
-            for (int x = 0; x < CW; ++x) l[x] *= ms.alpha[c0 + x];
-            wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
-            tc_after();
-#pragma unroll 1
-            for (int x = 0; x < C::H * CW; x += 16) {
-              const int hh = x / CW, y0 = x % CW;
-              float o[16];
-              ld16(tl + (2 + hh) * NR + c0 + y0, o);
-              ld_wait();
+            for (int x0 = 0; x0 < CW; x0 += CK) {
+              scores(x0, s, true);
 #pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] *= ms.alpha[c0 + y0 + y];
-              st16(tl + (2 + hh) * NR + c0 + y0, o);
+              for (int x = 0; x < CK; ++x) over = fmaxf(over, s[x]);
             }
-            st_wait();
+            set = vote_any<kSoft>(over > kGrow);
           }
-        }
-        if (n >= 2) wait(&ms.pvdone[p], ((n - 2) >> 1) & 1, fail);  // P(n - 2) has been read
-        uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
+          if (set) {
+            // set m: the rows' maxima over the 128 keys
 #pragma unroll
-        for (int x0 = 0; x0 < CW; x0 += CK) {
-          if (CW > CK) scores(x0, s);
+            for (int x0 = 0; x0 < CW; x0 += CK) {
+              scores(x0, s, false);
 #pragma unroll
-          for (int x = 0; x < CK; x += 8) {
-            uint32_t u[4];
-#pragma unroll
-            for (int y = 0; y < 8; y += 2) {
-              const float e0 = ex2(s[x + y] - ms.m[c0 + x0 + x + y]);
-              const float e1 = ex2(s[x + y + 1] - ms.m[c0 + x0 + x + y + 1]);
-              l[x0 + x + y] += e0;
-              l[x0 + x + y + 1] += e1;
-              u[y / 2] = pack2(e0, e1);
+              for (int x = 0; x < CK; ++x) {
+                const float v = warp_max(s[x]);
+                if (lane == x) ms.red[quad][c0 + x0 + x] = v;
+              }
             }
-            *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
-        // Values at hidden keys may hold anything, and 0 times what is not finite is NaN.  Those that
-        // no row sees become zeros; where rows differ in what they see, values that are not finite
-        // are taken out of the tile and added to the rows that do see them.
-        bool spoiled = false;
-        if (!whole) {
-          const bool gone = key < w.s.lo || key >= w.s.hi, mixed = w.s.i1 > w.s.i0;
-          const int at = (n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
-          bool bad = false;
+            softmax_sync<kSoft>();
+            if (tid < NR) {
+              const float old = first ? kUnset : ms.m[tid];
+              const float v = fmaxf(fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid])), old);
+              ms.m[tid] = v;
+              ms.alpha[tid] = ex2(old - v);
+            }
+            softmax_sync<kSoft>();
+            if (!first) {
+#pragma unroll
+              for (int x = 0; x < CW; ++x) l[x] *= ms.alpha[c0 + x];
+              wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
+              tc_after();
 #pragma unroll 1
-          for (int hh = 0; hh < C::H; ++hh) {
-            const int slot = (at + hh) % C::NS;
-            wait(&ms.full[slot], uint32_t((at + hh) / C::NS) & 1, fail);
-            uint8_t* row = ring + slot * C::SLOT;
-            if (c0 == 0 && (gone || mixed)) {
+              for (int x = 0; x < C::H * CW; x += 16) {
+                const int hh = x / CW, y0 = x % CW;
+                float o[16];
+                ld16(to + hh * NR + c0 + y0, o);
+                ld_wait();
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[y] *= ms.alpha[c0 + y0 + y];
+                st16(to + hh * NR + c0 + y0, o);
+              }
+              st_wait();
+            }
+          }
+          if (n >= 2) wait(&ms.pvdone[p], ((n - 2) >> 1) & 1, fail);  // P(n - 2) has been read
+          uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
+#pragma unroll
+          for (int x0 = 0; x0 < CW; x0 += CK) {
+            if (CW > CK || set) scores(x0, s, true);
+#pragma unroll
+            for (int x = 0; x < CK; x += 8) {
+              uint32_t u[4];
+#pragma unroll
+              for (int y = 0; y < 8; y += 2) {
+                const float e0 = ex2(s[x + y]), e1 = ex2(s[x + y + 1]);
+                l[x0 + x + y] += e0;
+                l[x0 + x + y + 1] += e1;
+                u[y / 2] = pack2(e0, e1);
+              }
+              *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+          // Values at hidden keys may hold anything, and 0 times what is not finite is NaN.  Those that
+          // no row sees become zeros; where some rows see a key and some do not, values that are not
+          // finite are taken out of the tile and added to the rows that do see them.
+          bool spoiled = false;
+          if (!whole) {
+            const bool gone = key < w.s.lo || key >= w.s.hi, mixed = w.s.i1 > w.s.i0;
+            const bool some = !gone && mixed && (key > oldest || (a.window > 0 && key <= newest - a.window));
+            const int at = (n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
+            bool bad = false;
+#pragma unroll 1
+            for (int hh = 0; hh < C::H; ++hh) {
+              const int slot = (at + hh) % C::NS;
+              wait(&ms.full[slot], uint32_t((at + hh) / C::NS) & 1, fail);
+              if (c0 > 0 || !(gone || some)) continue;
+              uint8_t* row = ring + slot * C::SLOT;
+              __nv_bfloat162 nan2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 4
               for (int c = 0; c < C::DS / 8; ++c) {
                 uint4* v = reinterpret_cast<uint4*>(row + (c / 8) * (kKeys * 128) + sw128(krow, c % 8));
-                uint32_t x[4] = {0, 0, 0, 0};
-                bool here = gone;
-                if (!gone) {
-                  x[0] = v->x, x[1] = v->y, x[2] = v->z, x[3] = v->w;
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    if ((x[i] & 0x7f80u) == 0x7f80u) x[i] &= 0xffff0000u, here = true;
-                    if ((x[i] & 0x7f800000u) == 0x7f800000u) x[i] &= 0xffffu, here = true;
-                  }
-                  bad |= here;
+                if (gone) {
+                  *v = make_uint4(0, 0, 0, 0);
+                } else {
+                  const uint4 x = *v;
+                  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, nan2);
+                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, nan2);
+                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, nan2);
+                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, nan2);
                 }
-                if (here) *v = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+              if (__hisnan(nan2.x) || __hisnan(nan2.y)) {
+                bad = true;
+#pragma unroll 1
+                for (int c = 0; c < C::DS; ++c) {
+                  uint16_t* v = reinterpret_cast<uint16_t*>(row + (c / 64) * (kKeys * 128) + sw128(krow, c % 64 / 8)) + c % 8;
+                  if ((*v & 0x7f80u) == 0x7f80u) *v = 0;
+                }
               }
             }
-          }
-          if (mixed) {
-            if (bad) ms.bad[atomicAdd(&ms.nbad, 1)] = uint8_t(krow);
-            spoiled = vote_any<kSoft>(bad);
-          }
-        }
-        proxy_fence();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) arrive(&ms.pfull[p]);
-        if (spoiled) {
-          wait(&ms.pvdone[p], ph, fail);
-          tc_after();
-          const int nbad = *const_cast<volatile int*>(&ms.nbad);
-#pragma unroll 1
-          for (int e = 0; e < nbad * C::H; ++e) {
-            const int k = key0 + ms.bad[e / C::H], hh = e % C::H, col = hh * 128 + krow;
-            const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (k >> a.kv.page_shift)];
-            const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
-                               (long long)(k & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
-            float add = 0.f;
-            if (col < D) {
-              if (E4M3) add = f16x2_to_f32x2(e4m3x2_to_f16x2(v[col])).x;
-              else add = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[col]);
-            }
-            if (isfinite(add)) add = 0.f;
-#pragma unroll 1
-            for (int x = 0; x < CW; x += 16) {
-              float o[16];
-              ld16(tl + (2 + hh) * NR + c0 + x, o);
-              ld_wait();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) {
-                const int pos = w.r.pos0 + w.s.i0 + (c0 + x + y) / a.G;
-                if (k <= pos && (a.window <= 0 || k > pos - a.window)) o[y] += add;
-              }
-              st16(tl + (2 + hh) * NR + c0 + x, o);
+            if (mixed) {
+              if (bad) ms.bad[atomicAdd(&ms.nbad, 1)] = uint8_t(krow);
+              spoiled = vote_any<kSoft>(bad);
             }
           }
-          st_wait();
+          proxy_fence();
           tc_before();
-          softmax_sync<kSoft>();
-          if (tid == 0) ms.nbad = 0;
+          __syncwarp();
+          if (lane == 0) arrive(&ms.pfull[p]);
+          if (spoiled) {
+            wait(&ms.pvdone[p], ph, fail);
+            tc_after();
+            const int nbad = *const_cast<volatile int*>(&ms.nbad);
+#pragma unroll 1
+            for (int e = 0; e < nbad * C::H; ++e) {
+              const int k = key0 + ms.bad[e / C::H], hh = e % C::H, col = hh * 128 + krow;
+              const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (k >> a.kv.page_shift)];
+              const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
+                                 (long long)(k & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
+              float add = 0.f;
+              if (col < D) {
+                if (E4M3) add = f16x2_to_f32x2(e4m3x2_to_f16x2(v[col])).x;
+                else add = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[col]);
+              }
+              if (isfinite(add)) add = 0.f;
+#pragma unroll 1
+              for (int x = 0; x < CW; x += 16) {
+                float o[16];
+                ld16(to + hh * NR + c0 + x, o);
+                ld_wait();
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                  const int pos = oldest + (c0 + x + y) / a.G;
+                  if (k <= pos && (a.window <= 0 || k > pos - a.window)) o[y] += add;
+                }
+                st16(to + hh * NR + c0 + x, o);
+              }
+            }
+            st_wait();
+            tc_before();
+            softmax_sync<kSoft>();
+            if (tid == 0) ms.nbad = 0;
+          }
         }
-
-        if (w.j + 1 == w.jend) {
-          // ---- the piece is done: its rows' sums, then O
-#pragma unroll
-          for (int x = 0; x < CW; x += 16) {
-            float v[16];
-#pragma unroll
-            for (int y = 0; y < 16; ++y) v[y] = l[x + y];
-            float t = transpose_sum<16>(v, lane);
-            t += __shfl_xor_sync(0xffffffffu, t, 16);
-            if (lane < 16) ms.red[quad][c0 + x + lane] = t;
-          }
-          softmax_sync<kSoft>();
-          const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
-          const int rows = (w.s.i1 - w.s.i0 + 1) * a.G;
-          const long long part = 2ll * run + (head ? 0 : 1);
-          if (tid < NR) {
-            const float t = ms.red[0][tid] + ms.red[1][tid] + ms.red[2][tid] + ms.red[3][tid];
-            const float vs = E4M3 && a.kv.v_scale ? a.kv.v_scale[w.h] : 1.f;
-            if (split && tid < rows) reinterpret_cast<float2*>(a.ml)[part * NR + tid] = make_float2(ms.m[tid], t);
-            ms.alpha[tid] = t == 0.f ? 0.f : vs / t;
-          }
-          if (split && head && tid == 0) {
-            a.head[run] = make_int4(w.b, w.h, w.rt, 1);
-            a.cut[run] = make_int2(w0 - w.jbeg, w0 - w.jbeg + w.s.nt);
-          }
-          softmax_sync<kSoft>();
-          wait(&ms.pvdone[p], ph, fail);
+        if (pending) {
+          // ---- O of the piece that ended with tile n - 1: its last product ran beside this tile's softmax
+          wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
           tc_after();
+          const int d_piece = n < count ? piece - 1 : piece;
+          const uint32_t from = tl + uint32_t(2 + (d_piece & 1) * C::H) * NR;
 #pragma unroll 1
           for (int x = 0; x < C::H * CW; x += 16) {
             const int hh = x / CW, row0 = c0 + x % CW, col = hh * 128 + krow;
-            if (row0 >= rows) continue;
+            if (row0 >= d_rows) continue;
             float o[16];
-            ld16(tl + (2 + hh) * NR + row0, o);
+            ld16(from + hh * NR + row0, o);
             ld_wait();
-            if (split) {
-              float* to = a.part + (part * NR + row0) * D + col;
+            if (d_part >= 0) {
+              float* out = a.part + ((long long)d_part * NR + row0) * D + col;
 #pragma unroll
               for (int y = 0; y < 16; ++y)
-                if (row0 + y < rows && col < D) to[y * D] = o[y];
+                if (row0 + y < d_rows && col < D) out[y * D] = o[y];
             } else {
-              int i = row0 / a.G, g = row0 - i * a.G;
-              uint16_t* to = a.o + (long long)(w.r.s0 + w.s.i0 + i) * a.os + (long long)(w.h * a.G + g) * D + col;
+              const int i = row0 / a.G;
+              int g = row0 - i * a.G;
+              uint16_t* out = a.o + (long long)(d_token + i) * a.os + (long long)(d_head * a.G + g) * D + col;
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
                 // a sum of zero is a row that sees no key; its O is zeros
-                if (row0 + y < rows && col < D)
-                  *to = __bfloat16_as_ushort(__float2bfloat16_rn(o[y] * ms.alpha[row0 + y]));
-                to += D;
+                if (row0 + y < d_rows && col < D) *out = __bfloat16_as_ushort(__float2bfloat16_rn(o[y] * ms.inv[row0 + y]));
+                out += D;
                 if (++g == a.G) {
                   g = 0;
-                  to += a.os - (long long)a.G * D;
+                  out += a.os - (long long)a.G * D;
                 }
               }
             }
           }
           tc_before();
-          softmax_sync<kSoft>();  // m, alpha, red and O are free
-          if (lane == 0) arrive(&ms.ofree);
+          __syncwarp();
+          if (lane == 0) arrive(&ms.ofree[d_piece & 1]);
+          pending = false;
         }
-        if (n + 1 < count) w.next(a, cap);
+        if (n < count) {
+          if (w.j + 1 == w.jend) {
+            // ---- the piece is done: its rows' sums
+#pragma unroll
+            for (int x = 0; x < CW; x += 16) {
+              float v[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) v[y] = l[x + y];
+              float t = transpose_sum<16>(v, lane);
+              t += __shfl_xor_sync(0xffffffffu, t, 16);
+              if (lane < 16) ms.red[quad][c0 + x + lane] = t;
+            }
+            softmax_sync<kSoft>();
+            const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
+            d_token = w.r.s0 + w.s.i0;
+            d_head = w.h;
+            d_rows = (w.s.i1 - w.s.i0 + 1) * a.G;
+            d_part = split ? 2 * run + (head ? 0 : 1) : -1;
+            pending = true;
+            if (tid < NR) {
+              const float t = ms.red[0][tid] + ms.red[1][tid] + ms.red[2][tid] + ms.red[3][tid];
+              const float vs = E4M3 && a.kv.v_scale ? a.kv.v_scale[w.h] : 1.f;
+              if (split && tid < d_rows)
+                reinterpret_cast<float2*>(a.ml)[(long long)d_part * NR + tid] = make_float2(ms.m[tid], t);
+              ms.inv[tid] = t == 0.f ? 0.f : vs / t;
+            }
+            if (split && head && tid == 0) {
+              a.head[run] = make_int4(w.b, w.h, w.rt, 1);
+              a.cut[run] = make_int2(w0 - w.jbeg, w0 - w.jbeg + w.s.nt);
+            }
+            softmax_sync<kSoft>();
+          }
+          if (n + 1 < count) w.next(a, cap);
+        }
       }
     }
   }

@@ -129,6 +129,9 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.G = Hq / kv->Hkv;
   a.window = window;
   a.tokens = nr / a.G;
+  // the schedule counts tiles in 31 bits
+  if ((double(T) / a.tokens + b->B) * kv->Hkv * (double(a.kv.table_stride) * kv->page / attn::kKeys + 1) > 2147483000.0)
+    return MOE_EINVAL;
   const int size = kv->e4m3 ? 1 : 2, box = kv->page < attn::kKeys ? kv->page : attn::kKeys;
   // sizes and byte strides of the pools, innermost first; a size of one takes any stride
   const cuuint64_t dims[4] = {cuuint64_t(kv->D), cuuint64_t(kv->page), cuuint64_t(kv->Hkv), cuuint64_t(kv->npages)};
