@@ -28,11 +28,12 @@
 // are not there are asked for past the pool's end and read as zeros.  E4M3
 // tiles land as they are and are turned into bf16 by four warps of their own.
 //
-// Split.  Every (request, key head, row tile) is a unit of tiles; all tiles of
-// a call are laid end to end and cut into equal runs, one per SM, whatever the
-// lengths.  A run takes its units in pieces; a piece that is not its whole unit
-// leaves (m, sum, O) in the scratch, and a second kernel joins the pieces of a
-// unit in their order.
+// Split.  Every (request, key head, row tile) is a unit: its tiles, and before
+// them a cost for its beginning and end (new queries, a maximum from scratch, an
+// output) counted in tiles.  All units of a call are laid end to end and cut
+// into equal runs, one per SM, whatever the lengths.  A run takes its units in
+// pieces; a piece that is not its whole unit leaves (m, sum, O) in the scratch,
+// and a second kernel joins the pieces of a unit in their order.
 #pragma once
 
 #include <cuda.h>
@@ -48,7 +49,7 @@ constexpr float kUnset = -1e30f;              // m of a row that has seen no key
 constexpr float kGrow = 8.0f;                 // m is set again when a score passes it by this (log2)
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr int kSmem = 232448;
-constexpr int kMisc = 5632;                   // barriers, row statistics, schedule
+constexpr int kMisc = 5888;                   // barriers, row statistics, schedule
 
 struct Args {
   CUtensorMap mk, mv, mq;  // pools [page][head][place][column], query rows [token][head][column]
@@ -60,9 +61,7 @@ struct Args {
   int32_t* err;
   float* part;  // [2 * CTAs][NR][D] pieces: head piece of CTA c at 2c, tail piece at 2c + 1
   float* ml;    // [2 * CTAs][NR][2] their m and sums
-  int4* head;   // [CTAs] head piece: request, key head, row tile; w = 1 when it starts inside its unit
-  int2* cut;    // [CTAs] that unit's tiles, first and last + 1, in the call's order of tiles
-  int* total;   // [1] tiles of the call
+  int4* join;   // [CTAs] where run c's first piece is the second of a unit: token, key head, rows, pieces (else 0)
 };
 
 template <int D, int NR, bool E4M3>
@@ -86,6 +85,9 @@ struct Cfg {
   static constexpr int THREADS = 32 * (SW + 3 + 4 * VG);
   static constexpr int COLS0 = (2 + 2 * H) * NR;                // two S, two O
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
+  // what a unit costs beside its tiles, in tiles: measured with units of one tile, about 3000 clocks,
+  // where 64 KB of keys and values take 2800 from memory
+  static constexpr int V = SLOT * H * 2 / (E4M3 ? 2 : 1) >= 65536 ? 1 : SLOT * H * 2 / (E4M3 ? 2 : 1) >= 32768 ? 2 : 3;
   static_assert(COLS0 <= 512 && NS >= 3 && (!E4M3 || NRAW >= 3), "resources of an SM");
 };
 
@@ -119,47 +121,55 @@ __device__ __forceinline__ Span span_of(const Req& r, int rt, int tokens, int wi
 __device__ __forceinline__ int cap_of(const KvView& kv) {
   return int(min((long long)kv.table_stride << kv.page_shift, (long long)INT_MAX - kKeys));
 }
-__device__ __forceinline__ int head_tiles(const Req& r, int tokens, int window, int cap) {
-  int w = 0;
-  for (int rt = 0; rt * tokens < r.n; ++rt) w += span_of(r, rt, tokens, window, cap).nt;
+// Tiles of a key head of a request, and its units.
+struct Load {
+  int tiles, units;
+};
+__device__ __forceinline__ Load head_load(const Req& r, int tokens, int window, int cap) {
+  Load w = {0, 0};
+  for (; w.units * tokens < r.n; ++w.units) w.tiles += span_of(r, w.units, tokens, window, cap).nt;
   return w;
 }
-// First tile of run c: `total` tiles in `runs` runs whose lengths differ by one at most.
+// First place of run c: `total` places in `runs` runs whose lengths differ by one at most.
 __device__ __forceinline__ int cut_at(int total, int runs, int c) {
   const int q = total / runs;
   return q * c + min(c, total - q * runs);
 }
+__device__ __forceinline__ int run_of(int total, int runs, int x) {
+  const int q = total / runs, longer = total - q * runs;
+  return x < longer * (q + 1) ? x / (q + 1) : longer + (x - longer * (q + 1)) / q;
+}
 
-// A walk over the tiles of a run: the same in every role.
+// A walk over the tiles of a run: the same in every role.  A unit takes V places before its tiles.
+template <int V>
 struct Walk {
   Req r;
   Span s;
   int b, h, rt, j, jbeg, jend;
-  int left;  // tiles after this one
-  __device__ __forceinline__ void unit(const Args& a, int cap, int from, int count) {
+  int rest;  // places of the run after this unit
+  __device__ __forceinline__ void unit(const Args& a, int cap, int off, int places) {
     s = span_of(r, rt, a.tokens, a.window, cap);
-    jbeg = j = from;
-    jend = min(s.nt, from + count);
-    left = count - 1;
+    jbeg = j = max(off - V, 0);
+    jend = min(max(off + places - V, 0), s.nt);
+    rest = off + places - (s.nt + V);
   }
-  // The run's first tile: tile `off` of request b.
-  __device__ __forceinline__ void start(const Args& a, int cap, int b_, int off, int count) {
+  // The run's first unit, from its place `off` in request b on.  False when the run has no tile.
+  __device__ __forceinline__ void start(const Args& a, int cap, int b_, int off, int places) {
     b = b_;
     r = load_req(a.kv, b);
-    const int per = head_tiles(r, a.tokens, a.window, cap);
-    for (h = 0; off >= per; ++h) off -= per;
+    const Load per = head_load(r, a.tokens, a.window, cap);
+    const int cost = per.tiles + V * per.units;
+    h = off / cost;
+    off -= h * cost;
     for (rt = 0;; ++rt) {
-      const int nt = span_of(r, rt, a.tokens, a.window, cap).nt;
-      if (off < nt) break;
-      off -= nt;
+      const int c = span_of(r, rt, a.tokens, a.window, cap).nt + V;
+      if (off < c) break;
+      off -= c;
     }
-    unit(a, cap, off, count);
+    unit(a, cap, off, places);
   }
-  __device__ __forceinline__ void next(const Args& a, int cap) {  // left > 0
-    if (++j < jend) {
-      --left;
-      return;
-    }
+  __device__ __forceinline__ void next(const Args& a, int cap) {  // a tile follows
+    if (++j < jend) return;
     if ((rt + 1) * a.tokens < r.n) {
       ++rt;
     } else {
@@ -171,9 +181,23 @@ struct Walk {
         } while (r.n == 0);
       }
     }
-    unit(a, cap, 0, left);
+    unit(a, cap, 0, rest);
   }
 };
+// Tiles before place x of a request's units.
+template <int V>
+__device__ __forceinline__ int tiles_before(const Args& a, const Req& r, int cap, int x) {
+  const Load per = head_load(r, a.tokens, a.window, cap);
+  const int cost = per.tiles + V * per.units, h = x / cost;
+  int t = h * per.tiles;
+  x -= h * cost;
+  for (int rt = 0;; ++rt) {
+    const int nt = span_of(r, rt, a.tokens, a.window, cap).nt;
+    if (x < nt + V) return t + max(x - V, 0);
+    x -= nt + V;
+    t += nt;
+  }
+}
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -303,10 +327,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Two E4M3 codes (low byte first) -> bf16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two) {
-  const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(two));
-  return pack2(f.x, f.y);
+// Four E4M3 codes (low byte first) -> bf16, exact.
+__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t four, uint32_t* out) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(four));
+  const float2 a = f16x2_to_f32x2(lo), b = f16x2_to_f32x2(hi);
+  out[0] = pack2(a.x, a.y);
+  out[1] = pack2(b.x, b.y);
 }
 
 // Shared-memory descriptors (start, leading and stride offsets in 16-byte units, version 1).
@@ -319,8 +348,9 @@ struct Misc {
   uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
-  int b, off;  // the run's first request, its first tile in it
-  int scan[32];
+  int b, off;    // the run's first request, its first place in it
+  int tiles[2];  // the call's tiles before the run and before the next one
+  int2 scan[32];
   alignas(16) float m[128];  // of the rows, log2 units
   alignas(16) float alpha[128];
   float inv[128];            // 1 / sum of a finished piece's rows
@@ -405,56 +435,72 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   }
   pdl_wait();
 
-  // ---- the run: all tiles of the call cut into equal parts
+  // ---- the run: all units of the call, end to end, cut into equal parts
+  constexpr int V = C::V;
   const int cap = cap_of(a.kv);
   const int B = a.kv.B, per = (B + C::THREADS - 1) / C::THREADS;
-  int mine = 0;
+  int2 mine = make_int2(0, 0);  // places and tiles of this thread's requests
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b < B) {
       const Req r = load_req(a.kv, b);
       if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
-      mine += a.kv.Hkv * head_tiles(r, a.tokens, a.window, cap);
+      const Load w = head_load(r, a.tokens, a.window, cap);
+      mine.x += a.kv.Hkv * (w.tiles + V * w.units);
+      mine.y += a.kv.Hkv * w.tiles;
     }
   }
-  int before = mine;
+  int2 before = mine;
 #pragma unroll
   for (int x = 1; x < 32; x <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, before, x);
-    if (lane >= x) before += y;
+    const int y0 = __shfl_up_sync(0xffffffffu, before.x, x), y1 = __shfl_up_sync(0xffffffffu, before.y, x);
+    if (lane >= x) {
+      before.x += y0;
+      before.y += y1;
+    }
   }
   if (lane == 31) ms.scan[warp] = before;
-  before -= mine;
+  before.x -= mine.x;
+  before.y -= mine.y;
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t taddr = ms.taddr;
-  const int sum = lane < C::THREADS / 32 ? ms.scan[lane] : 0;
-  before += __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
-  const int run = blockIdx.x, total = __reduce_add_sync(0xffffffffu, sum);
-  const int runs = min(int(gridDim.x), total);  // no run is empty
-  const int w0 = run < runs ? cut_at(total, runs, run) : 0;
-  const int count = run < runs ? cut_at(total, runs, run + 1) - w0 : 0;
-  if (tid == 0) {
-    a.head[run].w = 0;
-    if (run == 0) *a.total = total;
-  }
-  if (count > 0 && w0 >= before && w0 < before + mine) {
-    int off = w0 - before, b = tid * per;
-    while (per > 1) {
-      const int n = a.kv.Hkv * head_tiles(load_req(a.kv, b), a.tokens, a.window, cap);
-      if (off < n) break;
-      off -= n;
-      ++b;
+  const int2 sum = lane < C::THREADS / 32 ? ms.scan[lane] : make_int2(0, 0);
+  before.x += __reduce_add_sync(0xffffffffu, lane < warp ? sum.x : 0);
+  before.y += __reduce_add_sync(0xffffffffu, lane < warp ? sum.y : 0);
+  const int run = blockIdx.x, total = __reduce_add_sync(0xffffffffu, sum.x);
+  const int runs = min(int(gridDim.x), total);
+  const int x0 = run < runs ? cut_at(total, runs, run) : total, x1 = run < runs ? cut_at(total, runs, run + 1) : total;
+  if (mine.x > 0) {  // a cut falls into the requests of one thread
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      int x = (e ? x1 : x0) - before.x, t = before.y, b = tid * per;
+      if (x < 0 || x >= mine.x) continue;
+      Req r = load_req(a.kv, b);
+      while (per > 1) {
+        const Load w = head_load(r, a.tokens, a.window, cap);
+        const int c = a.kv.Hkv * (w.tiles + V * w.units);
+        if (x < c) break;
+        x -= c;
+        t += a.kv.Hkv * w.tiles;
+        r = load_req(a.kv, ++b);
+      }
+      if (e == 0) {
+        ms.b = b;
+        ms.off = x;
+      }
+      ms.tiles[e] = t + tiles_before<V>(a, r, cap, x);
     }
-    ms.b = b;
-    ms.off = off;
   }
+  if (tid == C::THREADS - 1 && x1 == total) ms.tiles[1] = before.y + mine.y;
   __syncthreads();
+  const int count = run < runs ? ms.tiles[1] - ms.tiles[0] : 0;
+  if (count == 0 && tid == 0) a.join[run] = make_int4(0, 0, 0, 0);
 
   if (count > 0) {
-    Walk w;
-    w.start(a, cap, ms.b, ms.off, count);
+    Walk<V> w;
+    w.start(a, cap, ms.b, ms.off, x1 - x0);
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- tensor cores
       // D f32, A and B bf16, N = NR, M = 128; the second product's operands are both MN-major
@@ -621,12 +667,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
           wait(&ms.empty[out.slot], out.phase, fail);
           const uint8_t* src = raw + in.slot * C::RAW + c * 8;
           uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
-#pragma unroll 8
-          for (int r = r0; r < kKeys; r += STEP) {
-            const uint2 v = *reinterpret_cast<const uint2*>(src + r * C::DS);
-            *reinterpret_cast<uint4*>(dst + sw128(r, c % 8)) =
-                make_uint4(e4m3x2_to_bf16x2(v.x & 0xffffu), e4m3x2_to_bf16x2(v.x >> 16),
-                           e4m3x2_to_bf16x2(v.y & 0xffffu), e4m3x2_to_bf16x2(v.y >> 16));
+          uint2 v[kKeys / STEP];
+#pragma unroll
+          for (int i = 0; i < kKeys / STEP; ++i) v[i] = *reinterpret_cast<const uint2*>(src + (r0 + i * STEP) * C::DS);
+#pragma unroll
+          for (int i = 0; i < kKeys / STEP; ++i) {
+            uint32_t o[4];
+            e4m3x4_to_bf16x4(v[i].x, o);
+            e4m3x4_to_bf16x4(v[i].y, o + 2);
+            *reinterpret_cast<uint4*>(dst + sw128(r0 + i * STEP, c % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
           proxy_fence();
           __syncwarp();
@@ -652,6 +701,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       // a finished piece whose O is still to be written
       int piece = -1, d_token = 0, d_head = 0, d_rows = 0, d_part = -1;
       bool pending = false;
+      if (tid == 0) {
+        // the unit's tiles take the places from `at` on; its first piece is the run's that has place `at`
+        int4 j = make_int4(0, 0, 0, 0);
+        const int at = x0 - w.jbeg;
+        if (w.jbeg > 0 && cut_at(total, runs, run - 1) <= at)
+          j = make_int4(w.r.s0 + w.s.i0, w.h, (w.s.i1 - w.s.i0 + 1) * a.G, run_of(total, runs, at + w.s.nt - 1) - run + 2);
+        a.join[run] = j;
+      }
 #pragma unroll 1
       for (int n = 0; n <= count; ++n) {
         const int p = n & 1;
@@ -910,10 +967,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
                 reinterpret_cast<float2*>(a.ml)[(long long)d_part * NR + tid] = make_float2(ms.m[tid], t);
               ms.inv[tid] = t == 0.f ? 0.f : vs / t;
             }
-            if (split && head && tid == 0) {
-              a.head[run] = make_int4(w.b, w.h, w.rt, 1);
-              a.cut[run] = make_int2(w0 - w.jbeg, w0 - w.jbeg + w.s.nt);
-            }
             softmax_sync<kSoft>();
           }
           if (n + 1 < count) w.next(a, cap);
@@ -930,7 +983,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 }
 
 // Joins the pieces of a unit: o = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k, in the order of
-// the pieces.  CTA (c, y): the unit that the cut before run c is the first to fall into, rows y, y + 16, ..
+// the pieces.  CTA (c, y): the unit whose second piece is run c's first, rows y, y + 16, ..
 constexpr int kJoinThreads = 256;
 constexpr int kMaxRuns = 512;
 template <int D, int NR>
@@ -940,16 +993,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
   __shared__ float4 acc[kJoinThreads];
   pdl_trigger();
   pdl_wait();
-  const int total = *a.total;
-  const int runs = min(int(gridDim.x), total), c = blockIdx.x, tid = threadIdx.x;
-  if (c < 1 || c >= runs) return;
-  const int4 hd = a.head[c];
-  const int2 unit = a.cut[c];
-  if (!hd.w || cut_at(total, runs, c - 1) > unit.x) return;
-  const Req r = load_req(a.kv, hd.x);
-  const int i0 = hd.z * a.tokens, rows = min(a.tokens, r.n - i0) * a.G;
-  int np = 1;  // pieces: the tail of run c - 1, then the heads of the runs that begin before the unit's end
-  while (c - 1 + np < runs && cut_at(total, runs, c - 1 + np) < unit.y) ++np;
+  const int c = blockIdx.x, tid = threadIdx.x;
+  const int4 unit = __ldcg(a.join + c);
+  const int rows = unit.z, np = unit.w;  // pieces: the tail of run c - 1, then the heads of np - 1 runs
   auto place = [&](int k) { return 2ll * (c - 1 + k) + (k == 0 ? 1 : 0); };
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     float m = kUnset;
@@ -992,13 +1038,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
         o.z += v.z;
         o.w += v.w;
       }
-      const float vs = a.kv.v_scale ? a.kv.v_scale[hd.y] : 1.f;
+      const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
       const float x = l == 0.f ? 0.f : vs / l;
       const int i = row / a.G, g = row - i * a.G;
       uint2 u;
       u.x = pack2(o.x * x, o.y * x);
       u.y = pack2(o.z * x, o.w * x);
-      *reinterpret_cast<uint2*>(a.o + (long long)(r.s0 + i0 + i) * a.os + (long long)(hd.y * a.G + g) * D + col * 4) = u;
+      *reinterpret_cast<uint2*>(a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D + col * 4) = u;
     }
     __syncthreads();
   }

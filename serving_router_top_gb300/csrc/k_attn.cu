@@ -7,8 +7,7 @@ struct moe_attn_ws {
   int Hq, Hkv, D, ctas;
   int32_t* error;
   float *part, *ml;
-  int4* head;
-  int2* cut;
+  int4* join;
 };
 
 namespace moe {
@@ -67,8 +66,8 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
   }
   w->ctas = sms < attn::kMaxRuns ? sms : attn::kMaxRuns;  // one CTA per SM
   const size_t rows = 2 * size_t(w->ctas) * (D == 256 ? 64 : 128);
-  const size_t o_part = 256, o_ml = o_part + rows * D * 4, o_head = o_ml + rows * 8, o_cut = o_head + size_t(w->ctas) * 16;
-  const size_t bytes = o_cut + size_t(w->ctas) * 8 + 4;
+  const size_t o_part = 256, o_ml = o_part + rows * D * 4, o_join = o_ml + rows * 8;
+  const size_t bytes = o_join + size_t(w->ctas) * 16;
   uint8_t* base = nullptr;
   if (cudaMalloc(&base, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -78,8 +77,7 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
   w->error = reinterpret_cast<int32_t*>(base);
   w->part = reinterpret_cast<float*>(base + o_part);
   w->ml = reinterpret_cast<float*>(base + o_ml);
-  w->head = reinterpret_cast<int4*>(base + o_head);
-  w->cut = reinterpret_cast<int2*>(base + o_cut);
+  w->join = reinterpret_cast<int4*>(base + o_join);
   if (cudaMemset(base, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     moe_attn_ws_destroy(w);
@@ -129,8 +127,8 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.G = Hq / kv->Hkv;
   a.window = window;
   a.tokens = nr / a.G;
-  // the schedule counts tiles in 31 bits
-  if ((double(T) / a.tokens + b->B) * kv->Hkv * (double(a.kv.table_stride) * kv->page / attn::kKeys + 1) > 2147483000.0)
+  // the schedule counts in 31 bits: a unit has at most its request's tiles, and three more places
+  if ((double(T) / a.tokens + b->B) * kv->Hkv * (double(a.kv.table_stride) * kv->page / attn::kKeys + 4) > 2147483000.0)
     return MOE_EINVAL;
   const int size = kv->e4m3 ? 1 : 2, box = kv->page < attn::kKeys ? kv->page : attn::kKeys;
   // sizes and byte strides of the pools, innermost first; a size of one takes any stride
@@ -149,9 +147,7 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.err = ws->error;
   a.part = ws->part;
   a.ml = ws->ml;
-  a.head = ws->head;
-  a.cut = ws->cut;
-  a.total = reinterpret_cast<int*>(ws->cut + ws->ctas);
+  a.join = ws->join;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (kv->D) {
     case 64: return attn::launch_d64(a, kv->e4m3, nr, ws->ctas, s);
