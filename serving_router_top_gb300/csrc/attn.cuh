@@ -14,9 +14,9 @@
 //
 // The running maximum is lazy: m is the exact maximum of a row at the time it
 // was last set, and it is set again, with O and the sums rescaled, only when a
-// score passes m + 8 (in log2 units), so a weight is at most 2^8 and most
-// tiles need one vote instead of a maximum over all threads.  Sums are kept by
-// each thread for its keys and added up once, at the end of a piece.
+// weight passes 2^8: most tiles' weights are computed at once, with one vote
+// after them instead of a maximum over all threads before them.  Sums are kept
+// by each thread for its keys and added up once, at the end of a piece.
 //
 // Roundings.  Scores and sums are fp32.  The operands are bf16: q and a bf16
 // cache as they are, E4M3 codes exactly, and P rounded once, half a unit of
@@ -46,7 +46,8 @@ namespace attn {
 
 constexpr int kKeys = 128;                    // keys in a tile
 constexpr float kUnset = -1e30f;              // m of a row that has seen no key
-constexpr float kGrow = 8.0f;                 // m is set again when a score passes it by this (log2)
+constexpr float kMost = 256.0f;               // m is set again when a weight passes this
+constexpr float kLost = 0x1p-100f;            // sums from before m grew by this factor are nothing to those after
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr int kSmem = 232448;
 constexpr int kMisc = 5888;                   // barriers, row statistics, schedule
@@ -153,20 +154,13 @@ struct Walk {
     jend = min(max(off + places - V, 0), s.nt);
     rest = off + places - (s.nt + V);
   }
-  // The run's first unit, from its place `off` in request b on.  False when the run has no tile.
-  __device__ __forceinline__ void start(const Args& a, int cap, int b_, int off, int places) {
-    b = b_;
+  // The run's first unit, from its place `off` on.
+  __device__ __forceinline__ void start(const Args& a, int cap, int4 first, int places) {
+    b = first.x;
+    h = first.y;
+    rt = first.z;
     r = load_req(a.kv, b);
-    const Load per = head_load(r, a.tokens, a.window, cap);
-    const int cost = per.tiles + V * per.units;
-    h = off / cost;
-    off -= h * cost;
-    for (rt = 0;; ++rt) {
-      const int c = span_of(r, rt, a.tokens, a.window, cap).nt + V;
-      if (off < c) break;
-      off -= c;
-    }
-    unit(a, cap, off, places);
+    unit(a, cap, first.w, places);
   }
   __device__ __forceinline__ void next(const Args& a, int cap) {  // a tile follows
     if (++j < jend) return;
@@ -184,19 +178,22 @@ struct Walk {
     unit(a, cap, 0, rest);
   }
 };
-// Tiles before place x of a request's units.
+// Place x of a request: its key head, row tile and place in their unit, and the request's tiles before it.
 template <int V>
-__device__ __forceinline__ int tiles_before(const Args& a, const Req& r, int cap, int x) {
-  const Load per = head_load(r, a.tokens, a.window, cap);
+__device__ __forceinline__ int find_place(const Args& a, const Req& r, const Load& per, int cap, int x, int4* unit) {
   const int cost = per.tiles + V * per.units, h = x / cost;
-  int t = h * per.tiles;
+  int t = h * per.tiles, rt = 0;
   x -= h * cost;
-  for (int rt = 0;; ++rt) {
+  for (;; ++rt) {
     const int nt = span_of(r, rt, a.tokens, a.window, cap).nt;
-    if (x < nt + V) return t + max(x - V, 0);
+    if (x < nt + V) break;
     x -= nt + V;
     t += nt;
   }
+  unit->y = h;
+  unit->z = rt;
+  unit->w = x;
+  return t + max(x - V, 0);
 }
 
 // ------------------------------------------------------------------ PTX
@@ -308,6 +305,19 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
+// Pairs in one instruction: a = a * f - m, and a += x.
+__device__ __forceinline__ void scale_sub2(float& a0, float& a1, float f, float m0, float m1) {
+  asm("{\n\t.reg .b64 a, f, m;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 m, {%3, %4};\n\t"
+      "fma.rn.f32x2 a, a, f, m;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(f), "f"(-m0), "f"(-m1));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float x0, float x1) {
+  asm("{\n\t.reg .b64 a, x;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, x;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(x0), "f"(x1));
+}
 // True in every softmax thread when it is in any of them.
 template <int N>
 __device__ __forceinline__ bool vote_any(bool p) {
@@ -348,10 +358,10 @@ struct Misc {
   uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
-  int b, off;    // the run's first request, its first place in it
+  int4 first;    // the run's first request, key head and row tile, and its first place in their unit
   int tiles[2];  // the call's tiles before the run and before the next one
   int2 scan[32];
-  alignas(16) float m[128];  // of the rows, log2 units
+  alignas(16) float m[128];      // of the rows, log2 units
   alignas(16) float alpha[128];
   float inv[128];            // 1 / sum of a finished piece's rows
   float red[4][128];
@@ -440,14 +450,16 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   const int cap = cap_of(a.kv);
   const int B = a.kv.B, per = (B + C::THREADS - 1) / C::THREADS;
   int2 mine = make_int2(0, 0);  // places and tiles of this thread's requests
+  Req r = {};
+  Load ld = {};  // the last of them
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b < B) {
-      const Req r = load_req(a.kv, b);
+      r = load_req(a.kv, b);
       if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
-      const Load w = head_load(r, a.tokens, a.window, cap);
-      mine.x += a.kv.Hkv * (w.tiles + V * w.units);
-      mine.y += a.kv.Hkv * w.tiles;
+      ld = head_load(r, a.tokens, a.window, cap);
+      mine.x += a.kv.Hkv * (ld.tiles + V * ld.units);
+      mine.y += a.kv.Hkv * ld.tiles;
     }
   }
   int2 before = mine;
@@ -477,20 +489,17 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
     for (int e = 0; e < 2; ++e) {
       int x = (e ? x1 : x0) - before.x, t = before.y, b = tid * per;
       if (x < 0 || x >= mine.x) continue;
-      Req r = load_req(a.kv, b);
-      while (per > 1) {
-        const Load w = head_load(r, a.tokens, a.window, cap);
-        const int c = a.kv.Hkv * (w.tiles + V * w.units);
+      for (; per > 1; ++b) {
+        r = load_req(a.kv, b);
+        ld = head_load(r, a.tokens, a.window, cap);
+        const int c = a.kv.Hkv * (ld.tiles + V * ld.units);
         if (x < c) break;
         x -= c;
-        t += a.kv.Hkv * w.tiles;
-        r = load_req(a.kv, ++b);
+        t += a.kv.Hkv * ld.tiles;
       }
-      if (e == 0) {
-        ms.b = b;
-        ms.off = x;
-      }
-      ms.tiles[e] = t + tiles_before<V>(a, r, cap, x);
+      int4 unit = make_int4(b, 0, 0, 0);
+      ms.tiles[e] = t + find_place<V>(a, r, ld, cap, x, &unit);
+      if (e == 0) ms.first = unit;
     }
   }
   if (tid == C::THREADS - 1 && x1 == total) ms.tiles[1] = before.y + mine.y;
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 
   if (count > 0) {
     Walk<V> w;
-    w.start(a, cap, ms.b, ms.off, x1 - x0);
+    w.start(a, cap, ms.first, x1 - x0);
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- tensor cores
       // D f32, A and B bf16, N = NR, M = 128; the second product's operands are both MN-major
@@ -701,6 +710,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       // a finished piece whose O is still to be written
       int piece = -1, d_token = 0, d_head = 0, d_rows = 0, d_part = -1;
       bool pending = false;
+      int newest = 0, oldest = 0, whole0 = 0, whole1 = 0;
       if (tid == 0) {
         // the unit's tiles take the places from `at` on; its first piece is the run's that has place `at`
         int4 j = make_int4(0, 0, 0, 0);
@@ -720,12 +730,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 #pragma unroll
             for (int i = 0; i < CW; ++i) l[i] = 0.f;
             factor = a.scale * 1.4426950408889634f * (E4M3 && a.kv.k_scale ? a.kv.k_scale[w.h] : 1.f);
+            // the row tile's tokens; the tiles of which every row sees every key
+            newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
+            whole1 = max(min(oldest + 1, cap), 0) / kKeys - w.s.tile0;
+            whole0 = a.window > 0 ? max(newest - a.window + kKeys, 0) / kKeys - w.s.tile0 : 0;
           }
           const uint32_t to = tl + uint32_t(2 + (piece & 1) * C::H) * NR;  // O of this piece
           const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
-          const int newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;  // the row tile's tokens
-          // every row of the tile sees every key of it
-          const bool whole = key0 + kKeys <= min(oldest + 1, cap) && (a.window <= 0 || key0 > newest - a.window);
+          const bool whole = w.j >= whole0 && w.j < whole1;
           // rows x0 .. x0 + CK - 1: scores in log2 units, less m where asked; hidden ones -inf
           auto scores = [&](int x0, float* s, bool less_m) {
 #pragma unroll
@@ -735,10 +747,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
             for (int x = 0; x < CK; x += 4) {
               float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
               if (less_m) m = *reinterpret_cast<const float4*>(&ms.m[c0 + x0 + x]);
-              s[x] = fmaf(s[x], factor, -m.x);
-              s[x + 1] = fmaf(s[x + 1], factor, -m.y);
-              s[x + 2] = fmaf(s[x + 2], factor, -m.z);
-              s[x + 3] = fmaf(s[x + 3], factor, -m.w);
+              scale_sub2(s[x], s[x + 1], factor, m.x, m.y);
+              scale_sub2(s[x + 2], s[x + 3], factor, m.z, m.w);
             }
             if (!whole) {
               // rows are in the order of their tokens: rows from .. to - 1 see this key
@@ -750,24 +760,51 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
                 if (c0 + x0 + x < from || c0 + x0 + x >= to_row) s[x] = -INFINITY;
             }
           };
-          wait(&ms.sfull[p], ph, fail);
-          tc_after();
-          float s[CK];
-          bool set = first;
-          if (!first) {
-            float over = -INFINITY;
+          uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
+          // Weights of the tile, in bf16 for the product and into the sums; true when a score passes
+          // m by kGrow.
+          // sums: 0 where m was given up as too small, 1 everywhere.
+          auto weights = [&](bool sums) {
+            __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
             for (int x0 = 0; x0 < CW; x0 += CK) {
+              float s[CK];
               scores(x0, s, true);
 #pragma unroll
-              for (int x = 0; x < CK; ++x) over = fmaxf(over, s[x]);
+              for (int x = 0; x < CK; x += 8) {
+                uint32_t u[4];
+#pragma unroll
+                for (int y = 0; y < 8; y += 2) {
+                  const float e0 = ex2(s[x + y]), e1 = ex2(s[x + y + 1]);
+                  if (sums) {
+                    add2(l[x0 + x + y], l[x0 + x + y + 1], e0, e1);
+                  } else {
+                    if (ms.alpha[c0 + x0 + x + y] <= kLost) l[x0 + x + y] += e0;
+                    if (ms.alpha[c0 + x0 + x + y + 1] <= kLost) l[x0 + x + y + 1] += e1;
+                  }
+                  u[y / 2] = pack2(e0, e1);
+                  most = __hmax2(most, *reinterpret_cast<const __nv_bfloat162*>(&u[y / 2]));
+                }
+                *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
+              }
             }
-            set = vote_any<kSoft>(over > kGrow);
+            return fmaxf(__low2float(most), __high2float(most)) > kMost;
+          };
+          wait(&ms.sfull[p], ph, fail);
+          tc_after();
+          if (n >= 2) wait(&ms.pvdone[p], ((n - 2) >> 1) & 1, fail);  // P(n - 2) has been read
+          bool set = first;
+          if (!first) {
+            // with the m there is; it holds for all but a few tiles
+            const bool over = weights(true);
+            if (whole) proxy_fence();
+            set = vote_any<kSoft>(over);
           }
           if (set) {
             // set m: the rows' maxima over the 128 keys
 #pragma unroll
             for (int x0 = 0; x0 < CW; x0 += CK) {
+              float s[CK];
               scores(x0, s, false);
 #pragma unroll
               for (int x = 0; x < CK; ++x) {
@@ -784,8 +821,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
             }
             softmax_sync<kSoft>();
             if (!first) {
+              // The sums hold this tile's weights against the old m already.  Where m grew by so much
+              // that those may have overflowed, what was there before them is nothing against them.
 #pragma unroll
-              for (int x = 0; x < CW; ++x) l[x] *= ms.alpha[c0 + x];
+              for (int x = 0; x < CW; ++x) l[x] = ms.alpha[c0 + x] > kLost ? l[x] * ms.alpha[c0 + x] : 0.f;
               wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
               tc_after();
 #pragma unroll 1
@@ -800,24 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
               }
               st_wait();
             }
-          }
-          if (n >= 2) wait(&ms.pvdone[p], ((n - 2) >> 1) & 1, fail);  // P(n - 2) has been read
-          uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
-#pragma unroll
-          for (int x0 = 0; x0 < CW; x0 += CK) {
-            if (CW > CK || set) scores(x0, s, true);
-#pragma unroll
-            for (int x = 0; x < CK; x += 8) {
-              uint32_t u[4];
-#pragma unroll
-              for (int y = 0; y < 8; y += 2) {
-                const float e0 = ex2(s[x + y]), e1 = ex2(s[x + y + 1]);
-                l[x0 + x + y] += e0;
-                l[x0 + x + y + 1] += e1;
-                u[y / 2] = pack2(e0, e1);
-              }
-              *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+            weights(first);
           }
           // Values at hidden keys may hold anything, and 0 times what is not finite is NaN.  Those that
           // no row sees become zeros; where some rows see a key and some do not, values that are not
@@ -863,7 +885,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
               spoiled = vote_any<kSoft>(bad);
             }
           }
-          proxy_fence();
+          if (!whole || set) proxy_fence();
           tc_before();
           __syncwarp();
           if (lane == 0) arrive(&ms.pfull[p]);
