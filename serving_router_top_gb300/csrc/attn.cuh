@@ -86,9 +86,10 @@ struct Cfg {
   static constexpr int THREADS = 32 * (SW + 3 + 4 * VG);
   static constexpr int COLS0 = (2 + 2 * H) * NR;                // two S, two O
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
-  // what a unit costs beside its tiles, in tiles: measured with units of one tile, about 3000 clocks,
-  // where 64 KB of keys and values take 2800 from memory
-  static constexpr int V = SLOT * H * 2 / (E4M3 ? 2 : 1) >= 65536 ? 1 : SLOT * H * 2 / (E4M3 ? 2 : 1) >= 32768 ? 2 : 3;
+  // What a unit costs beside its tiles, in tiles.  64 requests of 3 to 8192 tokens with 128 columns (64 KB
+  // of keys and values a tile): 1, 2, 3 and 4 give 50.1, 44.9, 46.4 and 48.9 us; 48 with 64 columns (32 KB)
+  // and a window of 1000: 33.5, 27.8, 25.9 and 26.8 us.
+  static constexpr int V = SLOT * H * 2 / (E4M3 ? 2 : 1) >= 65536 ? 2 : 3;
   static_assert(COLS0 <= 512 && NS >= 3 && (!E4M3 || NRAW >= 3), "resources of an SM");
 };
 
@@ -1005,9 +1006,23 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 }
 
 // Joins the pieces of a unit: o = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k, in the order of
-// the pieces.  CTA (c, y): the unit whose second piece is run c's first, rows y, y + 16, ..
-constexpr int kJoinThreads = 256;
+// the pieces.  CTA (c, y): the unit whose second piece is run c's first.  Few pieces (prompt chunks
+// have two): a warp takes a row, nothing waits for another warp, and 128 rows of 152 units take 5 us
+// where a CTA a row took 33.  Many (one long request: 38): a CTA takes a row, its warps share the pieces.
+constexpr int kJoinThreads = 256, kJoinRows = 16, kFewPieces = 8;
 constexpr int kMaxRuns = 512;
+
+template <int D>
+__device__ __forceinline__ void put_row(const Args& a, const int4& unit, int row, int col, float4 o, float l) {
+  const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
+  const float x = l == 0.f ? 0.f : vs / l;
+  const int i = row / a.G, g = row - i * a.G;
+  uint2 u;
+  u.x = pack2(o.x * x, o.y * x);
+  u.y = pack2(o.z * x, o.w * x);
+  *reinterpret_cast<uint2*>(a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D + col * 4) = u;
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ Args a) {
   constexpr int L = D / 4, PG = kJoinThreads / L;  // threads over a row's columns, over its pieces
@@ -1015,16 +1030,52 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
   __shared__ float4 acc[kJoinThreads];
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x, tid = threadIdx.x;
+  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const int4 unit = __ldcg(a.join + c);
   const int rows = unit.z, np = unit.w;  // pieces: the tail of run c - 1, then the heads of np - 1 runs
   auto place = [&](int k) { return 2ll * (c - 1 + k) + (k == 0 ? 1 : 0); };
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+  auto add = [](float4& o, float w, const float4& v) {
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  };
+  if (np <= kFewPieces) {
+    for (int row = blockIdx.y * (kJoinThreads / 32) + (tid >> 5); row < rows; row += kJoinRows * (kJoinThreads / 32)) {
+      float2 ml = make_float2(kUnset, 0.f);
+      if (lane < np) ml = __ldcg(reinterpret_cast<const float2*>(a.ml) + place(lane) * NR + row);
+      float m = ml.x;
+#pragma unroll
+      for (int x = kFewPieces / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+      const float w = ex2(ml.x - m);  // of piece `lane`
+#pragma unroll
+      for (int c0 = 0; c0 < L; c0 += 32) {
+        const int col = c0 + lane;
+        float4 v[kFewPieces];
+#pragma unroll
+        for (int k = 0; k < kFewPieces; ++k)
+          if (k < np && col < L)
+            v[k] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(k) * NR + row) * D) + col);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kFewPieces; ++k)
+          if (k < np) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            l = fmaf(wk, __shfl_sync(0xffffffffu, ml.y, k), l);
+            if (col < L) add(o, wk, v[k]);
+          }
+        if (col < L) put_row<D>(a, unit, row, col, o, l);
+      }
+    }
+    return;
+  }
+  for (int row = blockIdx.y; row < rows; row += kJoinRows) {
     float m = kUnset;
     for (int k = tid; k < np; k += kJoinThreads) m = fmaxf(m, __ldcg(a.ml + (place(k) * NR + row) * 2));
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if ((tid & 31) == 0) red[tid >> 5] = m;
+    if (lane == 0) red[tid >> 5] = m;
     __syncthreads();
     for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
     float l = 0.f;
@@ -1036,18 +1087,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     __syncthreads();  // f is whole, red has been read
-    if ((tid & 31) == 0) red[tid >> 5] = l;
+    if (lane == 0) red[tid >> 5] = l;
     const int col = tid % L, pg = tid / L;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = pg; k < np; k += PG) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (place(k) * NR + row) * D) + col);
-      const float w = f[k];
-      o.x = fmaf(w, v.x, o.x);
-      o.y = fmaf(w, v.y, o.y);
-      o.z = fmaf(w, v.z, o.z);
-      o.w = fmaf(w, v.w, o.w);
-    }
+    for (int k = pg; k < np; k += PG)
+      add(o, f[k], __ldcg(reinterpret_cast<const float4*>(a.part + (place(k) * NR + row) * D) + col));
     acc[tid] = o;
     __syncthreads();
     if (pg == 0) {
@@ -1060,13 +1105,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
         o.z += v.z;
         o.w += v.w;
       }
-      const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
-      const float x = l == 0.f ? 0.f : vs / l;
-      const int i = row / a.G, g = row - i * a.G;
-      uint2 u;
-      u.x = pack2(o.x * x, o.y * x);
-      u.y = pack2(o.z * x, o.w * x);
-      *reinterpret_cast<uint2*>(a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D + col * 4) = u;
+      put_row<D>(a, unit, row, col, o, l);
     }
     __syncthreads();
   }
@@ -1082,7 +1121,7 @@ template <int D, int NR, bool E4M3>
 int launch_one(const Args& a, int ctas, cudaStream_t s) {
   using C = Cfg<D, NR, E4M3>;
   if (launch_pdl(k_attn<D, NR, E4M3>, dim3(ctas), dim3(C::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
-  if (launch_pdl(k_join<D, NR>, dim3(ctas, 16), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+  if (launch_pdl(k_join<D, NR>, dim3(ctas, kJoinRows), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
   return MOE_OK;
 }
 template <int D, int NR, bool E4M3>
