@@ -178,11 +178,19 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None  # device index -> the handle of its current stream
+
+
 def _stream(stream) -> Optional[int]:
+    if stream is not None:
+        return stream.cuda_stream or None
+    global _raw_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream or None
+    if _raw_stream is None:
+        # torch.cuda.current_stream() builds a Stream object, 3 us a call on a Grace core
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device()) or None
 
 
 class _CudaArray:
@@ -544,23 +552,27 @@ class AttnWorkspace:
         return self.view.error
 
 
-def _heads(t, T: int, H: int, D: int, what: str):
+def _heads(t, shape, what: str):
     """Address and token stride of [T, H, D] bf16 rows whose heads follow one another."""
-    if t.dim() != 3 or tuple(t.shape) != (T, H, D) or t.element_size() != 2 or t.stride(2) != 1 or (
-            H > 1 and t.stride(1) != D):
-        raise ValueError(f"{what}: bf16 [{T}, {H}, {D}] with heads {D} apart, got {tuple(t.shape)} {t.dtype} "
-                         f"strides {t.stride()}")
-    return t.data_ptr(), t.stride(0)
+    if t.shape == shape and t.element_size() == 2:
+        tok, head, col = t.stride()
+        if col == 1 and (head == shape[2] or shape[1] <= 1):
+            return t.data_ptr(), tok
+    raise ValueError(f"{what}: bf16 {list(shape)} with heads {shape[2]} apart, got {list(t.shape)} {t.dtype} "
+                     f"strides {t.stride()}")
 
 
 def moe_kv_append(pages: KvPages, batch: KvBatch, rope: Optional[Rope], q, q_out, k, v, err=None, stream=None) -> None:
     """Rotate q into q_out and the keys by position; write keys and values into their pages."""
-    T, Hkv, D = batch.c.T, pages.Hkv, pages.D
-    Hq = 0 if q is None else q.shape[1]
-    qp, qs = (None, 0) if q is None else _heads(q, T, Hq, D, "q")
-    op, os_ = (None, 0) if q is None else _heads(q_out, T, Hq, D, "q_out")
-    kp, ks = _heads(k, T, Hkv, D, "k")
-    vp, vs = _heads(v, T, Hkv, D, "v")
+    T, D = batch.c.T, pages.D
+    kv = (T, pages.Hkv, D)
+    Hq, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _heads(q, (T, Hq, D), "q")
+        op, os_ = _heads(q_out, (T, Hq, D), "q_out")
+    kp, ks = _heads(k, kv, "k")
+    vp, vs = _heads(v, kv, "v")
     _check(load().moe_kv_append(pages.ref, batch.ref, None if rope is None else rope.handle, qp, qs, op, os_, Hq, kp, ks,
                                 vp, vs, _ptr(err), _stream(stream)), "moe_kv_append")
 
@@ -568,9 +580,9 @@ def moe_kv_append(pages: KvPages, batch: KvBatch, rope: Optional[Rope], q, q_out
 def moe_paged_attention(pages: KvPages, batch: KvBatch, q, o, ws: AttnWorkspace, scale: float, window: int = 0,
                         stream=None) -> None:
     """o (bf16 [T, Hq, D]) = attention of every new token over its request's pages."""
-    T, D = batch.c.T, pages.D
-    qp, qs = _heads(q, T, ws.Hq, D, "q")
-    op, os_ = _heads(o, T, ws.Hq, D, "o")
+    rows = (batch.c.T, ws.Hq, pages.D)
+    qp, qs = _heads(q, rows, "q")
+    op, os_ = _heads(o, rows, "o")
     _check(load().moe_paged_attention(pages.ref, batch.ref, qp, qs, ws.Hq, op, os_, scale, window, ws.handle,
                                       _stream(stream)), "moe_paged_attention")
 
@@ -585,17 +597,17 @@ class BlockNormDesc:
     def __init__(self, **kw):
         self.tensors = kw
         y, gate = kw["y"], kw["gate"]
-        self.T = None if y is None else y.shape[0]
-        widths = {t.shape[-1] for t in (y, gate, kw["w_post"], kw["w_pre"]) if t is not None}
-        if len(widths) > 1 or (gate is not None and gate.shape[0] not in (1, self.T)):
-            raise ValueError("block_norm_desc: y, gate and the weights differ in size")
-        self.H = widths.pop() if widths else None
         for t in (y, gate):
             if t is not None and (t.dim() != 2 or t.element_size() != 2 or t.stride(1) != 1):
                 raise ValueError("block_norm_desc: y is bf16 [T, H], gate bf16 [T, H] or [1, H], columns contiguous")
         for t in (kw["w_post"], kw["w_pre"]):
             if t is not None and (t.dim() != 1 or t.element_size() != 2 or not t.is_contiguous()):
                 raise ValueError("block_norm_desc: the weights are contiguous bf16 [H]")
+        self.T = None if y is None else y.shape[0]
+        widths = {t.shape[-1] for t in (y, gate, kw["w_post"], kw["w_pre"]) if t is not None}
+        if len(widths) > 1 or (gate is not None and gate.shape[0] not in (1, self.T)):
+            raise ValueError("block_norm_desc: y, gate and the weights differ in size")
+        self.H = widths.pop() if widths else None
         self.c = moe_block_norm_desc(
             _ptr(y), 0 if y is None else y.stride(0), 1 if kw["post_norm"] else 0, _ptr(kw["w_post"]), _ptr(gate),
             0 if gate is None or gate.shape[0] == 1 else gate.stride(0), 1 if kw["gate_sigmoid"] else 0,
@@ -611,9 +623,17 @@ def block_norm_desc(y=None, post_norm: bool = False, w_post=None, gate=None, gat
 
 def moe_block_norm(desc: BlockNormDesc, x, x_out, xn, T: int, H: int, stream=None) -> None:
     """x_out (fp32) = x + res_scale * gate * post-norm(y); xn (bf16) = pre-norm of the next block of x_out."""
-    if x.dtype.itemsize != 4 or tuple(x.shape) != (T, H) or desc.H not in (None, H) or desc.T not in (None, T) or any(
-            t is not None and (tuple(t.shape) != (T, H) or t.element_size() != size)
-            for t, size in ((x_out, 4), (xn, 2))):
+    rows = (T, H)
+    xp = xs = op = os_ = np_ = ns = None
+    ok = x.shape == rows and x.element_size() == 4 and desc.H in (None, H) and desc.T in (None, T)
+    if ok:
+        xp, xs = x.data_ptr(), x.stride(0)
+        if x_out is not None:
+            ok = x_out.shape == rows and x_out.element_size() == 4
+            op, os_ = x_out.data_ptr(), x_out.stride(0)
+        if xn is not None:
+            ok = ok and xn.shape == rows and xn.element_size() == 2
+            np_, ns = xn.data_ptr(), xn.stride(0)
+    if not ok:
         raise ValueError(f"moe_block_norm: x, x_out fp32 and xn bf16 are [{T}, {H}], as are y, gate and the weights")
-    _check(load().moe_block_norm(desc.ref, _ptr(x), x.stride(0), _ptr(x_out), 0 if x_out is None else x_out.stride(0),
-                                 _ptr(xn), 0 if xn is None else xn.stride(0), T, H, _stream(stream)), "moe_block_norm")
+    _check(load().moe_block_norm(desc.ref, xp, xs, op, os_ or 0, np_, ns or 0, T, H, _stream(stream)), "moe_block_norm")
