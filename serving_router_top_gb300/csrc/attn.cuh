@@ -440,6 +440,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       bar_init(&ms.ofree[i], C::SW);
     }
     bar_init(&ms.drain, 1);
+    for (const CUtensorMap* m : {&a.mk, &a.mv, &a.mq})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ms.fail = 0;
     ms.nbad = 0;
@@ -1006,108 +1008,67 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 }
 
 // Joins the pieces of a unit: o = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k, in the order of
-// the pieces.  CTA (c, y): the unit whose second piece is run c's first.  Few pieces (prompt chunks
-// have two): a warp takes a row, nothing waits for another warp, and 128 rows of 152 units take 5 us
-// where a CTA a row took 33.  Many (one long request: 38): a CTA takes a row, its warps share the pieces.
-constexpr int kJoinThreads = 256, kJoinRows = 16, kFewPieces = 8;
+// the pieces.  CTA (c, y): the unit whose second piece is run c's first.  A warp takes a row, P
+// pieces at a time, so no warp waits for another: a CTA a row took 33 us for prompt chunks' 128 rows,
+// this takes 3.
+constexpr int kJoinThreads = 128;
 constexpr int kMaxRuns = 512;
-
-template <int D>
-__device__ __forceinline__ void put_row(const Args& a, const int4& unit, int row, int col, float4 o, float l) {
-  const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
-  const float x = l == 0.f ? 0.f : vs / l;
-  const int i = row / a.G, g = row - i * a.G;
-  uint2 u;
-  u.x = pack2(o.x * x, o.y * x);
-  u.y = pack2(o.z * x, o.w * x);
-  *reinterpret_cast<uint2*>(a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D + col * 4) = u;
-}
-
+constexpr int join_y(int nr) { return nr > 32 ? 8 : nr / 4; }
 template <int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ Args a) {
-  constexpr int L = D / 4, PG = kJoinThreads / L;  // threads over a row's columns, over its pieces
-  __shared__ float f[kMaxRuns + 1], red[kJoinThreads / 32];
-  __shared__ float4 acc[kJoinThreads];
+  constexpr int L = D / 4, W = kJoinThreads / 32, P = 8;  // four columns a lane; pieces in flight
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 unit = __ldcg(a.join + c);
   const int rows = unit.z, np = unit.w;  // pieces: the tail of run c - 1, then the heads of np - 1 runs
-  auto place = [&](int k) { return 2ll * (c - 1 + k) + (k == 0 ? 1 : 0); };
-  auto add = [](float4& o, float w, const float4& v) {
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
-  };
-  if (np <= kFewPieces) {
-    for (int row = blockIdx.y * (kJoinThreads / 32) + (tid >> 5); row < rows; row += kJoinRows * (kJoinThreads / 32)) {
-      float2 ml = make_float2(kUnset, 0.f);
-      if (lane < np) ml = __ldcg(reinterpret_cast<const float2*>(a.ml) + place(lane) * NR + row);
-      float m = ml.x;
-#pragma unroll
-      for (int x = kFewPieces / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-      const float w = ex2(ml.x - m);  // of piece `lane`
-#pragma unroll
-      for (int c0 = 0; c0 < L; c0 += 32) {
-        const int col = c0 + lane;
-        float4 v[kFewPieces];
-#pragma unroll
-        for (int k = 0; k < kFewPieces; ++k)
-          if (k < np && col < L)
-            v[k] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(k) * NR + row) * D) + col);
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kFewPieces; ++k)
-          if (k < np) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            l = fmaf(wk, __shfl_sync(0xffffffffu, ml.y, k), l);
-            if (col < L) add(o, wk, v[k]);
-          }
-        if (col < L) put_row<D>(a, unit, row, col, o, l);
-      }
-    }
-    return;
-  }
-  for (int row = blockIdx.y; row < rows; row += kJoinRows) {
+  auto place = [&](int k) { return (2ll * (c - 1 + k) + (k == 0 ? 1 : 0)) * NR; };
+  const float2* ml = reinterpret_cast<const float2*>(a.ml);
+  constexpr int Y = join_y(NR);
+  for (int row = blockIdx.y * W + warp; row < rows; row += Y * W) {
     float m = kUnset;
-    for (int k = tid; k < np; k += kJoinThreads) m = fmaxf(m, __ldcg(a.ml + (place(k) * NR + row) * 2));
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if (lane == 0) red[tid >> 5] = m;
-    __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
+    for (int k = lane; k < np; k += 32) m = fmaxf(m, __ldcg(&ml[place(k) + row]).x);
+    m = warp_max(m);
     float l = 0.f;
-    for (int k = tid; k < np; k += kJoinThreads) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(a.ml) + place(k) * NR + row);
-      f[k] = ex2(v.x - m);
-      l += f[k] * v.y;
-    }
+    float4 o[(L + 31) / 32];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    __syncthreads();  // f is whole, red has been read
-    if (lane == 0) red[tid >> 5] = l;
-    const int col = tid % L, pg = tid / L;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = pg; k < np; k += PG)
-      add(o, f[k], __ldcg(reinterpret_cast<const float4*>(a.part + (place(k) * NR + row) * D) + col));
-    acc[tid] = o;
-    __syncthreads();
-    if (pg == 0) {
-      l = 0.f;
-      for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
-      for (int k = 1; k < PG; ++k) {
-        const float4 v = acc[k * L + col];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
+    for (int i = 0; i < (L + 31) / 32; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < np; k0 += P) {
+      float2 mine = make_float2(kUnset, 0.f);  // of piece k0 + lane
+      if (lane < P && k0 + lane < np) mine = __ldcg(&ml[place(k0 + lane) + row]);
+      const float w = ex2(mine.x - m);
+#pragma unroll
+      for (int i = 0; i < (L + 31) / 32; ++i) {
+        const int col = i * 32 + lane;
+        float4 v[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          if (k0 + k < np && col < L)
+            v[k] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(k0 + k) + row) * D) + col);
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          if (k0 + k < np) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            if (i == 0) l = fmaf(wk, __shfl_sync(0xffffffffu, mine.y, k), l);
+            if (col < L) {
+              o[i].x = fmaf(wk, v[k].x, o[i].x);
+              o[i].y = fmaf(wk, v[k].y, o[i].y);
+              o[i].z = fmaf(wk, v[k].z, o[i].z);
+              o[i].w = fmaf(wk, v[k].w, o[i].w);
+            }
+          }
       }
-      put_row<D>(a, unit, row, col, o, l);
     }
-    __syncthreads();
+    const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
+    const float x = l == 0.f ? 0.f : vs / l;
+    const int i = row / a.G, g = row - i * a.G;
+    uint16_t* out = a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D;
+#pragma unroll
+    for (int j = 0; j < (L + 31) / 32; ++j) {
+      const int col = j * 32 + lane;
+      if (col < L)
+        reinterpret_cast<uint2*>(out)[col] = make_uint2(pack2(o[j].x * x, o[j].y * x), pack2(o[j].z * x, o[j].w * x));
+    }
   }
 }
 
@@ -1121,7 +1082,7 @@ template <int D, int NR, bool E4M3>
 int launch_one(const Args& a, int ctas, cudaStream_t s) {
   using C = Cfg<D, NR, E4M3>;
   if (launch_pdl(k_attn<D, NR, E4M3>, dim3(ctas), dim3(C::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
-  if (launch_pdl(k_join<D, NR>, dim3(ctas, kJoinRows), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+  if (launch_pdl(k_join<D, NR>, dim3(ctas, join_y(NR)), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
   return MOE_OK;
 }
 template <int D, int NR, bool E4M3>
