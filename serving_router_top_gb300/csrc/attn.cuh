@@ -74,15 +74,15 @@ struct Cfg {
   static constexpr int QBYTES = NR * D * 2;
   static constexpr int PBYTES = kKeys * NR * 2;
   static constexpr int FREE = kSmem - kMisc - 2 * PBYTES;
-  // E4M3: three tiles' worth of bf16, all other room for codes on their way
+  // E4M3: three slots of bf16 for each 128 columns, all other room for codes on their way
   static constexpr int NSV = D < 128 ? 6 : 3;
-  static constexpr int QB = E4M3 ? ((FREE - NSV * SLOT - 2 * QBYTES) / (RAW + 1) >= 4 ? 2 : 1)
-                                 : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
+  static constexpr int VG = !E4M3 ? 0 : NR > 32 ? 1 : 2;  // groups of four converting warps
+  static constexpr int places(int qb) { return (FREE - qb * QBYTES - NSV * SLOT) / (RAW + 1); }
+  static constexpr int QB = E4M3 ? (places(2) >= NSV + 2 ? 2 : 1) : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
   static constexpr int NS0 = E4M3 ? NSV : (FREE - QB * QBYTES) / SLOT, NS = NS0 > 16 ? 16 : NS0;
-  static constexpr int NRAW0 = E4M3 ? (FREE - QB * QBYTES - NS * SLOT) / (RAW + 1) : 0, NRAW = NRAW0 > 16 ? 16 : NRAW0;
-  static constexpr int CW = NR < 32 ? NR : NR < 128 ? 32 : 64;  // rows a softmax warp holds
+  static constexpr int NRAW0 = E4M3 ? places(QB) : 0, NRAW = NRAW0 > 16 ? 16 : NRAW0;
+  static constexpr int CW = NR < 32 ? NR : 32;                 // rows a softmax warp holds
   static constexpr int SW = 4 * (NR / CW);                      // softmax warps
-  static constexpr int VG = !E4M3 ? 0 : NR > 32 ? 1 : 2;        // groups of four converting warps
   static constexpr int THREADS = 32 * (SW + 3 + 4 * VG);
   static constexpr int COLS0 = (2 + 2 * H) * NR;                // two S, two O
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
@@ -91,6 +91,9 @@ struct Cfg {
   // and a window of 1000: 33.5, 27.8, 25.9 and 26.8 us.
   static constexpr int V = SLOT * H * 2 / (E4M3 ? 2 : 1) >= 65536 ? 2 : 3;
   static_assert(COLS0 <= 512 && NS >= 3 && (!E4M3 || NRAW >= 3), "resources of an SM");
+  // A wait on a barrier's parity tells its phase only while the phase before it is known to be over.
+  // Of two converting groups, the one at place x has seen place x - 2 - NS consumed.
+  static_assert(VG < 2 || NRAW >= NS + 2, "place x - NRAW is converted before a group waits for place x");
 };
 
 // ------------------------------------------------------------------ schedule
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       }
     } else {
       // -------------------------------------------------------- softmax
-      constexpr int CW = C::CW, CK = CW == 16 || E4M3 ? 16 : 32;  // rows of a warp, and at a time
+      constexpr int CW = C::CW, CK = CW == 16 || E4M3 || NR == 128 ? 16 : 32;  // rows of a warp, and at a time
       const int quad = warp & 3, c0 = (warp >> 2) * CW;
       const int krow = quad * 32 + lane;  // this thread's key in a tile, and its column of v
       const uint32_t tl = taddr + (uint32_t(quad * 32) << 16);
@@ -853,6 +856,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
             const bool some = !gone && mixed && (key > oldest || (a.window > 0 && key <= newest - a.window));
             const int at = (n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
             bool bad = false;
+            if constexpr (C::NS < 3 * C::H) {
+              // V(n)'s slots may still be held by V(n - 1) or K(n + 1): see those filled first, so that
+              // the slots' phases tell V(n)'s.  With more slots it was K(n) at the latest.
+              if (n >= 1) wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
+              if (n + 1 < count) wait(&ms.sfull[p ^ 1], ((n + 1) >> 1) & 1, fail);
+            }
 #pragma unroll 1
             for (int hh = 0; hh < C::H; ++hh) {
               const int slot = (at + hh) % C::NS;

@@ -91,6 +91,26 @@ def test_scores_that_rise_along_the_cache():
     assert ((o - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("G,n", [(4, 1), (8, 4), (8, 7)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_many_units_of_many_tiles_beside_junk(D, G, n, e4m3):
+    """Every run passes several ends of requests, whose last pages hold NaN, with its rings full."""
+    g = torch.Generator().manual_seed(D + n)
+    lens = [int(x) for x in torch.exp(torch.rand(24, generator=g) * 3.5 + 5.3)]  # 200 .. 6600
+    ns = [int(x) for x in torch.randint(1, n + 1, (24,), generator=g)]
+    P = Paged(lens, ns, 2, D, 64, e4m3, seed=n)
+    q = strided_rows(P.T, 2 * G, D, 0, g)
+    ref, tol = attention_ref(P, q, 2 * G, D ** -0.5, 0)
+    pages, bt = P.device()
+    ws, qd = moe.AttnWorkspace(2 * G, 2, D), q.cuda()
+    for _ in range(5):
+        o = torch.empty_like(qd)
+        moe.moe_paged_attention(pages, bt, qd, o, ws, D ** -0.5)
+        assert ((o.cpu().double() - ref).abs() <= tol).all()
+    assert moe.moe_attn_sync_status(ws) == moe.MOE_OK
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
 def test_any_scale(scale):
     check(Paged([300], [3], 1, 128, 16), 8, scale=scale)
