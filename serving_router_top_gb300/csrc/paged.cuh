@@ -58,20 +58,4 @@ inline bool rows_ok(const void* p, long long stride, int T, long long width) {
   return p && !(reinterpret_cast<uintptr_t>(p) & 15) && (T <= 1 || (stride >= width && stride % 8 == 0));
 }
 
-// The request that token row t belongs to: the last b with q_start[b] <= t < q_start[b+1],
-// or -1.  Called by every thread of the CTA.
-__device__ __forceinline__ int request_of(const KvView& kv, int t) {
-  int n = 0;
-  for (int b0 = 0; b0 < kv.B; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    n += __syncthreads_count(b < kv.B && kv.q_start[b] <= t);
-  }
-  return n > 0 && t < kv.q_start[n] ? n - 1 : -1;
-}
-
-// Position of token row t of request b; negative when kv_len is too small.
-__device__ __forceinline__ long long position_of(const KvView& kv, int b, int t) {
-  return (long long)kv.kv_len[b] - (kv.q_start[b + 1] - t);
-}
-
 }  // namespace moe
