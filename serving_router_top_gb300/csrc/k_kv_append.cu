@@ -86,22 +86,25 @@ __device__ __forceinline__ void store8(const Args& a, int t, int head, int col, 
 
 // One CTA per token; a thread takes kMine items of 16 columns of a head at a time (the two halves'
 // vectors of eight pairs, or two neighbours).  The first items' loads are on their way while the
-// CTA finds its request, position, page and angles: that chain of dependent loads, not the bytes,
-// was the time of a token (8192 tokens of 32 + 2 x 4 heads of 128: 38.9 us without).
+// CTA finds its request, position, page and angles, a chain of dependent loads.  8192 tokens of
+// 32 + 2 x 4 heads of 128 columns, 168 MB: 38.9 us with the loads after the chain, 28.1 us now, 6.0 TB/s.
+// Four tokens to a CTA, the next one's loads beside the last one's stores, take 101 registers and 47 us;
+// one or three items a thread 32.0 and 28.4 us.
 constexpr int kMine = 2;
 
 template <bool E4M3, int D>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant__ Args a) {
   constexpr int kItems = D / 16;
-  __shared__ float2 cs[kMaxPairs];  // cos, sin of each pair's angle
+  // cos, sin of each pair's angle: pair 8 j + i at [i][j], as the lanes of a head read them (64 bytes
+  // apart, those met in four banks, and the prompt chunk took 32.2 us)
+  __shared__ float2 cs[8][kMaxPairs / 8];
   __shared__ int owner, position;
   pdl_trigger();
-  if (threadIdx.x == 0) owner = -1;
   pdl_wait();
   const int t = blockIdx.x, step = blockDim.x, pairs = a.rot / 2;
   const int n = (a.Hq + 2 * a.kv.Hkv) * kItems;
   struct Item {
-    int head, c0, c1, pair;  // pair < 0: the columns stay as they are
+    int head, c0, c1, pair;  // its pairs are 8 pair .. 8 pair + 7; < 0: the columns stay as they are
     uint4 v0, v1;
   };
   auto fetch = [&](int it, Item& x) {
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
     const int head = it / kItems, j = it - head * kItems;
     const bool turn = head < a.Hq + a.kv.Hkv && 16 * j < a.rot, halves = turn && !a.interleaved;
     x.head = head;
-    x.pair = turn ? 8 * j : -1;
+    x.pair = turn ? j : -1;
     x.c0 = halves ? 8 * j : 16 * j;
     x.c1 = halves ? pairs + 8 * j : 16 * j + 8;
     const uint16_t* src = head < a.Hq ? a.q + (long long)t * a.qs + head * D
@@ -124,17 +127,17 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   for (int i = 0; i < kMine; ++i) fetch(threadIdx.x + i * step, x[i]);
 
   // the request whose rows t is one of
-  __syncthreads();  // owner is -1
+  bool found = false;
   for (int b = threadIdx.x; b < a.kv.B; b += step) {
     const int s0 = a.kv.q_start[b], s1 = a.kv.q_start[b + 1], len = a.kv.kv_len[b];
     if (s0 <= t && t < s1) {
       owner = b;
       position = int(min(max((long long)len - (s1 - t), (long long)INT_MIN), (long long)INT_MAX));
+      found = true;
     }
   }
-  __syncthreads();
+  if (!__syncthreads_or(found)) return;
   const int b = owner, pos = position;
-  if (b < 0) return;
   long long at = -1;  // byte offset of (page, place) in the pools
   int id = -1;
   if (pos >= 0 && (pos >> a.kv.page_shift) < a.kv.table_stride)
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
     const long long frac = (long long)(uint64_t(int64_t(pos)) * a.turns[i]);
     float c, s;
     sincospif(float(frac) * 0x1p-63f, &s, &c);
-    cs[i] = make_float2(c, s);
+    cs[i & 7][i >> 3] = make_float2(c, s);
   }
   if (id >= 0 && id < a.kv.npages)
     at = id * a.kv.page_stride + (long long)(pos & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
       if (!a.interleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 r = cs[x.pair + i];
+          const float2 r = cs[i][x.pair];
           const float u = f0[i], w = f1[i];
           f0[i] = u * r.x - w * r.y;
           f1[i] = w * r.x + u * r.y;
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 r = cs[x.pair + i], r2 = cs[x.pair + 4 + i];
+          const float2 r = cs[i][x.pair], r2 = cs[4 + i][x.pair];
           float u = f0[2 * i], w = f0[2 * i + 1];
           f0[2 * i] = u * r.x - w * r.y;
           f0[2 * i + 1] = w * r.x + u * r.y;
