@@ -358,13 +358,94 @@ __device__ __forceinline__ uint64_t desc(uint32_t start, uint32_t lbo, uint32_t 
          (uint64_t(1) << 46) | (swizzle << 61);
 }
 
+struct PlanShared {
+  int4 first;    // the run's first request, key head and row tile, and its first place in their unit
+  int tiles[2];  // the call's tiles before the run and before the next one
+  int2 scan[32];
+};
+struct Plan {
+  int total, runs, x0, x1, count;  // places and runs of the call; the run's places and tiles
+};
+// The run: all units of the call, end to end, cut into equal parts.  Called by every thread of the CTA;
+// its two barriers also end the CTA's set-up.
+template <int V, int THREADS>
+__device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = a.kv.B, per = (B + THREADS - 1) / THREADS;
+  int2 mine = make_int2(0, 0);  // places and tiles of this thread's requests
+  Req r = {};
+  Load ld = {};  // the last of them
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < B) {
+      r = load_req(a.kv, b);
+      if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
+      ld = head_load(r, a.tokens, a.window, cap);
+      mine.x += a.kv.Hkv * (ld.tiles + V * ld.units);
+      mine.y += a.kv.Hkv * ld.tiles;
+    }
+  }
+  int2 before = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const int y0 = __shfl_up_sync(0xffffffffu, before.x, x), y1 = __shfl_up_sync(0xffffffffu, before.y, x);
+    if (lane >= x) {
+      before.x += y0;
+      before.y += y1;
+    }
+  }
+  if (lane == 31) sh.scan[warp] = before;
+  before.x -= mine.x;
+  before.y -= mine.y;
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const int2 sum = lane < THREADS / 32 ? sh.scan[lane] : make_int2(0, 0);
+  before.x += __reduce_add_sync(0xffffffffu, lane < warp ? sum.x : 0);
+  before.y += __reduce_add_sync(0xffffffffu, lane < warp ? sum.y : 0);
+  Plan p;
+  const int run = blockIdx.x;
+  p.total = __reduce_add_sync(0xffffffffu, sum.x);
+  p.runs = min(int(gridDim.x), p.total);
+  p.x0 = run < p.runs ? cut_at(p.total, p.runs, run) : p.total;
+  p.x1 = run < p.runs ? cut_at(p.total, p.runs, run + 1) : p.total;
+  if (mine.x > 0) {  // a cut falls into the requests of one thread
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+      int x = (e ? p.x1 : p.x0) - before.x, t = before.y, b = tid * per;
+      if (x < 0 || x >= mine.x) continue;
+      for (; per > 1; ++b) {
+        r = load_req(a.kv, b);
+        ld = head_load(r, a.tokens, a.window, cap);
+        const int c = a.kv.Hkv * (ld.tiles + V * ld.units);
+        if (x < c) break;
+        x -= c;
+        t += a.kv.Hkv * ld.tiles;
+      }
+      int4 unit = make_int4(b, 0, 0, 0);
+      sh.tiles[e] = t + find_place<V>(a, r, ld, cap, x, &unit);
+      if (e == 0) sh.first = unit;
+    }
+  }
+  if (tid == THREADS - 1 && p.x1 == p.total) sh.tiles[1] = before.y + mine.y;
+  __syncthreads();
+  p.count = run < p.runs ? sh.tiles[1] - sh.tiles[0] : 0;
+  return p;
+}
+// What the join needs of the unit that a run's first piece, begun at tile jbeg, is the second piece of.
+template <int V>
+__device__ __forceinline__ int4 join_record(const Args& a, const Plan& p, const Walk<V>& w) {
+  // the unit's tiles take the places from `at` on; its first piece is the run's that has place `at`
+  const int run = blockIdx.x, at = p.x0 - w.jbeg;
+  if (w.jbeg == 0 || cut_at(p.total, p.runs, run - 1) > at) return make_int4(0, 0, 0, 0);
+  return make_int4(w.r.s0 + w.s.i0, w.h, (w.s.i1 - w.s.i0 + 1) * a.G, run_of(p.total, p.runs, at + w.s.nt - 1) - run + 2);
+}
+
 struct Misc {
   uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
-  int4 first;    // the run's first request, key head and row tile, and its first place in their unit
-  int tiles[2];  // the call's tiles before the run and before the next one
-  int2 scan[32];
+  PlanShared plan;
   alignas(16) float m[128];      // of the rows, log2 units
   alignas(16) float alpha[128];
   float inv[128];            // 1 / sum of a finished piece's rows
@@ -451,71 +532,16 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
   }
   pdl_wait();
 
-  // ---- the run: all units of the call, end to end, cut into equal parts
   constexpr int V = C::V;
   const int cap = cap_of(a.kv);
-  const int B = a.kv.B, per = (B + C::THREADS - 1) / C::THREADS;
-  int2 mine = make_int2(0, 0);  // places and tiles of this thread's requests
-  Req r = {};
-  Load ld = {};  // the last of them
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < B) {
-      r = load_req(a.kv, b);
-      if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
-      ld = head_load(r, a.tokens, a.window, cap);
-      mine.x += a.kv.Hkv * (ld.tiles + V * ld.units);
-      mine.y += a.kv.Hkv * ld.tiles;
-    }
-  }
-  int2 before = mine;
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const int y0 = __shfl_up_sync(0xffffffffu, before.x, x), y1 = __shfl_up_sync(0xffffffffu, before.y, x);
-    if (lane >= x) {
-      before.x += y0;
-      before.y += y1;
-    }
-  }
-  if (lane == 31) ms.scan[warp] = before;
-  before.x -= mine.x;
-  before.y -= mine.y;
-  tc_before();
-  __syncthreads();
-  tc_after();
+  const Plan plan = plan_run<V, C::THREADS>(a, cap, ms.plan);
   const uint32_t taddr = ms.taddr;
-  const int2 sum = lane < C::THREADS / 32 ? ms.scan[lane] : make_int2(0, 0);
-  before.x += __reduce_add_sync(0xffffffffu, lane < warp ? sum.x : 0);
-  before.y += __reduce_add_sync(0xffffffffu, lane < warp ? sum.y : 0);
-  const int run = blockIdx.x, total = __reduce_add_sync(0xffffffffu, sum.x);
-  const int runs = min(int(gridDim.x), total);
-  const int x0 = run < runs ? cut_at(total, runs, run) : total, x1 = run < runs ? cut_at(total, runs, run + 1) : total;
-  if (mine.x > 0) {  // a cut falls into the requests of one thread
-#pragma unroll 1
-    for (int e = 0; e < 2; ++e) {
-      int x = (e ? x1 : x0) - before.x, t = before.y, b = tid * per;
-      if (x < 0 || x >= mine.x) continue;
-      for (; per > 1; ++b) {
-        r = load_req(a.kv, b);
-        ld = head_load(r, a.tokens, a.window, cap);
-        const int c = a.kv.Hkv * (ld.tiles + V * ld.units);
-        if (x < c) break;
-        x -= c;
-        t += a.kv.Hkv * ld.tiles;
-      }
-      int4 unit = make_int4(b, 0, 0, 0);
-      ms.tiles[e] = t + find_place<V>(a, r, ld, cap, x, &unit);
-      if (e == 0) ms.first = unit;
-    }
-  }
-  if (tid == C::THREADS - 1 && x1 == total) ms.tiles[1] = before.y + mine.y;
-  __syncthreads();
-  const int count = run < runs ? ms.tiles[1] - ms.tiles[0] : 0;
+  const int run = blockIdx.x, count = plan.count;
   if (count == 0 && tid == 0) a.join[run] = make_int4(0, 0, 0, 0);
 
   if (count > 0) {
     Walk<V> w;
-    w.start(a, cap, ms.first, x1 - x0);
+    w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- tensor cores
       // D f32, A and B bf16, N = NR, M = 128; the second product's operands are both MN-major
@@ -717,14 +743,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       int piece = -1, d_token = 0, d_head = 0, d_rows = 0, d_part = -1;
       bool pending = false;
       int newest = 0, oldest = 0, whole0 = 0, whole1 = 0;
-      if (tid == 0) {
-        // the unit's tiles take the places from `at` on; its first piece is the run's that has place `at`
-        int4 j = make_int4(0, 0, 0, 0);
-        const int at = x0 - w.jbeg;
-        if (w.jbeg > 0 && cut_at(total, runs, run - 1) <= at)
-          j = make_int4(w.r.s0 + w.s.i0, w.h, (w.s.i1 - w.s.i0 + 1) * a.G, run_of(total, runs, at + w.s.nt - 1) - run + 2);
-        a.join[run] = j;
-      }
+      if (tid == 0) a.join[run] = join_record<V>(a, plan, w);
 #pragma unroll 1
       for (int n = 0; n <= count; ++n) {
         const int p = n & 1;
