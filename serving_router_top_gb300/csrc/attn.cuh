@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
       }
     } else {
       // -------------------------------------------------------- softmax
-      constexpr int CW = C::CW, CK = CW == 16 || E4M3 || NR == 128 ? 16 : 32;  // rows of a warp, and at a time
+      constexpr int CW = C::CW, CK = CW == 16 || E4M3 ? 16 : 32;  // rows of a warp, and at a time
       const int quad = warp & 3, c0 = (warp >> 2) * CW;
       const int krow = quad * 32 + lane;  // this thread's key in a tile, and its column of v
       const uint32_t tl = taddr + (uint32_t(quad * 32) << 16);
@@ -1100,10 +1100,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
   }
 }
 
-// Tile of rows for calls of about n new tokens a request and G query heads a key head: the smallest
-// that holds a request's rows, else the largest.  A tile holds the heads of NR / G whole tokens.
+// Rows of a unit for calls of about n new tokens a request and G query heads a key head: the smallest
+// tile that holds a request's rows, and above 64 rows the two 128-row tiles of attn_chunk.cuh where it
+// applies.  A tile holds the heads of whole tokens.
+constexpr int kChunkRows = 256;
 inline int row_tile(int D, int e4m3, int G, int n) {
-  return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || e4m3 || D > 128 ? 64 : 128;
+  return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || e4m3 || D > 128 ? 64 : kChunkRows;
 }
 
 template <int D, int NR, bool E4M3>

@@ -1,0 +1,429 @@
+// Attention of prompt chunks: the same split, pages and join as attn.cuh, with the rows on the lanes.
+//
+// With 128 rows and more there is nothing to pad, and the other way round then costs less:
+//   S = Q K^T      [128 rows x 128 keys]   (M = rows)
+//   O += P V       [128 rows x D]          P from tensor memory
+// A thread has one row, so its maximum and sum need no other thread; P never passes through shared
+// memory; and a tile of keys and values is read from shared memory once as an N-side operand for
+// each 128 rows.  attn.cuh's form at 128 rows moves 224 KB of shared memory a tile (K and V in and out,
+// Q, P in and out), 1800 clocks of 128 bytes, beside 1250 clocks of products, and takes 2450; this form
+// moves 128 KB.
+//
+// A CTA holds two row tiles of whole tokens, each with its own softmax warps: while one's weights are
+// computed, the tensor core works for the other.  m is lazy as in attn.cuh, but a row's own: it is set
+// again when a score passes it by 8 (log2).  P overwrites its S in tensor memory (64 of the 128
+// columns), so the next S of a row tile waits for the product that reads it.
+#pragma once
+
+#include "attn.cuh"
+
+namespace moe {
+namespace attn {
+namespace chunk {
+
+constexpr float kGrow = 8.0f;  // log2
+
+template <int D>
+struct Cfg {
+  static constexpr int SLOT = kKeys * D * 2, QTILE = 128 * D * 2;
+  static constexpr int NS0 = (kSmem - kMisc - 2 * QTILE) / SLOT, NS = NS0 > 8 ? 8 : NS0 / 2 * 2;  // even: K and V in turn
+  static constexpr int MMA = 8, LOAD = 9, THREADS = 32 * 11;  // warps 0-3 and 4-7: softmax of a row tile each
+  static constexpr int V = SLOT >= 32768 ? 2 : 3;             // as in attn.cuh, by the bytes of a tile
+  static_assert(NS >= 4, "shared memory of an SM");
+};
+
+struct Misc {
+  uint64_t full[8], empty[8], qfull, qfree, sfull[2], pfull[2], pvdone[2], ofree[2], drain;
+  uint32_t taddr;
+  int fail;
+  PlanShared plan;
+  int page[2][kKeys];
+  int nbad[4];  // keys of a tile with values that are not finite, of four tiles in turn
+  uint8_t bad[4][kKeys];
+};
+static_assert(sizeof(Misc) <= kMisc, "misc");
+
+// Four steps of 16 keys: A (P) from tensor memory, eight columns a step, B (V) 2048 bytes on.
+__device__ __forceinline__ void mma4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, 128;\n\t"
+      "add.u32 a2, %1, 16;\n\tadd.u64 b2, %2, 256;\n\t"
+      "add.u32 a3, %1, 24;\n\tadd.u64 b3, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void st16u(uint32_t t, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_constant__ Args a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* ring = smem;
+  uint8_t* sq = ring + C::NS * C::SLOT;
+  Misc& ms = *reinterpret_cast<Misc*>(sq + 2 * C::QTILE);
+  volatile int* fail = &ms.fail;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+  pdl_trigger();
+  if (warp == C::MMA) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ms.taddr)), "n"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  } else if (tid == 32 * C::LOAD) {
+    for (int i = 0; i < C::NS; ++i) {
+      bar_init(&ms.full[i], 1);
+      bar_init(&ms.empty[i], 1);
+    }
+    bar_init(&ms.qfull, 1);
+    bar_init(&ms.qfree, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&ms.sfull[i], 1);
+      bar_init(&ms.pfull[i], 4);
+      bar_init(&ms.pvdone[i], 1);
+      bar_init(&ms.ofree[i], 4);
+    }
+    bar_init(&ms.drain, 1);
+    for (const CUtensorMap* m : {&a.mk, &a.mv, &a.mq})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    ms.fail = 0;
+  }
+  pdl_wait();
+  constexpr int V = C::V;
+  const int cap = cap_of(a.kv);
+  const Plan plan = plan_run<V, C::THREADS>(a, cap, ms.plan);
+  const uint32_t taddr = ms.taddr;
+  const int run = blockIdx.x, count = plan.count;
+  if (count == 0 && tid == 0) a.join[run] = make_int4(0, 0, 0, 0);
+
+  if (count > 0) {
+    Walk<V> w;
+    w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
+    const int half = a.tokens / 2;  // tokens of a row tile
+    auto both = [&]() { return w.s.i1 - w.s.i0 + 1 > half; };  // the unit has rows for the second row tile
+    if (warp == C::MMA) {
+      // -------------------------------------------------------- tensor cores
+      // D f32, A and B bf16, M = 128; S: N = 128 keys, both K-major; O: N = D, B (V) MN-major
+      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
+      constexpr uint32_t kIdescS = kBase | (uint32_t(kKeys >> 3) << 17), kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
+      Ring<C::NS> kr(0), vr(0);
+      vr.next();
+      int scores[2] = {0, 0}, pieces[2] = {0, 0}, qn = 0;  // S products and pieces of each row tile, pieces of the run
+      auto put_s = [&](int x) {  // S = Q K(n)^T; its columns hold the last P until that product is done
+        if (scores[x] > 0) wait(&ms.pvdone[x], (scores[x] - 1) & 1, fail);
+        ++scores[x];
+        tc_after();
+        const uint64_t qd = desc(su32(sq + x * C::QTILE), 16, 1024, 2), kd = desc(su32(ring + kr.slot * C::SLOT), 16, 1024, 2);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          mma4<2, 2>(taddr + x * 128, qd + k * (128 * 128 >> 4), kd + k * (kKeys * 128 >> 4), kIdescS, k > 0);
+        commit_to(&ms.sfull[x]);
+      };
+      auto begin = [&]() {  // the tile's keys are there, and the queries of its piece
+        if (w.j == w.jbeg) wait(&ms.qfull, qn++ & 1, fail);
+        wait(&ms.full[kr.slot], kr.phase, fail);
+      };
+      auto end = [&]() {
+        commit_to(&ms.empty[kr.slot]);
+        if (w.j + 1 == w.jend) commit_to(&ms.qfree);
+        kr.next();
+        kr.next();
+      };
+      begin();
+      put_s(0);
+      if (both()) put_s(1);
+      end();
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        const bool first = w.j == w.jbeg, two = both(), more = n + 1 < count;
+        auto put_o = [&](int x) {  // O += P V(n)
+          wait(&ms.pfull[x], (scores[x] - 1) & 1, fail);
+          if (first && pieces[x]++ > 0) wait(&ms.ofree[x], (pieces[x] - 2) & 1, fail);
+          tc_after();
+          const uint64_t vd = desc(su32(ring + vr.slot * C::SLOT), kKeys * 128, 1024, 2);
+#pragma unroll
+          for (int k = 0; k < kKeys / 64; ++k)
+            mma4_ta(taddr + 256 + x * D, taddr + x * 128 + k * 32, vd + k * 512, kIdescO, !first || k > 0);
+          commit_to(&ms.pvdone[x]);
+        };
+        wait(&ms.full[vr.slot], vr.phase, fail);
+        put_o(0);
+        if (more) {
+          w.next(a, cap);
+          begin();
+          put_s(0);
+        }
+        if (two) put_o(1);
+        commit_to(&ms.empty[vr.slot]);
+        vr.next();
+        vr.next();
+        if (more) {
+          if (both()) put_s(1);
+          end();
+        }
+      }
+      commit_to(&ms.drain);
+      const unsigned long long t0 = now_ns();
+      for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(&ms.drain))
+            : "memory");
+    } else if (warp >= C::LOAD) {
+      // -------------------------------------------------------- loads: keys and queries, values
+      const bool keys = warp == C::LOAD;
+      const KvView& kv = a.kv;
+      const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
+      const CUtensorMap* tm = keys ? &a.mk : &a.mv;
+      int* page = ms.page[keys ? 0 : 1];
+      Ring<C::NS> rg(1);
+      if (!keys) rg.next();
+      int qn = 0;
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        if (keys && w.j == w.jbeg) {
+          if (qn > 0) wait(&ms.qfree, (qn - 1) & 1, fail);
+          ++qn;
+          if (lane == 0 && !*fail) {
+            const int tiles = both() ? 2 : 1;
+            expect(&ms.qfull, uint32_t(tiles * half * a.G * D * 2));
+            for (int x = 0; x < tiles; ++x)
+              for (int c = 0; c < D / 64; ++c)
+                load_rows(sq + x * C::QTILE + c * (128 * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0 + x * half,
+                          &ms.qfull);
+          }
+        }
+        const int key0 = (w.s.tile0 + w.j) * kKeys;
+        const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
+        for (int x = lane; x < boxes; x += 32) {
+          const int key = key0 + (x << box_shift);
+          int id = -2;
+          if (key < w.s.hi && key + (1 << box_shift) > w.s.lo) id = row[key >> kv.page_shift];
+          const bool ok = id >= 0 && id < kv.npages;
+          if (!ok && id != -2) set_error(a.err, MOE_ERANGE);
+          page[x] = ok ? id : kv.npages;  // past the end: zeros
+        }
+        __syncwarp();
+        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
+        wait(&ms.empty[rg.slot], rg.phase, fail);
+        if (!*fail) {
+          if (lane == 0) expect(&ms.full[rg.slot], C::SLOT);
+          __syncwarp();
+#pragma unroll 1
+          for (int x = lane; x < boxes * (D / 64); x += 32) {
+            const int p = x & (boxes - 1), c = x >> (7 - box_shift);
+            load_box(ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128, tm, c * 64, tok, w.h, page[p],
+                     &ms.full[rg.slot]);
+          }
+        }
+        __syncwarp();
+        rg.next();
+        rg.next();
+        if (n + 1 < count) w.next(a, cap);
+      }
+    } else {
+      // -------------------------------------------------------- softmax, a row a thread
+      const int x = warp >> 2, quad = warp & 3, krow = quad * 32 + lane;  // row tile; row in it, and key in a tile
+      const uint32_t ts = taddr + (uint32_t(quad * 32) << 16) + x * 128, to = taddr + (uint32_t(quad * 32) << 16) + 256 + x * D;
+      const float factor = a.scale * 1.4426950408889634f;
+      const int mine = x * half + krow / a.G;  // the row's token in its unit
+      float m = kUnset, l = 0.f;
+      int k = 0;  // tiles of this row tile
+      if (tid == 0) a.join[run] = join_record<V>(a, plan, w);
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        const bool active = x == 0 || both();
+        if (active) {
+          const bool first = w.j == w.jbeg;
+          if (first) m = kUnset, l = 0.f;
+          const int newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
+          const int pos = min(w.r.pos0 + w.s.i0 + mine, newest);
+          const int key0 = (w.s.tile0 + w.j) * kKeys;
+          const bool whole = key0 + kKeys <= min(oldest + 1, cap) && (a.window <= 0 || key0 > newest - a.window);
+          wait(&ms.sfull[x], k & 1, fail);
+          tc_after();
+          float s[kKeys];
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 16) ld16(ts + i, s + i);
+          ld_wait();
+          float f = factor;
+          if (!whole || factor <= 0.f) {
+            const int from = a.window > 0 ? pos - a.window + 1 - key0 : INT_MIN, to_key = min(pos + 1, cap) - key0;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] = i < from || i >= to_key ? -INFINITY : s[i] * factor;
+            f = 1.f;
+          }
+          float top = -INFINITY, top1 = -INFINITY;  // the row's largest score
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 2) top = fmaxf(top, s[i]), top1 = fmaxf(top1, s[i + 1]);
+          top = fmaxf(top, top1) * f;
+          const bool grow = top > m + kGrow;  // true for the first that a row sees: m is unset
+          if (__any_sync(0xffffffffu, grow)) {
+            const float old = m;
+            if (grow) m = top;
+            const float alpha = grow ? ex2(old - m) : 1.f;
+            l *= alpha;
+            if (!first) {
+              wait(&ms.pvdone[x], (k - 1) & 1, fail);
+              tc_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                ld16(to + c, o);
+                ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                st16(to + c, o);
+              }
+              st_wait();
+            }
+          }
+          float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              scale_sub2(s[c + i], s[c + i + 1], f, m, m);
+              const float e0 = ex2(s[c + i]), e1 = ex2(s[c + i + 1]);
+              add2(sum0, sum1, e0, e1);
+              u[i / 2] = pack2(e0, e1);
+            }
+            st16u(ts + c / 2, u);
+          }
+          l += sum0 + sum1;
+          // Values at hidden keys, as in attn.cuh: zeros where no row sees the key; where some do, what is
+          // not finite leaves the tile and goes to their rows below.  The first row tile's threads, one a
+          // key, do it for both: its product comes first.
+          const bool mixed = !whole && w.s.i1 > w.s.i0;
+          if (!whole && x == 0) {
+            if (mixed && krow == 0) ms.nbad[n & 3] = 0;
+            if (mixed) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+            const int key = key0 + krow, slot = (2 * n + 1) % C::NS;
+            const bool gone = key < w.s.lo || key >= w.s.hi;
+            const bool some = !gone && mixed && (key > oldest || (a.window > 0 && key <= newest - a.window));
+            wait(&ms.full[slot], uint32_t((2 * n + 1) / C::NS) & 1, fail);  // V(n - NS / 2) has been used
+            uint8_t* row = ring + slot * C::SLOT;
+            if (gone) {
+#pragma unroll 4
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(row + (c / 8) * (kKeys * 128) + sw128(krow, c % 8)) = make_uint4(0, 0, 0, 0);
+            } else if (some) {
+              bool bad = false;
+#pragma unroll 1
+              for (int c = 0; c < D; ++c) {
+                uint16_t* v = reinterpret_cast<uint16_t*>(row + (c / 64) * (kKeys * 128) + sw128(krow, c % 64 / 8)) + c % 8;
+                if ((*v & 0x7f80u) == 0x7f80u) *v = 0, bad = true;
+              }
+              if (bad) ms.bad[n & 3][atomicAdd(&ms.nbad[n & 3], 1)] = uint8_t(krow);
+            }
+            proxy_fence();
+            if (mixed) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+          }
+          st_wait();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) arrive(&ms.pfull[x]);
+          const bool last = w.j + 1 == w.jend;
+          if (mixed || last) {
+            wait(&ms.pvdone[x], k & 1, fail);
+            tc_after();
+          }
+          if (mixed) {
+            const int nbad = *const_cast<volatile int*>(&ms.nbad[n & 3]);
+#pragma unroll 1
+            for (int e = 0; e < nbad; ++e) {
+              const int key = key0 + ms.bad[n & 3][e];
+              const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (key >> a.kv.page_shift)];
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(
+                  a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
+                  (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride);
+              const bool sees = key <= pos && (a.window <= 0 || key > pos - a.window);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                ld16(to + c, o);
+                ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float add = bf16_bits_to_f32(v[c + i]);
+                  if (sees && !isfinite(add)) o[i] += add;
+                }
+                st16(to + c, o);
+              }
+            }
+            if (nbad) st_wait();
+          }
+          if (last) {
+            // ---- the piece is done
+            const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
+            const int unit_row = x * half * a.G + krow, rows = min(half, w.s.i1 - w.s.i0 + 1 - x * half) * a.G;
+            const bool live = krow < rows;
+            const long long part = (2ll * run + (head ? 0 : 1)) * 256 + unit_row;
+            if (split && live) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m, l);
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // a sum of zero is a row that sees no key; its O is zeros
+            uint16_t* out = a.o + (long long)(w.r.s0 + w.s.i0 + mine) * a.os + (long long)(w.h * a.G + krow % a.G) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              ld16(to + c, o);
+              ld_wait();
+              if (!live) continue;
+              if (split) {
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                  *reinterpret_cast<float4*>(a.part + part * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              } else {
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv);
+                reinterpret_cast<uint4*>(out + c)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                reinterpret_cast<uint4*>(out + c)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+              }
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) arrive(&ms.ofree[x]);
+          }
+          ++k;
+        }
+        if (n + 1 < count) w.next(a, cap);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *fail) set_error(a.err, MOE_ETIMEOUT);
+  if (warp == C::MMA) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512));
+  }
+}
+
+template <int D>
+int launch(const Args& a, int ctas, cudaStream_t s) {
+  if (launch_pdl(k_chunk<D>, dim3(ctas), dim3(Cfg<D>::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_pdl(k_join<D, 256>, dim3(ctas, join_y(256)), dim3(kJoinThreads), 0, s, a) == cudaSuccess ? MOE_OK : MOE_ECUDA;
+}
+template <int D>
+int opt_in() {
+  return cudaFuncSetAttribute(k_join<D, 256>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
+                 cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
+             ? MOE_OK
+             : MOE_ECUDA;
+}
+
+}  // namespace chunk
+}  // namespace attn
+}  // namespace moe

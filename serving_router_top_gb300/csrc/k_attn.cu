@@ -65,7 +65,7 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
     return MOE_ECUDA;
   }
   w->ctas = sms < attn::kMaxRuns ? sms : attn::kMaxRuns;  // one CTA per SM
-  const size_t rows = 2 * size_t(w->ctas) * (D == 256 ? 64 : 128);
+  const size_t rows = 2 * size_t(w->ctas) * (D == 256 ? 64 : attn::kChunkRows);
   const size_t o_part = 256, o_ml = o_part + rows * D * 4, o_join = o_ml + rows * 8;
   const size_t bytes = o_join + size_t(w->ctas) * 16;
   uint8_t* base = nullptr;
@@ -126,7 +126,8 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.os = T > 1 ? o_stride : width;
   a.G = Hq / kv->Hkv;
   a.window = window;
-  a.tokens = nr / a.G;
+  const int tile = nr == attn::kChunkRows ? nr / 2 / a.G : nr / a.G;  // tokens of a row tile
+  a.tokens = nr == attn::kChunkRows ? 2 * tile : tile;
   // the schedule counts in 31 bits: a unit has at most its request's tiles, and three more places
   if ((double(T) / a.tokens + b->B) * kv->Hkv * (double(a.kv.table_stride) * kv->page / attn::kKeys + 4) > 2147483000.0)
     return MOE_EINVAL;
@@ -138,7 +139,7 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   const cuuint32_t boxes[4] = {cuuint32_t(kv->e4m3 ? (kv->D < 128 ? kv->D : 128) : 64), cuuint32_t(box), 1, 1};
   const cuuint64_t qdims[3] = {cuuint64_t(kv->D), cuuint64_t(Hq), cuuint64_t(T)};
   const cuuint64_t qpitches[2] = {cuuint64_t(kv->D) * 2, cuuint64_t(T > 1 ? q_stride : width) * 2};
-  const cuuint32_t qbox[3] = {64, cuuint32_t(a.G), cuuint32_t(a.tokens)};
+  const cuuint32_t qbox[3] = {64, cuuint32_t(a.G), cuuint32_t(tile)};
   if (!attn::encode(&a.mk, kv->k, kv->e4m3, 4, dims, pitches, boxes) ||
       !attn::encode(&a.mv, kv->v, kv->e4m3, 4, dims, pitches, boxes) ||
       !attn::encode(&a.mq, const_cast<uint16_t*>(q), 0, 3, qdims, qpitches, qbox))

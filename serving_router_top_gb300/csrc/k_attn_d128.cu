@@ -1,5 +1,6 @@
-// moe_paged_attention for heads of 128 columns: the kernels of attn.cuh at their tiles of rows.
+// moe_paged_attention for heads of 128 columns: the kernels of attn.cuh at their tiles of rows, and of attn_chunk.cuh.
 #include "attn.cuh"
+#include "attn_chunk.cuh"
 
 namespace moe {
 namespace attn {
@@ -16,7 +17,7 @@ int launch_d128(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s) {
       case 16: return launch_one<128, 16, false>(a, ctas, s);
       case 32: return launch_one<128, 32, false>(a, ctas, s);
       case 64: return launch_one<128, 64, false>(a, ctas, s);
-      default: return launch_one<128, 128, false>(a, ctas, s);
+      default: return chunk::launch<128>(a, ctas, s);
     }
   }
 }
@@ -25,7 +26,7 @@ int opt_in_d128() {
   return opt_in<128, 16, false>() ||
                  opt_in<128, 32, false>() ||
                  opt_in<128, 64, false>() ||
-                 opt_in<128, 128, false>() ||
+                 chunk::opt_in<128>() ||
                  opt_in<128, 16, true>() ||
                  opt_in<128, 32, true>() ||
                  opt_in<128, 64, true>()

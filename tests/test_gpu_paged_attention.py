@@ -112,8 +112,58 @@ def test_many_units_of_many_tiles_beside_junk(D, G, n, e4m3):
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
-def test_any_scale(scale):
-    check(Paged([300], [3], 1, 128, 16), 8, scale=scale)
+@pytest.mark.parametrize("n", [3, 50])
+def test_any_scale(scale, n):
+    check(Paged([300], [n], 1, 128, 16), 8, scale=scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 3, 8, 20, 64])
+@pytest.mark.parametrize("window", [0, 70])
+def test_chunks(D, G, window):
+    """Row tiles of two 128s: whole and ragged ones, one of the two empty, several units and splits."""
+    per = 128 // G
+    ns = [2 * per, per + 1, per, 4 * per + 3, 1]
+    lens = [n + e for n, e in zip(ns, [700, 0, 129, 1300, 255])]
+    check(Paged(lens, ns, 2, D, 32, lead=3, seed=G), 2 * G, window)
+
+
+def test_chunks_with_peaked_scores():
+    check(Paged([900, 600], [90, 300], 2, 128, 32, seed=8, k_std=3.0), 16, q_std=8.0)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_a_chunk_s_token_does_not_see_does_not_reach_it(value, window, D):
+    P = Paged([300], [100], 1, D, 16)  # positions 200 .. 299, 8 heads: rows of both tiles
+    for at in (250, 299, 130):
+        P.v[int(P.table[0, at // 16]), 0, at % 16, at % D] = value
+    q = strided_rows(P.T, 8, D, 0, torch.Generator().manual_seed(0))
+    o = run(P, q, 8, 0.1, window).cpu().double()
+    ref, tol = attention_ref(P, q, 8, 0.1, window)
+    near = (o - ref).abs() <= tol
+    for at in (250, 299, 130):
+        rows = [i for i in range(100) if at <= 200 + i and not (window and at <= 200 + i - window)]
+        others = [i for i in range(100) if i not in rows]
+        assert near[others][..., at % D].all()
+        if rows:
+            assert not o[rows][..., at % D].isfinite().any()
+    clean = torch.ones(D, dtype=torch.bool)
+    clean[[at % D for at in (250, 299, 130)]] = False
+    assert near[..., clean].all()
+
+
+def test_chunks_give_the_same_bits_every_time():
+    P = Paged([4000, 500], [333, 200], 2, 128, 64)
+    pages, bt = P.device()
+    q = strided_rows(P.T, 16, 128, 0, torch.Generator().manual_seed(0)).cuda()
+    ws, first, o = moe.AttnWorkspace(16, 2, 128), torch.empty_like(q), torch.empty_like(q)
+    moe.moe_paged_attention(pages, bt, q, first, ws, 0.1)
+    for _ in range(10):
+        moe.moe_paged_attention(pages, bt, q, o, ws, 0.1)
+        assert torch.equal(o, first)
+    assert moe.moe_attn_sync_status(ws) == moe.MOE_OK
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
