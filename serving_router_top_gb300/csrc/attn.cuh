@@ -456,6 +456,31 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= kMisc, "misc");
 
+// Whether a key's row of N columns in a slot has a value that is not finite: 0 times it is NaN.
+template <int N>
+__device__ __forceinline__ bool not_finite(const uint8_t* slot, int key) {
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 t = zero;
+#pragma unroll 4
+  for (int c = 0; c < N / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(slot + (c / 8) * (kKeys * 128) + sw128(key, c % 8));
+    t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, t);
+    t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, t);
+    t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, t);
+    t = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, t);
+  }
+  return __hisnan(t.x) || __hisnan(t.y);
+}
+// Those values become zeros.
+template <int N>
+__device__ __forceinline__ void drop_not_finite(uint8_t* slot, int key) {
+#pragma unroll 1
+  for (int c = 0; c < N; ++c) {
+    uint16_t* v = reinterpret_cast<uint16_t*>(slot + (c / 64) * (kKeys * 128) + sw128(key, c % 64 / 8)) + c % 8;
+    if ((*v & 0x7f80u) == 0x7f80u) *v = 0;
+  }
+}
+
 // A place in a ring of N slots.
 template <int N>
 struct Ring {
@@ -887,28 +912,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
               wait(&ms.full[slot], uint32_t((at + hh) / C::NS) & 1, fail);
               if (c0 > 0 || !(gone || some)) continue;
               uint8_t* row = ring + slot * C::SLOT;
-              __nv_bfloat162 nan2 = __floats2bfloat162_rn(0.f, 0.f);
+              if (gone) {
 #pragma unroll 4
-              for (int c = 0; c < C::DS / 8; ++c) {
-                uint4* v = reinterpret_cast<uint4*>(row + (c / 8) * (kKeys * 128) + sw128(krow, c % 8));
-                if (gone) {
-                  *v = make_uint4(0, 0, 0, 0);
-                } else {
-                  const uint4 x = *v;
-                  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, nan2);
-                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, nan2);
-                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, nan2);
-                  nan2 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, nan2);
-                }
-              }
-              if (__hisnan(nan2.x) || __hisnan(nan2.y)) {
+                for (int c = 0; c < C::DS / 8; ++c)
+                  *reinterpret_cast<uint4*>(row + (c / 8) * (kKeys * 128) + sw128(krow, c % 8)) = make_uint4(0, 0, 0, 0);
+              } else if (not_finite<C::DS>(row, krow)) {
                 bad = true;
-#pragma unroll 1
-                for (int c = 0; c < C::DS; ++c) {
-                  uint16_t* v = reinterpret_cast<uint16_t*>(row + (c / 64) * (kKeys * 128) + sw128(krow, c % 64 / 8)) + c % 8;
-                  if ((*v & 0x7f80u) == 0x7f80u) *v = 0;
-                }
+                drop_not_finite<C::DS>(row, krow);
               }
             }
             if (mixed) {
@@ -1041,7 +1051,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 // this takes 3.
 constexpr int kJoinThreads = 128;
 constexpr int kMaxRuns = 512;
-constexpr int join_y(int nr) { return nr > 32 ? 8 : nr / 4; }
+constexpr int join_y(int nr) { return nr > 64 ? 16 : nr > 32 ? 8 : nr / 4; }
 template <int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ Args a) {
   constexpr int L = D / 4, W = kJoinThreads / 32, P = 8;  // four columns a lane; pieces in flight

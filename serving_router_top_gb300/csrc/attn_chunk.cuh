@@ -240,7 +240,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
       const float factor = a.scale * 1.4426950408889634f;
       const int mine = x * half + krow / a.G;  // the row's token in its unit
       float m = kUnset, l = 0.f;
-      int k = 0;  // tiles of this row tile
+      int spoiled_key0 = 0;
+      int k = 0;         // tiles of this row tile
+      int spoiled = -1;  // a tile that may have lost values that are not finite, once its product is done
+      // Adds them to this row where it sees their keys.
+      auto restore = [&]() {
+        const int nbad = *const_cast<volatile int*>(&ms.nbad[spoiled & 3]);
+        const int pos = min(w.r.pos0 + w.s.i0 + mine, w.r.pos0 + w.s.i1);
+#pragma unroll 1
+        for (int e = 0; e < nbad; ++e) {
+          const int key = spoiled_key0 + ms.bad[spoiled & 3][e];
+          const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (key >> a.kv.page_shift)];
+          const uint16_t* v = reinterpret_cast<const uint16_t*>(
+              a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
+              (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride);
+          const bool sees = key <= pos && (a.window <= 0 || key > pos - a.window);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            ld16(to + c, o);
+            ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float add = bf16_bits_to_f32(v[c + i]);
+              if (sees && !isfinite(add)) o[i] += add;
+            }
+            st16(to + c, o);
+          }
+        }
+        if (nbad) st_wait();
+        spoiled = -1;
+      };
       if (tid == 0) a.join[run] = join_record<V>(a, plan, w);
 #pragma unroll 1
       for (int n = 0; n < count; ++n) {
@@ -254,6 +284,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
           const bool whole = key0 + kKeys <= min(oldest + 1, cap) && (a.window <= 0 || key0 > newest - a.window);
           wait(&ms.sfull[x], k & 1, fail);
           tc_after();
+          if (spoiled >= 0) restore();  // S follows the product of the tile before it
           float s[kKeys];
 #pragma unroll
           for (int i = 0; i < kKeys; i += 16) ld16(ts + i, s + i);
@@ -320,14 +351,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
 #pragma unroll 4
               for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint4*>(row + (c / 8) * (kKeys * 128) + sw128(krow, c % 8)) = make_uint4(0, 0, 0, 0);
-            } else if (some) {
-              bool bad = false;
-#pragma unroll 1
-              for (int c = 0; c < D; ++c) {
-                uint16_t* v = reinterpret_cast<uint16_t*>(row + (c / 64) * (kKeys * 128) + sw128(krow, c % 64 / 8)) + c % 8;
-                if ((*v & 0x7f80u) == 0x7f80u) *v = 0, bad = true;
-              }
-              if (bad) ms.bad[n & 3][atomicAdd(&ms.nbad[n & 3], 1)] = uint8_t(krow);
+            } else if (some && not_finite<D>(row, krow)) {
+              drop_not_finite<D>(row, krow);
+              ms.bad[n & 3][atomicAdd(&ms.nbad[n & 3], 1)] = uint8_t(krow);
             }
             proxy_fence();
             if (mixed) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
@@ -336,37 +362,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
           tc_before();
           __syncwarp();
           if (lane == 0) arrive(&ms.pfull[x]);
-          const bool last = w.j + 1 == w.jend;
-          if (mixed || last) {
+          if (mixed) spoiled = n, spoiled_key0 = key0;
+          if (w.j + 1 == w.jend) {
             wait(&ms.pvdone[x], k & 1, fail);
             tc_after();
-          }
-          if (mixed) {
-            const int nbad = *const_cast<volatile int*>(&ms.nbad[n & 3]);
-#pragma unroll 1
-            for (int e = 0; e < nbad; ++e) {
-              const int key = key0 + ms.bad[n & 3][e];
-              const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (key >> a.kv.page_shift)];
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(
-                  a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
-                  (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride);
-              const bool sees = key <= pos && (a.window <= 0 || key > pos - a.window);
-#pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                float o[16];
-                ld16(to + c, o);
-                ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float add = bf16_bits_to_f32(v[c + i]);
-                  if (sees && !isfinite(add)) o[i] += add;
-                }
-                st16(to + c, o);
-              }
-            }
-            if (nbad) st_wait();
-          }
-          if (last) {
+            if (mixed) restore();
             // ---- the piece is done
             const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
             const int unit_row = x * half * a.G + krow, rows = min(half, w.s.i1 - w.s.i0 + 1 - x * half) * a.G;
