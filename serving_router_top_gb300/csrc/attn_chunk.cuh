@@ -66,6 +66,24 @@ __device__ __forceinline__ void st16u(uint32_t t, const uint32_t* v) {
       : "memory");
 }
 
+// Of four lanes with four groups of four values each: lane i gets the lanes' groups i, in their order.
+__device__ __forceinline__ void turn4(float (&v)[16], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (!(g & d)) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // this lane's group that belongs to the other one, against the other's
+          const float give = up ? v[4 * g + i] : v[4 * (g | d) + i];
+          const float got = __shfl_xor_sync(0xffffffffu, give, d);
+          if (up) v[4 * g + i] = got;
+          else v[4 * (g | d) + i] = got;
+        }
+      }
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_constant__ Args a) {
   using C = Cfg<D>;
@@ -370,27 +388,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
             // ---- the piece is done
             const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
             const int unit_row = x * half * a.G + krow, rows = min(half, w.s.i1 - w.s.i0 + 1 - x * half) * a.G;
-            const bool live = krow < rows;
-            const long long part = (2ll * run + (head ? 0 : 1)) * 256 + unit_row;
-            if (split && live) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m, l);
-            const float inv = l == 0.f ? 0.f : 1.f / l;  // a sum of zero is a row that sees no key; its O is zeros
-            uint16_t* out = a.o + (long long)(w.r.s0 + w.s.i0 + mine) * a.os + (long long)(w.h * a.G + krow % a.G) * D;
+            const long long part = (2ll * run + (head ? 0 : 1)) * kChunkRows + unit_row;
+            if (split && krow < rows) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m, l);
+            const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a sum of zero is a row that sees no key; its O is zeros
+            unsigned long long row = reinterpret_cast<unsigned long long>(a.part + part * D);
+            if (!split)
+              row = reinterpret_cast<unsigned long long>(a.o + (long long)(w.r.s0 + w.s.i0 + mine) * a.os +
+                                                         (long long)(w.h * a.G + krow % a.G) * D);
+            if (krow >= rows) row = 0;
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               float o[16];
               ld16(to + c, o);
               ld_wait();
-              if (!live) continue;
-              if (split) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                  *reinterpret_cast<float4*>(a.part + part * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-              } else {
-                uint32_t u[8];
+              for (int i = 0; i < 16; ++i) o[i] *= inv;
+              // Four lanes turn their four rows' pieces round and write each row's together: a row a
+              // thread, 16 bytes at a time, took 10000 clocks.
+              turn4(o, lane);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = pack2(o[2 * i] * inv, o[2 * i + 1] * inv);
-                reinterpret_cast<uint4*>(out + c)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-                reinterpret_cast<uint4*>(out + c)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+              for (int r = 0; r < 4; ++r) {  // row r of the four, columns c + 4 (lane % 4) ..
+                const unsigned long long at = __shfl_sync(0xffffffffu, row, lane / 4 * 4 + r);
+                if (!at) continue;
+                if (split)
+                  *reinterpret_cast<float4*>(at + (c + lane % 4 * 4) * 4) = make_float4(o[4 * r], o[4 * r + 1], o[4 * r + 2], o[4 * r + 3]);
+                else
+                  *reinterpret_cast<uint2*>(at + (c + lane % 4 * 4) * 2) = make_uint2(pack2(o[4 * r], o[4 * r + 1]), pack2(o[4 * r + 2], o[4 * r + 3]));
               }
             }
             tc_before();
