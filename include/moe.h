@@ -580,8 +580,10 @@ int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
  * Scores, softmax sums and outputs accumulate in fp32; the weights exp(s - m)
  * are rounded to 16 bits for the product with v.  A key in a page whose id is
  * outside [0, npages) reads as zeros and records MOE_ERANGE in the workspace's
- * error word; so does kv_len beyond page * table_stride, cut there.  The result
- * does not vary between runs.  scale finite; window >= 0, 0 for none.
+ * error word; so does kv_len beyond page * table_stride or 2^29, cut there.
+ * max_n only picks the kernel.  The result does not vary between runs.  scale
+ * finite; window >= 0, 0 for none.  Calls with (T + B) * Hkv * (page *
+ * table_stride / 128 + 4) < 2^31 are taken; larger ones may be MOE_EINVAL.
  * Asynchronous on `stream`; one stream drives a workspace at a time. */
 int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const uint16_t* q, long long q_stride, int Hq,
                         uint16_t* o, long long o_stride, float scale, int window, moe_attn_ws* ws,

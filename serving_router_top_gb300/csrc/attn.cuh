@@ -123,8 +123,11 @@ __device__ __forceinline__ Span span_of(const Req& r, int rt, int tokens, int wi
   s.nt = max((s.hi + kKeys - 1) / kKeys - s.tile0, 1);  // a tile even where nothing is seen: its rows get zeros
   return s;
 }
-__device__ __forceinline__ int cap_of(const KvView& kv) {
-  return int(min((long long)kv.table_stride << kv.page_shift, (long long)INT_MAX - kKeys));
+// Tokens that a request's pages hold, below kMaxTokens: sums of two positions and a window stay in 32 bits.
+constexpr int kMaxTokens = 1 << 29;
+__host__ __device__ inline int cap_of(const KvView& kv) {
+  const long long held = (long long)kv.table_stride << kv.page_shift;
+  return held < kMaxTokens ? int(held) : kMaxTokens;
 }
 // Tiles of a key head of a request, and its units.
 struct Load {
@@ -1046,67 +1049,97 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 }
 
 // Joins the pieces of a unit: o = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k, in the order of
-// the pieces.  CTA (c, y): the unit whose second piece is run c's first.  A warp takes a row, P
-// pieces at a time, so no warp waits for another: a CTA a row took 33 us for prompt chunks' 128 rows,
-// this takes 3.
+// the pieces.  CTA (c, y): the unit whose second piece is run c's first.  A warp takes R rows and P
+// pieces of each at a time (R P = 8 loads of 16 bytes in flight a lane), so no warp waits for another:
+// a CTA a row took 33 us for prompt chunks' 128 rows of 152 units, a row a warp 9.
 constexpr int kJoinThreads = 128;
 constexpr int kMaxRuns = 512;
 constexpr int join_y(int nr) { return nr > 64 ? 16 : nr > 32 ? 8 : nr / 4; }
-template <int D, int NR>
-__global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ Args a) {
-  constexpr int L = D / 4, W = kJoinThreads / 32, P = 8;  // four columns a lane; pieces in flight
-  pdl_trigger();
-  pdl_wait();
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int4 unit = __ldcg(a.join + c);
-  const int rows = unit.z, np = unit.w;  // pieces: the tail of run c - 1, then the heads of np - 1 runs
+
+template <int D, int NR, int R>
+__device__ __forceinline__ void join_rows(const Args& a, const int4& unit, int row0) {
+  constexpr int L = D / 4, P = 8 / R, C = (L + 31) / 32;  // four columns a lane
+  const int c = blockIdx.x, lane = threadIdx.x & 31, rows = unit.z, np = unit.w;
+  // pieces: the tail of run c - 1, then the heads of np - 1 runs
   auto place = [&](int k) { return (2ll * (c - 1 + k) + (k == 0 ? 1 : 0)) * NR; };
   const float2* ml = reinterpret_cast<const float2*>(a.ml);
-  constexpr int Y = join_y(NR);
-  for (int row = blockIdx.y * W + warp; row < rows; row += Y * W) {
-    float m = kUnset;
-    for (int k = lane; k < np; k += 32) m = fmaxf(m, __ldcg(&ml[place(k) + row]).x);
-    m = warp_max(m);
-    float l = 0.f;
-    float4 o[(L + 31) / 32];
+  float m[R], l[R];
+  float4 o[R][C];
 #pragma unroll
-    for (int i = 0; i < (L + 31) / 32; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < np; k0 += P) {
-      float2 mine = make_float2(kUnset, 0.f);  // of piece k0 + lane
-      if (lane < P && k0 + lane < np) mine = __ldcg(&ml[place(k0 + lane) + row]);
-      const float w = ex2(mine.x - m);
+  for (int r = 0; r < R; ++r) {
+    m[r] = kUnset;
+    l[r] = 0.f;
 #pragma unroll
-      for (int i = 0; i < (L + 31) / 32; ++i) {
-        const int col = i * 32 + lane;
-        float4 v[P];
+    for (int i = 0; i < C; ++i) o[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 + r < rows)
+      for (int k = lane; k < np; k += 32) m[r] = fmaxf(m[r], __ldcg(&ml[place(k) + row0 + r]).x);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) m[r] = warp_max(m[r]);
+  for (int k0 = 0; k0 < np; k0 += P) {
+    float2 mine[R];  // of piece k0 + lane
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mine[r] = make_float2(kUnset, 0.f);
+      if (lane < P && k0 + lane < np && row0 + r < rows) mine[r] = __ldcg(&ml[place(k0 + lane) + row0 + r]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int col = i * 32 + lane;
+      float4 v[R][P];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < P; ++k)
-          if (k0 + k < np && col < L)
-            v[k] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(k0 + k) + row) * D) + col);
+          if (k0 + k < np && col < L && row0 + r < rows)
+            v[r][k] = __ldcg(reinterpret_cast<const float4*>(a.part + (place(k0 + k) + row0 + r) * D) + col);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float w = ex2(mine[r].x - m[r]);
 #pragma unroll
         for (int k = 0; k < P; ++k)
-          if (k0 + k < np) {
+          if (k0 + k < np && row0 + r < rows) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
-            if (i == 0) l = fmaf(wk, __shfl_sync(0xffffffffu, mine.y, k), l);
+            if (i == 0) l[r] = fmaf(wk, __shfl_sync(0xffffffffu, mine[r].y, k), l[r]);
             if (col < L) {
-              o[i].x = fmaf(wk, v[k].x, o[i].x);
-              o[i].y = fmaf(wk, v[k].y, o[i].y);
-              o[i].z = fmaf(wk, v[k].z, o[i].z);
-              o[i].w = fmaf(wk, v[k].w, o[i].w);
+              o[r][i].x = fmaf(wk, v[r][k].x, o[r][i].x);
+              o[r][i].y = fmaf(wk, v[r][k].y, o[r][i].y);
+              o[r][i].z = fmaf(wk, v[r][k].z, o[r][i].z);
+              o[r][i].w = fmaf(wk, v[r][k].w, o[r][i].w);
             }
           }
       }
     }
-    const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
-    const float x = l == 0.f ? 0.f : vs / l;
-    const int i = row / a.G, g = row - i * a.G;
+  }
+  const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (row0 + r >= rows) break;
+    const float x = l[r] == 0.f ? 0.f : vs / l[r];
+    const int i = (row0 + r) / a.G, g = row0 + r - i * a.G;
     uint16_t* out = a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D;
 #pragma unroll
-    for (int j = 0; j < (L + 31) / 32; ++j) {
+    for (int j = 0; j < C; ++j) {
       const int col = j * 32 + lane;
       if (col < L)
-        reinterpret_cast<uint2*>(out)[col] = make_uint2(pack2(o[j].x * x, o[j].y * x), pack2(o[j].z * x, o[j].w * x));
+        reinterpret_cast<uint2*>(out)[col] =
+            make_uint2(pack2(o[r][j].x * x, o[r][j].y * x), pack2(o[r][j].z * x, o[r][j].w * x));
     }
+  }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ Args a) {
+  constexpr int W = join_y(NR) * kJoinThreads / 32;  // warps of a unit
+  pdl_trigger();
+  pdl_wait();
+  const int4 unit = __ldcg(a.join + blockIdx.x);
+  const int first = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  if (NR > W && unit.w <= 2) {  // more rows than warps, and few pieces
+    constexpr int R = NR / W > 4 ? 4 : NR / W;
+    for (int row = R * first; row < unit.z; row += R * W) join_rows<D, NR, R>(a, unit, row);
+  } else {
+    for (int row = first; row < unit.z; row += W) join_rows<D, NR, 1>(a, unit, row);
   }
 }
 

@@ -125,7 +125,7 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.o = o;
   a.os = T > 1 ? o_stride : width;
   a.G = Hq / kv->Hkv;
-  a.window = window;
+  a.window = window < attn::cap_of(a.kv) ? window : 0;  // one that holds every key is none
   const int tile = nr == attn::kChunkRows ? nr / 2 / a.G : nr / a.G;  // tokens of a row tile
   a.tokens = nr == attn::kChunkRows ? 2 * tile : tile;
   // the schedule counts in 31 bits: a unit has at most its request's tiles, and three more places

@@ -319,3 +319,28 @@ def test_refusals_with_a_workspace():
     for other in (moe.AttnWorkspace(4, 1, 64), moe.AttnWorkspace(4, 2, 128)):
         with pytest.raises((moe.MoeError, ValueError)):
             moe.moe_paged_attention(pages, bt, q, torch.empty_like(q), other, 1.0)
+
+
+def test_sizes_past_the_schedule_s_count_are_refused():
+    k = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda").expand(1, 1024, 1, 64).contiguous()
+    q = torch.zeros(64, 1024, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(1, 1 << 24, dtype=torch.int32, device="cuda")
+    ws = moe.AttnWorkspace(1024, 1024, 64)
+    bt = moe.KvBatch(torch.tensor([0, 64], dtype=torch.int32).cuda(), torch.tensor([64], dtype=torch.int32).cuda(), table,
+                     64, 64)
+    pages = moe.KvPages(k, k)
+    moe.moe_paged_attention(pages, bt, q, torch.empty_like(q), ws, 1.0)  # 2^24 tokens: within the count
+    assert moe.moe_attn_sync_status(ws) == moe.MOE_OK
+    c = pages.c
+    c.page, c.head_stride, c.tok_stride = 1 << 15, 64, 64 * 1024  # 2^39 tokens a table: refused before any launch
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_paged_attention(pages, bt, q, torch.empty_like(q), ws, 1.0)
+    assert e.value.code == moe.MOE_EINVAL
+
+
+@pytest.mark.parametrize("n", [2, 80])
+def test_a_window_that_holds_everything(n):
+    P = Paged([300], [n], 1, 64, 16)
+    q = strided_rows(n, 8, 64, 0, torch.Generator().manual_seed(0))
+    assert torch.equal(run(P, q, 8, 0.1, 0), run(P, q, 8, 0.1, (1 << 31) - 1))
+    assert torch.equal(run(P, q, 8, 0.1, 0), run(P, q, 8, 0.1, 300))
