@@ -31,7 +31,7 @@
 // Split.  Every (request, key head, row tile) is a unit: its tiles, and before
 // them a cost for its beginning and end (new queries, a maximum from scratch, an
 // output) counted in tiles.  All units of a call are laid end to end and cut
-// into equal runs, one per SM, whatever the lengths.  A run takes its units in
+// into equal runs, one or two per SM, whatever the lengths.  A run takes its units in
 // pieces; a piece that is not its whole unit leaves (m, sum, O) in the scratch,
 // and a second kernel joins the pieces of a unit in their order.
 #pragma once
@@ -49,8 +49,9 @@ constexpr float kUnset = -1e30f;              // m of a row that has seen no key
 constexpr float kMost = 256.0f;               // m is set again when a weight passes this
 constexpr float kLost = 0x1p-100f;            // sums from before m grew by this factor are nothing to those after
 constexpr unsigned long long kWaitNs = 1000000000ull;
-constexpr int kSmem = 232448;
-constexpr int kMisc = 5888;                   // barriers, row statistics, schedule
+constexpr int kSmem = 232448;                 // shared memory of one CTA on an SM, and of each of two
+constexpr int kSmem2 = 115712;
+constexpr int misc_bytes(int nr) { return (2176 + 28 * nr + 127) / 128 * 128; }  // barriers, row statistics, schedule
 
 struct Args {
   CUtensorMap mk, mv, mq;  // pools [page][head][place][column], query rows [token][head][column]
@@ -60,9 +61,9 @@ struct Args {
   int G, window, tokens;   // query heads a key head; visible keys (0: all); tokens in a row tile
   float scale;
   int32_t* err;
-  float* part;  // [2 * CTAs][NR][D] pieces: head piece of CTA c at 2c, tail piece at 2c + 1
-  float* ml;    // [2 * CTAs][NR][2] their m and sums
-  int4* join;   // [CTAs] where run c's first piece is the second of a unit: token, key head, rows, pieces (else 0)
+  float* part;  // [2 * runs][NR][D] pieces: head piece of run c at 2c, tail piece at 2c + 1
+  float* ml;    // [2 * runs][NR][2] their m and sums
+  int4* join;   // [runs] where run c's first piece is the second of a unit: token, key head, rows, pieces (else 0)
 };
 
 template <int D, int NR, bool E4M3>
@@ -73,12 +74,17 @@ struct Cfg {
   static constexpr int RAW = E4M3 ? kKeys * DS : 0;  // a slot's codes
   static constexpr int QBYTES = NR * D * 2;
   static constexpr int PBYTES = kKeys * NR * 2;
-  static constexpr int FREE = kSmem - kMisc - 2 * PBYTES;
+  // Two CTAs to an SM where each still has three slots of 128 columns or five of 64: they hide each
+  // other's waits (a tile's softmax is a chain of about 1100 clocks whatever its rows, an SM's share of
+  // the memory brings 64 columns' 32 KB in 1400) and the ends of units.
+  static constexpr int OCC = !E4M3 && (kSmem2 - misc_bytes(NR) - 2 * PBYTES - QBYTES) / SLOT >= (D < 128 ? 5 : 3) && H == 1 ? 2 : 1;
+  static constexpr int SMEM = OCC == 2 ? kSmem2 : kSmem;
+  static constexpr int FREE = SMEM - misc_bytes(NR) - 2 * PBYTES;
   // E4M3: three slots of bf16 for each 128 columns, all other room for codes on their way
   static constexpr int NSV = D < 128 ? 6 : 3;
   static constexpr int VG = !E4M3 ? 0 : NR > 32 ? 1 : 2;  // groups of four converting warps
   static constexpr int places(int qb) { return (FREE - qb * QBYTES - NSV * SLOT) / (RAW + 1); }
-  static constexpr int QB = E4M3 ? (places(2) >= NSV + 2 ? 2 : 1) : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
+  static constexpr int QB = OCC == 2 ? 1 : E4M3 ? (places(2) >= NSV + 2 ? 2 : 1) : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
   static constexpr int NS0 = E4M3 ? NSV : (FREE - QB * QBYTES) / SLOT, NS = NS0 > 16 ? 16 : NS0;
   static constexpr int NRAW0 = E4M3 ? places(QB) : 0, NRAW = NRAW0 > 16 ? 16 : NRAW0;
   static constexpr int CW = NR < 32 ? NR : 32;                 // rows a softmax warp holds
@@ -444,20 +450,20 @@ __device__ __forceinline__ int4 join_record(const Args& a, const Plan& p, const 
   return make_int4(w.r.s0 + w.s.i0, w.h, (w.s.i1 - w.s.i0 + 1) * a.G, run_of(p.total, p.runs, at + w.s.nt - 1) - run + 2);
 }
 
+template <int NR>
 struct Misc {
   uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
   PlanShared plan;
-  alignas(16) float m[128];      // of the rows, log2 units
-  alignas(16) float alpha[128];
-  float inv[128];            // 1 / sum of a finished piece's rows
-  float red[4][128];
+  alignas(16) float m[NR];   // of the rows, log2 units
+  alignas(16) float alpha[NR];
+  float inv[NR];             // 1 / sum of a finished piece's rows
+  float red[4][NR];
   int page[2][kKeys];        // pages of a tile's boxes, for keys and for values
   int nbad;
   uint8_t bad[kKeys];  // keys of a tile with values that are not finite
 };
-static_assert(sizeof(Misc) <= kMisc, "misc");
 
 // Whether a key's row of N columns in a slot has a value that is not finite: 0 times it is NaN.
 template <int N>
@@ -517,14 +523,16 @@ __device__ __forceinline__ float transpose_sum(float (&v)[W], int lane) {
 }
 
 template <int D, int NR, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::OCC) k_attn(const __grid_constant__ Args a) {
   using C = Cfg<D, NR, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* sq = ring + C::NS * C::SLOT;
   uint8_t* sp = sq + C::QB * C::QBYTES;
   uint8_t* raw = sp + 2 * C::PBYTES;
-  Misc& ms = *reinterpret_cast<Misc*>(raw + C::NRAW * C::RAW);
+  using Ms = Misc<NR>;
+  static_assert(sizeof(Ms) <= misc_bytes(NR), "misc");
+  Ms& ms = *reinterpret_cast<Ms*>(raw + C::NRAW * C::RAW);
   volatile int* fail = &ms.fail;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr int kMmaWarp = C::SW, kLoadWarp = C::SW + 1, kSoft = 32 * C::SW;  // loads: keys, then values
@@ -1053,7 +1061,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, 1) k_attn(const __g
 // pieces of each at a time (R P = 8 loads of 16 bytes in flight a lane), so no warp waits for another:
 // a CTA a row took 33 us for prompt chunks' 128 rows of 152 units, a row a warp 9.
 constexpr int kJoinThreads = 128;
-constexpr int kMaxRuns = 512;
 constexpr int join_y(int nr) { return nr > 64 ? 16 : nr > 32 ? 8 : nr / 4; }
 
 template <int D, int NR, int R>
@@ -1152,9 +1159,10 @@ inline int row_tile(int D, int e4m3, int G, int n) {
 }
 
 template <int D, int NR, bool E4M3>
-int launch_one(const Args& a, int ctas, cudaStream_t s) {
+int launch_one(const Args& a, int sms, cudaStream_t s) {
   using C = Cfg<D, NR, E4M3>;
-  if (launch_pdl(k_attn<D, NR, E4M3>, dim3(ctas), dim3(C::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
+  const int ctas = sms * C::OCC;
+  if (launch_pdl(k_attn<D, NR, E4M3>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, a) != cudaSuccess) return MOE_ECUDA;
   if (launch_pdl(k_join<D, NR>, dim3(ctas, join_y(NR)), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
   return MOE_OK;
 }
@@ -1162,7 +1170,8 @@ template <int D, int NR, bool E4M3>
 int opt_in() {
   // the join keeps the split of L1 and shared memory that the kernel before it had
   return cudaFuncSetAttribute(k_join<D, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
-                 cudaFuncSetAttribute(k_attn<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
+                 cudaFuncSetAttribute(k_attn<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NR, E4M3>::SMEM) ==
+                     cudaSuccess
              ? MOE_OK
              : MOE_ECUDA;
 }

@@ -26,7 +26,7 @@ constexpr float kGrow = 8.0f;  // log2
 template <int D>
 struct Cfg {
   static constexpr int SLOT = kKeys * D * 2, QTILE = 128 * D * 2;
-  static constexpr int NS0 = (kSmem - kMisc - 2 * QTILE) / SLOT, NS = NS0 > 8 ? 8 : NS0 / 2 * 2;  // even: K and V in turn
+  static constexpr int NS0 = (kSmem - misc_bytes(128) - 2 * QTILE) / SLOT, NS = NS0 > 8 ? 8 : NS0 / 2 * 2;  // even: K and V in turn
   static constexpr int MMA = 8, LOAD = 9, THREADS = 32 * 11;  // warps 0-3 and 4-7: softmax of a row tile each
   static constexpr int V = SLOT >= 32768 ? 2 : 3;             // as in attn.cuh, by the bytes of a tile
   static_assert(NS >= 4, "shared memory of an SM");
@@ -41,7 +41,7 @@ struct Misc {
   int nbad[4];  // keys of a tile with values that are not finite, of four tiles in turn
   uint8_t bad[4][kKeys];
 };
-static_assert(sizeof(Misc) <= kMisc, "misc");
+static_assert(sizeof(Misc) <= misc_bytes(128), "misc");
 
 // Four steps of 16 keys: A (P) from tensor memory, eight columns a step, B (V) 2048 bytes on.
 __device__ __forceinline__ void mma4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {

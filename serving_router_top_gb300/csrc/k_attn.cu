@@ -4,7 +4,7 @@
 #include "attn.cuh"
 
 struct moe_attn_ws {
-  int Hq, Hkv, D, ctas;
+  int Hq, Hkv, D, sms;
   int32_t* error;
   float *part, *ml;
   int4* join;
@@ -12,9 +12,9 @@ struct moe_attn_ws {
 
 namespace moe {
 namespace attn {
-int launch_d64(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
-int launch_d128(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
-int launch_d256(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s);
+int launch_d64(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
+int launch_d128(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
+int launch_d256(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
 int opt_in_d64();
 int opt_in_d128();
 int opt_in_d256();
@@ -64,10 +64,11 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
     free(w);
     return MOE_ECUDA;
   }
-  w->ctas = sms < attn::kMaxRuns ? sms : attn::kMaxRuns;  // one CTA per SM
-  const size_t rows = 2 * size_t(w->ctas) * (D == 256 ? 64 : attn::kChunkRows);
+  w->sms = sms;
+  const size_t runs = 2 * size_t(sms);
+  const size_t rows = 2 * runs * (D == 256 ? 64 : attn::kChunkRows);
   const size_t o_part = 256, o_ml = o_part + rows * D * 4, o_join = o_ml + rows * 8;
-  const size_t bytes = o_join + size_t(w->ctas) * 16;
+  const size_t bytes = o_join + runs * 16;
   uint8_t* base = nullptr;
   if (cudaMalloc(&base, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -151,8 +152,8 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.join = ws->join;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (kv->D) {
-    case 64: return attn::launch_d64(a, kv->e4m3, nr, ws->ctas, s);
-    case 128: return attn::launch_d128(a, kv->e4m3, nr, ws->ctas, s);
-    default: return attn::launch_d256(a, kv->e4m3, nr, ws->ctas, s);
+    case 64: return attn::launch_d64(a, kv->e4m3, nr, ws->sms, s);
+    case 128: return attn::launch_d128(a, kv->e4m3, nr, ws->sms, s);
+    default: return attn::launch_d256(a, kv->e4m3, nr, ws->sms, s);
   }
 }

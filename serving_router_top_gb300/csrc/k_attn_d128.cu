@@ -5,19 +5,19 @@
 namespace moe {
 namespace attn {
 
-int launch_d128(const Args& a, int e4m3, int nr, int ctas, cudaStream_t s) {
+int launch_d128(const Args& a, int e4m3, int nr, int sms, cudaStream_t s) {
   if (e4m3) {
     switch (nr) {
-      case 16: return launch_one<128, 16, true>(a, ctas, s);
-      case 32: return launch_one<128, 32, true>(a, ctas, s);
-      default: return launch_one<128, 64, true>(a, ctas, s);
+      case 16: return launch_one<128, 16, true>(a, sms, s);
+      case 32: return launch_one<128, 32, true>(a, sms, s);
+      default: return launch_one<128, 64, true>(a, sms, s);
     }
   } else {
     switch (nr) {
-      case 16: return launch_one<128, 16, false>(a, ctas, s);
-      case 32: return launch_one<128, 32, false>(a, ctas, s);
-      case 64: return launch_one<128, 64, false>(a, ctas, s);
-      default: return chunk::launch<128>(a, ctas, s);
+      case 16: return launch_one<128, 16, false>(a, sms, s);
+      case 32: return launch_one<128, 32, false>(a, sms, s);
+      case 64: return launch_one<128, 64, false>(a, sms, s);
+      default: return chunk::launch<128>(a, sms, s);
     }
   }
 }
