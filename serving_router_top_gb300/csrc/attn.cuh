@@ -1150,6 +1150,82 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(const __grid_constant__ A
   }
 }
 
+// The same for 16-row tiles and units of many pieces: a CTA takes a row, its warps take eight pieces in
+// turn and the first adds up what they found.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_join_many(const __grid_constant__ Args a) {
+  constexpr int L = D / 4, W = kJoinThreads / 32, P = 8, C = (L + 31) / 32, NR = 16;
+  __shared__ float4 acc[W][L];
+  __shared__ float2 stat[W];
+  pdl_trigger();
+  pdl_wait();
+  const int4 unit = __ldcg(a.join + blockIdx.x);
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, np = unit.w;
+  for (int row = blockIdx.y; row < unit.z; row += gridDim.y) {
+    auto place = [&](int k) { return (2ll * (c - 1 + k) + (k == 0 ? 1 : 0)) * NR + row; };
+    const float2* ml = reinterpret_cast<const float2*>(a.ml);
+    float m = kUnset, l = 0.f;  // of this warp's pieces
+    float4 o[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = P * warp; k0 < np; k0 += P * W) {
+      float2 mine = make_float2(kUnset, 0.f);
+      if (lane < P && k0 + lane < np) mine = __ldcg(&ml[place(k0 + lane)]);
+      float4 v[C][P];
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          if (k0 + k < np && i * 32 + lane < L)
+            v[i][k] = __ldcg(reinterpret_cast<const float4*>(a.part + place(k0 + k) * D) + i * 32 + lane);
+      const float top = fmaxf(m, warp_max(mine.x)), keep = ex2(m - top), w = ex2(mine.x - top);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] = make_float4(o[i].x * keep, o[i].y * keep, o[i].z * keep, o[i].w * keep);
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        if (k0 + k < np) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          l = fmaf(wk, __shfl_sync(0xffffffffu, mine.y, k), l);
+#pragma unroll
+          for (int i = 0; i < C; ++i)
+            if (i * 32 + lane < L) {
+              o[i].x = fmaf(wk, v[i][k].x, o[i].x);
+              o[i].y = fmaf(wk, v[i][k].y, o[i].y);
+              o[i].z = fmaf(wk, v[i][k].z, o[i].z);
+              o[i].w = fmaf(wk, v[i][k].w, o[i].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (i * 32 + lane < L) acc[warp][i * 32 + lane] = o[i];
+    if (lane == 0) stat[warp] = make_float2(m, l);
+    __syncthreads();
+    if (threadIdx.x < L) {
+      float top = kUnset;
+      for (int w = 0; w < W; ++w) top = fmaxf(top, stat[w].x);
+      l = 0.f;
+      float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < W; ++w) {
+        const float f = ex2(stat[w].x - top);
+        const float4 v = acc[w][threadIdx.x];
+        l = fmaf(f, stat[w].y, l);
+        r.x = fmaf(f, v.x, r.x);
+        r.y = fmaf(f, v.y, r.y);
+        r.z = fmaf(f, v.z, r.z);
+        r.w = fmaf(f, v.w, r.w);
+      }
+      const float vs = a.kv.v_scale ? a.kv.v_scale[unit.y] : 1.f, x = l == 0.f ? 0.f : vs / l;
+      const int i = row / a.G, g = row - i * a.G;
+      uint16_t* out = a.o + (long long)(unit.x + i) * a.os + (long long)(unit.y * a.G + g) * D;
+      reinterpret_cast<uint2*>(out)[threadIdx.x] = make_uint2(pack2(r.x * x, r.y * x), pack2(r.z * x, r.w * x));
+    }
+    __syncthreads();
+  }
+}
+
 // Rows of a unit for calls of about n new tokens a request and G query heads a key head: the smallest
 // tile that holds a request's rows, and above 64 rows the two 128-row tiles of attn_chunk.cuh where it
 // applies.  A tile holds the heads of whole tokens.
@@ -1161,15 +1237,22 @@ inline int row_tile(int D, int e4m3, int G, int n) {
 template <int D, int NR, bool E4M3>
 int launch_one(const Args& a, int sms, cudaStream_t s) {
   using C = Cfg<D, NR, E4M3>;
-  const int ctas = sms * C::OCC;
+  // So few units that each is cut into more than sixteen pieces even at one run an SM: one run then, as
+  // every further piece is another to join, and the join for many.  One token over 131071 keys: 52.4 us
+  // at two runs an SM, 49.6 at one, 46.9 with this join.
+  const bool many = NR == 16 && (long long)a.kv.B * a.kv.Hkv * 16 < sms && cap_of(a.kv) > 16 * kKeys;
+  const int ctas = many ? sms : sms * C::OCC;
   if (launch_pdl(k_attn<D, NR, E4M3>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, a) != cudaSuccess) return MOE_ECUDA;
-  if (launch_pdl(k_join<D, NR>, dim3(ctas, join_y(NR)), dim3(kJoinThreads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+  const cudaError_t e = NR == 16 && many ? launch_pdl(k_join_many<D>, dim3(ctas, a.G < 16 ? a.G : 16), dim3(kJoinThreads), 0, s, a)
+                                         : launch_pdl(k_join<D, NR>, dim3(ctas, join_y(NR)), dim3(kJoinThreads), 0, s, a);
+  if (e != cudaSuccess) return MOE_ECUDA;
   return MOE_OK;
 }
 template <int D, int NR, bool E4M3>
 int opt_in() {
   // the join keeps the split of L1 and shared memory that the kernel before it had
   return cudaFuncSetAttribute(k_join<D, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
+                 cudaFuncSetAttribute(k_join_many<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
                  cudaFuncSetAttribute(k_attn<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NR, E4M3>::SMEM) ==
                      cudaSuccess
              ? MOE_OK

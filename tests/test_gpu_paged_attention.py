@@ -59,6 +59,9 @@ CASES = [
     ([200, 300], [2, 2], 10, 2, 128, 32, 128, False, "hnd"),
     ([9000], [1], 4, 1, 128, 64, 0, False, "hnd"),
     ([9001], [4], 8, 1, 256, 64, 0, True, "hnd"),
+    ([9000], [1], 12, 1, 256, 64, 0, False, "hnd"),
+    ([30000], [1], 10, 1, 256, 64, 0, True, "kv"),
+    ([30011], [2], 12, 2, 64, 64, 0, False, "nhd"),
     ([7, 130, 12, 300, 1, 64, 90, 2] * 20, [1, 4, 2, 1, 1, 3, 1, 2] * 20, 8, 2, 64, 16, 0, False, "hnd"),
 ]
 
