@@ -18,15 +18,25 @@
 // after them instead of a maximum over all threads before them.  Sums are kept
 // by each thread for its keys and added up once, at the end of a piece.
 //
-// Roundings.  Scores and sums are fp32.  The operands are bf16: q and a bf16
-// cache as they are, E4M3 codes exactly, and P rounded once, half a unit of
-// 2^-8 relative to each weight however small (f16 would keep three bits more
-// of the large weights and lose those 2^-32 below the largest).
+// Roundings.  Scores and sums are fp32.  A bf16 cache and q are the operands as
+// they are; P is rounded once to bf16, half a unit of 2^-8 relative to each
+// weight however small (f16 would keep three bits more of the large weights and
+// lose those 2^-32 below the largest).
+//
+// E4M3 caches.  Keys go to the tensor core as they are, against q in two E4M3
+// terms: q 2^e = t0 + t1 / 32, with 2^e such that the row's largest is in
+// [2^7, 2^8).  A bf16 value has 8 significant bits and a term takes 4, so the two
+// are exact for what is within 2^-14 of the row's largest and off by 2^-22 of it
+// below.  The terms are 2 NR rows of one product, whose halves the softmax adds.
+// Values become bf16, exactly: as many terms of P would lose weights 2^-23 below
+// the largest, thousands of which can be half the sum.  With keys converted too,
+// the conversions' 128 KB in and out of shared memory a tile of 256 columns took
+// longer than the memory: 16 windows of up to 32768 keys 50.7 us, now QQQ us.
 //
 // Movement.  One warp asks the copy engine for the tiles (a page, or 128 keys of
 // a larger one, by 64 columns a box, swizzled for the tensor core); pages that
 // are not there are asked for past the pool's end and read as zeros.  E4M3
-// tiles land as they are and are turned into bf16 by four warps of their own.
+// values land as they are and are turned into bf16 by four warps of their own.
 //
 // Split.  Every (request, key head, row tile) is a unit: its tiles, and before
 // them a cost for its beginning and end (new queries, a maximum from scratch, an
@@ -51,13 +61,14 @@ constexpr float kLost = 0x1p-100f;            // sums from before m grew by this
 constexpr unsigned long long kWaitNs = 1000000000ull;
 constexpr int kSmem = 232448;                 // shared memory of one CTA on an SM, and of each of two
 constexpr int kSmem2 = 115712;
-constexpr int misc_bytes(int nr) { return (2176 + 28 * nr + 127) / 128 * 128; }  // barriers, row statistics, schedule
+constexpr int misc_bytes(int nr) { return (2192 + 60 * nr + 127) / 128 * 128; }  // barriers, row statistics, schedule
 
 struct Args {
   CUtensorMap mk, mv, mq;  // pools [page][head][place][column], query rows [token][head][column]
   KvView kv;
+  const uint16_t* q;
   uint16_t* o;
-  long long os;
+  long long qs, os;
   int G, window, tokens;   // query heads a key head; visible keys (0: all); tokens in a row tile
   float scale;
   int32_t* err;
@@ -72,7 +83,7 @@ struct Cfg {
   static constexpr int H = D / DS;                   // slots of a key or value tile
   static constexpr int SLOT = kKeys * DS * 2;
   static constexpr int RAW = E4M3 ? kKeys * DS : 0;  // a slot's codes
-  static constexpr int QBYTES = NR * D * 2;
+  static constexpr int QBYTES = 2 * NR * D;          // the rows in bf16, or their two E4M3 terms
   static constexpr int PBYTES = kKeys * NR * 2;
   // Two CTAs to an SM where each still has three slots of 128 columns or five of 64: they hide each
   // other's waits (a tile's softmax is a chain of about 1100 clocks whatever its rows, an SM's share of
@@ -80,26 +91,24 @@ struct Cfg {
   static constexpr int OCC = !E4M3 && (kSmem2 - misc_bytes(NR) - 2 * PBYTES - QBYTES) / SLOT >= (D < 128 ? 5 : 3) && H == 1 ? 2 : 1;
   static constexpr int SMEM = OCC == 2 ? kSmem2 : kSmem;
   static constexpr int FREE = SMEM - misc_bytes(NR) - 2 * PBYTES;
-  // E4M3: three slots of bf16 for each 128 columns, all other room for codes on their way
-  static constexpr int NSV = D < 128 ? 6 : 3;
-  static constexpr int VG = !E4M3 ? 0 : NR > 32 ? 1 : 2;  // groups of four converting warps
-  static constexpr int places(int qb) { return (FREE - qb * QBYTES - NSV * SLOT) / (RAW + 1); }
-  static constexpr int QB = OCC == 2 ? 1 : E4M3 ? (places(2) >= NSV + 2 ? 2 : 1) : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
-  static constexpr int NS0 = E4M3 ? NSV : (FREE - QB * QBYTES) / SLOT, NS = NS0 > 16 ? 16 : NS0;
-  static constexpr int NRAW0 = E4M3 ? places(QB) : 0, NRAW = NRAW0 > 16 ? 16 : NRAW0;
+  // E4M3: a ring of bf16 values, the rest for keys and values as they come
+  static constexpr int NV = 2;
+  static constexpr int codes(int qb) { return E4M3 ? (FREE - qb * QBYTES - NV * SLOT) / (RAW + !E4M3) : 0; }
+  static constexpr int QB = OCC == 2 ? 1 : E4M3 ? (codes(2) >= 5 ? 2 : 1) : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
+  static constexpr int NS0 = E4M3 ? NV : (FREE - QB * QBYTES) / SLOT, NS = NS0 > 16 ? 16 : NS0;
+  static constexpr int NK0 = (codes(QB) + 1) / 2, NK = NK0 > 8 ? 8 : NK0, NR0 = codes(QB) / 2, NRAW = NR0 > 8 ? 8 : NR0;
+  static constexpr int SN = E4M3 ? 2 * NR : NR;      // columns of S
   static constexpr int CW = NR < 32 ? NR : 32;                 // rows a softmax warp holds
   static constexpr int SW = 4 * (NR / CW);                      // softmax warps
-  static constexpr int THREADS = 32 * (SW + 3 + 4 * VG);
-  static constexpr int COLS0 = (2 + 2 * H) * NR;                // two S, two O
+  static constexpr int CV = !E4M3 ? 0 : NR > 32 ? 4 : 8;        // converting warps
+  static constexpr int THREADS = 32 * (SW + 3 + CV);
+  static constexpr int COLS0 = 2 * SN + 2 * H * NR;             // two S, two O
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
   // What a unit costs beside its tiles, in tiles.  64 requests of 3 to 8192 tokens with 128 columns (64 KB
   // of keys and values a tile): 1, 2, 3 and 4 give 50.1, 44.9, 46.4 and 48.9 us; 48 with 64 columns (32 KB)
   // and a window of 1000: 33.5, 27.8, 25.9 and 26.8 us.
-  static constexpr int V = SLOT * H * 2 / (E4M3 ? 2 : 1) >= 65536 ? 2 : 3;
-  static_assert(COLS0 <= 512 && NS >= 3 && (!E4M3 || NRAW >= 3), "resources of an SM");
-  // A wait on a barrier's parity tells its phase only while the phase before it is known to be over.
-  // Of two converting groups, the one at place x has seen place x - 2 - NS consumed.
-  static_assert(VG < 2 || NRAW >= NS + 2, "place x - NRAW is converted before a group waits for place x");
+  static constexpr int V = !E4M3 && SLOT * H * 2 >= 65536 ? 2 : 3;
+  static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
 };
 
 // ------------------------------------------------------------------ schedule
@@ -212,6 +221,7 @@ __device__ __forceinline__ int find_place(const Args& a, const Req& r, const Loa
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 // 128-byte swizzle: row r of 128 bytes, 16-byte piece c
+__device__ __forceinline__ uint32_t sw64(int r, int c) { return uint32_t(r * 64 + ((c ^ (r >> 1 & 3)) << 4)); }  // rows of 64 bytes
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return uint32_t(r * 128 + ((c ^ (r & 7)) << 4)); }
 __device__ __forceinline__ void bar_init(uint64_t* b, int n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n));
@@ -285,6 +295,20 @@ __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(A), "n"(B), "n"(2 * A), "n"(2 * B), "n"(3 * A), "n"(3 * B)
       : "memory");
 }
+// Steps of 32 E4M3 codes along the contracted dimension, both operands K-major.
+template <int STEPS>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int k = 0; k < STEPS; k += 2)
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 a1, b1;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n\t}" ::"r"(d),
+        "l"(a + 2 * k), "l"(b + 2 * k), "r"(idesc), "r"(k > 0 ? 1u : acc)
+        : "memory");
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -319,11 +343,11 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 // Pairs in one instruction: a = a * f - m, and a += x.
-__device__ __forceinline__ void scale_sub2(float& a0, float& a1, float f, float m0, float m1) {
-  asm("{\n\t.reg .b64 a, f, m;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 m, {%3, %4};\n\t"
+__device__ __forceinline__ void scale_sub2(float& a0, float& a1, float f0, float f1, float m0, float m1) {
+  asm("{\n\t.reg .b64 a, f, m;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\t"
       "fma.rn.f32x2 a, a, f, m;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "+f"(a0), "+f"(a1)
-      : "f"(f), "f"(-m0), "f"(-m1));
+      : "f"(f0), "f"(f1), "f"(-m0), "f"(-m1));
 }
 __device__ __forceinline__ void add2(float& a0, float& a1, float x0, float x1) {
   asm("{\n\t.reg .b64 a, x;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\t"
@@ -349,6 +373,12 @@ __device__ __forceinline__ void softmax_sync() {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two values -> two E4M3 codes (low byte first), to nearest even.
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 // Four E4M3 codes (low byte first) -> bf16, exact.
 __device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t four, uint32_t* out) {
@@ -452,14 +482,15 @@ __device__ __forceinline__ int4 join_record(const Args& a, const Plan& p, const 
 
 template <int NR>
 struct Misc {
-  uint64_t full[16], empty[16], rfull[16], rempty[16], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
+  uint64_t full[16], empty[16], kfull[8], kempty[8], rfull[8], rempty[8], factors[2], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
   PlanShared plan;
   alignas(16) float m[NR];   // of the rows, log2 units
   alignas(16) float alpha[NR];
+  alignas(16) float qf[4][NR];  // E4M3: factors of four pieces' rows (queries run three pieces ahead at most)
   float inv[NR];             // 1 / sum of a finished piece's rows
-  float red[4][NR];
+  float red[4][NR], sum[4][NR];
   int page[2][kKeys];        // pages of a tile's boxes, for keys and for values
   int nbad;
   uint8_t bad[kKeys];  // keys of a tile with values that are not finite
@@ -526,13 +557,14 @@ template <int D, int NR, bool E4M3>
 __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::OCC) k_attn(const __grid_constant__ Args a) {
   using C = Cfg<D, NR, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem;
-  uint8_t* sq = ring + C::NS * C::SLOT;
+  uint8_t* ring = smem;                         // keys and values, or values alone
+  uint8_t* kring = ring + C::NS * C::SLOT;      // E4M3: keys
+  uint8_t* raw = kring + C::NK * C::RAW;        // E4M3: values as they come
+  uint8_t* sq = raw + C::NRAW * C::RAW;
   uint8_t* sp = sq + C::QB * C::QBYTES;
-  uint8_t* raw = sp + 2 * C::PBYTES;
   using Ms = Misc<NR>;
   static_assert(sizeof(Ms) <= misc_bytes(NR), "misc");
-  Ms& ms = *reinterpret_cast<Ms*>(raw + C::NRAW * C::RAW);
+  Ms& ms = *reinterpret_cast<Ms*>(sp + 2 * C::PBYTES);
   volatile int* fail = &ms.fail;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr int kMmaWarp = C::SW, kLoadWarp = C::SW + 1, kSoft = 32 * C::SW;  // loads: keys, then values
@@ -544,16 +576,21 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   } else if (tid == 32 * kLoadWarp) {
     for (int i = 0; i < C::NS; ++i) {
-      bar_init(&ms.full[i], E4M3 ? 4 : 1);
+      bar_init(&ms.full[i], E4M3 ? C::CV : 1);
       bar_init(&ms.empty[i], 1);
+    }
+    for (int i = 0; i < C::NK; ++i) {
+      bar_init(&ms.kfull[i], 1);
+      bar_init(&ms.kempty[i], 1);
     }
     for (int i = 0; i < C::NRAW; ++i) {
       bar_init(&ms.rfull[i], 1);
-      bar_init(&ms.rempty[i], 4);
+      bar_init(&ms.rempty[i], C::CV);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&ms.qfull[i], 1);
+      bar_init(&ms.qfull[i], E4M3 ? C::CV : 1);
       bar_init(&ms.qfree[i], 1);
+      bar_init(&ms.factors[i], 1);
       bar_init(&ms.sfull[i], 1);
       bar_init(&ms.pfull[i], C::SW);
       bar_init(&ms.pvdone[i], 1);
@@ -583,6 +620,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
       // D f32, A and B bf16, N = NR, M = 128; the second product's operands are both MN-major
       constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(NR >> 3) << 17) | (8u << 24);
       constexpr uint32_t kIdescS = kBase, kIdescO = kBase | (1u << 15) | (1u << 16);
+      constexpr uint32_t kIdescQ = (1u << 4) | (uint32_t(C::SN >> 3) << 17) | (8u << 24);  // E4M3 both, N = 2 NR
+      Ring<E4M3 ? C::NK : 1> kr(0);
       Ring<C::NS> rg(0);
       int qn = -1;             // pieces begun, less one
       int pieces = -1;         // pieces whose O has been begun, less one
@@ -595,11 +634,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           if (first) {
             ++qn;
             wait(&ms.qfull[qn % C::QB], (qn / C::QB) & 1, fail);
+            if (E4M3 && lane == 0) arrive(&ms.factors[qn & 1]);
+            __syncwarp();
           }
-          const uint32_t d = taddr + uint32_t(n & 1) * NR;
-          const uint64_t qd = desc(su32(sq + (qn % C::QB) * C::QBYTES), 16, 1024, 2);
+          const uint32_t d = taddr + uint32_t(n & 1) * C::SN;
+          // rows of 128 bytes, swizzled so; 64 codes make 64
+          constexpr bool k64 = E4M3 && C::DS == 64;
+          const uint64_t qd = desc(su32(sq + (qn % C::QB) * C::QBYTES), 16, k64 ? 512 : 1024, k64 ? 4 : 2);
 #pragma unroll
           for (int hh = 0; hh < C::H; ++hh) {
+            if constexpr (E4M3) {
+              wait(&ms.kfull[kr.slot], kr.phase, fail);
+              tc_after();
+              mma_e4m3<C::DS / 32>(d, desc(su32(kring + kr.slot * C::RAW), 16, k64 ? 512 : 1024, k64 ? 4 : 2),
+                                   qd + hh * (C::SN * C::DS >> 4), kIdescQ, hh > 0);
+              commit_to(&ms.kempty[kr.slot]);
+              kr.next();
+              continue;
+            }
             wait(&ms.full[rg.slot], rg.phase, fail);
             tc_after();
             const uint64_t kd = desc(su32(ring + rg.slot * C::SLOT), 16, 1024, 2);
@@ -621,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
             ++pieces;
             if (pieces >= 2) wait(&ms.ofree[pieces & 1], ((pieces >> 1) - 1) & 1, fail);
           }
-          const uint32_t od = taddr + uint32_t(2 + (pieces & 1) * C::H) * NR;
+          const uint32_t od = taddr + uint32_t(2 * C::SN + (pieces & 1) * C::H * NR);
           const uint64_t pd = desc(su32(sp + p * C::PBYTES), 128, 2048, 0);
 #pragma unroll
           for (int hh = 0; hh < C::H; ++hh) {
@@ -667,7 +719,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           if (x < boxes && key < w.s.hi && key + (1 << box_shift) > w.s.lo) id[i] = row[key >> kv.page_shift];
         }
       };
-      Ring<E4M3 ? C::NRAW : C::NS> rg(1);  // a fresh slot is empty
+      Ring<C::NS> rg(1);  // a fresh slot is empty
+      Ring<E4M3 ? C::NK : 1> kr(1);
+      Ring<E4M3 ? C::NRAW : 1> rr(1);
       auto skip = [&]() {
 #pragma unroll
         for (int hh = 0; hh < C::H; ++hh) rg.next();
@@ -680,7 +734,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
       }
 #pragma unroll 1
       for (int n = 0; n < count; ++n) {
-        if (keys && w.j == w.jbeg) {
+        if (!E4M3 && keys && w.j == w.jbeg) {
           ++qn;
           if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
           if (lane == 0 && !*fail) {
@@ -707,8 +761,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
         }
 #pragma unroll 1
         for (int hh = 0; hh < C::H; ++hh) {
-          uint64_t* full = E4M3 ? &ms.rfull[rg.slot] : &ms.full[rg.slot];
-          wait(E4M3 ? &ms.rempty[rg.slot] : &ms.empty[rg.slot], rg.phase, fail);
+          // E4M3: keys and values have rings of their own
+          const int slot = !E4M3 ? rg.slot : keys ? kr.slot : rr.slot;
+          uint64_t* full = (!E4M3 ? ms.full : keys ? ms.kfull : ms.rfull) + slot;
+          wait((!E4M3 ? ms.empty : keys ? ms.kempty : ms.rempty) + slot, !E4M3 ? rg.phase : keys ? kr.phase : rr.phase, fail);
           if (*fail) break;
           if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
           __syncwarp();
@@ -716,52 +772,108 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
 #pragma unroll 1
           for (int x = lane; x < boxes * CHUNKS; x += 32) {
             const int p = x & (boxes - 1), c = x >> (7 - box_shift);
-            uint8_t* dst = E4M3 ? raw + rg.slot * C::RAW + (p << box_shift) * C::DS
-                                : ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
+            uint8_t* dst = E4M3 ? (keys ? kring : raw) + slot * C::RAW + (p << box_shift) * C::DS
+                                : ring + slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
             load_box(dst, tm, hh * C::DS + c * 64, tok, h, page[p], full);
           }
           __syncwarp();
-          rg.next();
+          if (!E4M3) rg.next();
+          else if (keys) kr.next();
+          else rr.next();
         }
-        if (keys ? n > 0 : n + 2 != count) skip();
+        if (!E4M3 && (keys ? n > 0 : n + 2 != count)) skip();
       }
     } else if (warp > kLoadWarp + 1) {
       // -------------------------------------------------------- E4M3 codes -> bf16
       if constexpr (E4M3) {
-        const int group = (warp - kLoadWarp - 2) >> 2, vt = tid & 127;
-        static_assert((C::SW + 3) % 4 == 3, "the groups' threads");
-        constexpr int CH = C::DS / 8, STEP = 128 / CH;  // 8 codes a thread make one 16-byte piece
+        const int vw = warp - kLoadWarp - 2, vt = vw * 32 + lane;
+        constexpr int CH = C::DS / 8, STEP = 32 * C::CV / CH;  // 8 codes a thread make one 16-byte piece
         const int r0 = vt / CH, c = vt % CH;
         Ring<C::NRAW> in(0);
         Ring<C::NS> out(1);
-        if (group) {
-          in.next();
-          out.next();
-        }
+        int qn = -1;
+        // The rows of a piece as two terms, a warp a row, and the factors of their scores.
+        auto queries = [&](const Walk<V>& k) {
+          ++qn;
+          if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
+          // eight columns a thread: L threads a row, `AT` rows at a time
+          constexpr int L = D / 8, AT = 32 * C::CV / L, STEPS = (NR + AT - 1) / AT, AHEAD = STEPS < 4 ? STEPS : 4;
+          const int rows = (k.s.i1 - k.s.i0 + 1) * a.G, at = vt % L * 8;
+          const float base = a.scale * 1.4426950408889634f * (a.kv.k_scale ? a.kv.k_scale[k.h] : 1.f);
+          const uint16_t* src = a.q + (long long)(k.r.s0 + k.s.i0) * a.qs + (long long)k.h * a.G * D + at;
+          uint8_t* dst = sq + (qn % C::QB) * C::QBYTES + at / C::DS * (C::SN * C::DS) + at % 16;
+          auto load = [&](int r) {
+            const int i = r / a.G;
+            return r < rows ? *reinterpret_cast<const uint4*>(src + i * a.qs + (r - i * a.G) * D) : make_uint4(0, 0, 0, 0);
+          };
+          int r = vt / L;
+          uint4 u[AHEAD];
+#pragma unroll
+          for (int y = 0; y < AHEAD; ++y) u[y] = load(r + y * AT);
 #pragma unroll 1
-        for (int x = group; x < 2 * C::H * count; x += C::VG) {  // the groups take turns
-          wait(&ms.rfull[in.slot], in.phase, fail);
-          wait(&ms.empty[out.slot], out.phase, fail);
-          const uint8_t* src = raw + in.slot * C::RAW + c * 8;
-          uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
-          uint2 v[kKeys / STEP];
+          for (; r < NR; r += AT) {
+            const uint32_t w4[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-          for (int i = 0; i < kKeys / STEP; ++i) v[i] = *reinterpret_cast<const uint2*>(src + (r0 + i * STEP) * C::DS);
+            for (int y = 0; y + 1 < AHEAD; ++y) u[y] = u[y + 1];
+            if constexpr (STEPS > AHEAD) u[AHEAD - 1] = load(r + AHEAD * AT);
+            float f[8], most = 0.f;
 #pragma unroll
-          for (int i = 0; i < kKeys / STEP; ++i) {
-            uint32_t o[4];
-            e4m3x4_to_bf16x4(v[i].x, o);
-            e4m3x4_to_bf16x4(v[i].y, o + 2);
-            *reinterpret_cast<uint4*>(dst + sw128(r0 + i * STEP, c % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int x = 0; x < 8; ++x) {
+              f[x] = __uint_as_float(x & 1 ? w4[x / 2] & 0xffff0000u : w4[x / 2] << 16);
+              most = fmaxf(most, fabsf(f[x]));
+            }
+#pragma unroll
+            for (int x = 1; x < L; x <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+            const uint32_t e = __float_as_uint(most) >> 23;
+            const float up = __uint_as_float(min(261u - e, 237u) << 23);  // the largest in [2^7, 2^8)
+            if (at == 0) ms.qf[qn & 3][r] = base / up;
+            uint32_t t[2][4];
+#pragma unroll
+            for (int x = 0; x < 8; x += 2) {
+              // an infinity becomes NaN, as its scores' softmax would be
+              const float v0 = fabsf(f[x]) < INFINITY ? f[x] * up : NAN, v1 = fabsf(f[x + 1]) < INFINITY ? f[x + 1] * up : NAN;
+              t[0][x / 2] = e4m3x2(v0, v1);
+              const float2 b = f16x2_to_f32x2(e4m3x2_to_f16x2(uint16_t(t[0][x / 2])));
+              t[1][x / 2] = e4m3x2((v0 - b.x) * 32.f, (v1 - b.y) * 32.f);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int row = z * NR + r;
+              *reinterpret_cast<uint2*>(dst + (C::DS == 64 ? sw64(row, at % C::DS / 16) : sw128(row, at % C::DS / 16))) =
+                  make_uint2(t[z][0] | t[z][1] << 16, t[z][2] | t[z][3] << 16);
+            }
           }
           proxy_fence();
           __syncwarp();
-          if (lane == 0) {
-            arrive(&ms.full[out.slot]);
-            arrive(&ms.rempty[in.slot]);
+          if (lane == 0) arrive(&ms.qfull[qn % C::QB]);
+        };
+        queries(w);
+#pragma unroll 1
+        for (int n = 0; n < count; ++n) {
+          if (n + 1 < count) {
+            w.next(a, cap);
+            if (w.j == w.jbeg) queries(w);  // before this tile's values: S of the next tile comes first
           }
-#pragma unroll
-          for (int g = 0; g < C::VG; ++g) {
+#pragma unroll 1
+          for (int hh = 0; hh < C::H; ++hh) {
+            wait(&ms.rfull[in.slot], in.phase, fail);
+            wait(&ms.empty[out.slot], out.phase, fail);
+            const uint8_t* src = raw + in.slot * C::RAW + c * 8;
+            uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
+#pragma unroll 4
+            for (int i = 0; i < kKeys / STEP; ++i) {
+              const uint2 v = *reinterpret_cast<const uint2*>(src + (r0 + i * STEP) * C::DS);
+              uint32_t o[4];
+              e4m3x4_to_bf16x4(v.x, o);
+              e4m3x4_to_bf16x4(v.y, o + 2);
+              *reinterpret_cast<uint4*>(dst + sw128(r0 + i * STEP, c % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) {
+              arrive(&ms.full[out.slot]);
+              arrive(&ms.rempty[in.slot]);
+            }
             in.next();
             out.next();
           }
@@ -774,14 +886,93 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
       const int krow = quad * 32 + lane;  // this thread's key in a tile, and its column of v
       const uint32_t tl = taddr + (uint32_t(quad * 32) << 16);
       float l[CW];
-      float factor = 0.f;  // of the scores, in log2 units
+      float factor = 0.f, v_factor = 1.f;  // of the scores, in log2 units, and of the values
       // a finished piece whose O is still to be written
       int piece = -1, d_token = 0, d_head = 0, d_rows = 0, d_part = -1;
       bool pending = false;
       int newest = 0, oldest = 0, whole0 = 0, whole1 = 0;
       if (tid == 0) a.join[run] = join_record<V>(a, plan, w);
+      // Rows x0 .. x0 + CK - 1 of tile n (p = n & 1): scores in log2 units, less m where asked.
+      auto scores = [&](int p, int x0, float* s, bool less_m) {
+#pragma unroll
+        for (int i = 0; i < CK; i += 16) ld16(tl + p * C::SN + c0 + x0 + i, s + i);
+        float second[E4M3 ? CK : 1];
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int i = 0; i < CK; i += 16) ld16(tl + p * C::SN + NR + c0 + x0 + i, second + i);
+        }
+        ld_wait();
+#pragma unroll
+        for (int x = 0; x < CK; x += 4) {
+          float4 m = make_float4(0.f, 0.f, 0.f, 0.f), f = make_float4(factor, factor, factor, factor);
+          if (less_m) m = *reinterpret_cast<const float4*>(&ms.m[c0 + x0 + x]);
+          if constexpr (E4M3) {
+            f = *reinterpret_cast<const float4*>(&ms.qf[piece & 3][c0 + x0 + x]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[x + y] = fmaf(second[x + y], 0x1p-5f, s[x + y]);
+          }
+          scale_sub2(s[x], s[x + 1], f.x, f.y, m.x, m.y);
+          scale_sub2(s[x + 2], s[x + 3], f.z, f.w, m.z, m.w);
+        }
+      };
+      // Weights of the tile, in bf16 for the product and into the sums; true when a score passes m by
+      // kGrow.  hide: sets hidden scores to -inf.  sums: 0 where m was given up as too small, 1 everywhere.
+      auto weights = [&](int p, auto hide, bool sums) {
+        uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
+        __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+        for (int x0 = 0; x0 < CW; x0 += CK) {
+          float s[CK];
+          scores(p, x0, s, true);
+          hide(x0, s);
+#pragma unroll
+          for (int x = 0; x < CK; x += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int y = 0; y < 8; y += 2) {
+              const float e0 = ex2(s[x + y]), e1 = ex2(s[x + y + 1]);
+              if (sums) {
+                add2(l[x0 + x + y], l[x0 + x + y + 1], e0, e1);
+              } else {
+                if (ms.alpha[c0 + x0 + x + y] <= kLost) l[x0 + x + y] += e0;
+                if (ms.alpha[c0 + x0 + x + y + 1] <= kLost) l[x0 + x + y + 1] += e1;
+              }
+              u[y / 2] = pack2(e0, e1);
+              most = __hmax2(most, *reinterpret_cast<const __nv_bfloat162*>(&u[y / 2]));
+            }
+            *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+        return fmaxf(__low2float(most), __high2float(most)) > kMost;
+      };
+      // S of tile n is there and P(n - 2) has been read.
+      auto ready = [&](int n) {
+        wait(&ms.sfull[n & 1], (n >> 1) & 1, fail);
+        tc_after();
+        if (n >= 2) wait(&ms.pvdone[n & 1], ((n - 2) >> 1) & 1, fail);
+      };
 #pragma unroll 1
       for (int n = 0; n <= count; ++n) {
+        bool over = false;
+        if (n < count && !pending && w.j > w.jbeg) {
+          // Tiles inside a piece of which every row sees every key, with the m there is; it holds for all
+          // but a few.  A loop of its own: the code of all that a tile may need beside this is far apart,
+          // and fetching past it cost 600 clocks a tile.
+          const int to = min(w.jend - 1, whole1);
+          if (w.j >= whole0) {
+#pragma unroll 1
+            for (; w.j < to; ++w.j, ++n) {
+              ready(n);
+              const bool high = weights(n & 1, [](int, float*) {}, true);
+              proxy_fence();
+              over = vote_any<kSoft>(high);
+              if (over) break;
+              tc_before();
+              __syncwarp();
+              if (lane == 0) arrive(&ms.pfull[n & 1]);
+            }
+          }
+        }
         const int p = n & 1;
         const uint32_t ph = (n >> 1) & 1;
         if (n < count) {
@@ -790,117 +981,77 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
             ++piece;
 #pragma unroll
             for (int i = 0; i < CW; ++i) l[i] = 0.f;
-            factor = a.scale * 1.4426950408889634f * (E4M3 && a.kv.k_scale ? a.kv.k_scale[w.h] : 1.f);
+            factor = a.scale * 1.4426950408889634f;
+            if (E4M3 && a.kv.v_scale) v_factor = a.kv.v_scale[w.h];
+            if (E4M3) wait(&ms.factors[piece & 1], (piece >> 1) & 1, fail);
             // the row tile's tokens; the tiles of which every row sees every key
             newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
             whole1 = max(min(oldest + 1, cap), 0) / kKeys - w.s.tile0;
             whole0 = a.window > 0 ? max(newest - a.window + kKeys, 0) / kKeys - w.s.tile0 : 0;
           }
-          const uint32_t to = tl + uint32_t(2 + (piece & 1) * C::H) * NR;  // O of this piece
+          const uint32_t to = tl + uint32_t(2 * C::SN + (piece & 1) * C::H * NR);  // O of this piece
           const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
           const bool whole = w.j >= whole0 && w.j < whole1;
-          // rows x0 .. x0 + CK - 1: scores in log2 units, less m where asked; hidden ones -inf
-          auto scores = [&](int x0, float* s, bool less_m) {
+          auto hide = [&](int x0, float* s) {
+            if (whole) return;
+            // rows are in the order of their tokens: rows from .. to - 1 see this key
+            const int i_from = max(key - oldest, 0), i_to = a.window > 0 ? key - oldest + a.window : a.tokens;
+            const int from = key >= cap || i_from > a.tokens ? INT_MAX : i_from * a.G;
+            const int to_row = i_to >= a.tokens ? INT_MAX : i_to * a.G;
 #pragma unroll
-            for (int i = 0; i < CK; i += 16) ld16(tl + p * NR + c0 + x0 + i, s + i);
-            ld_wait();
-#pragma unroll
-            for (int x = 0; x < CK; x += 4) {
-              float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (less_m) m = *reinterpret_cast<const float4*>(&ms.m[c0 + x0 + x]);
-              scale_sub2(s[x], s[x + 1], factor, m.x, m.y);
-              scale_sub2(s[x + 2], s[x + 3], factor, m.z, m.w);
-            }
-            if (!whole) {
-              // rows are in the order of their tokens: rows from .. to - 1 see this key
-              const int i_from = max(key - oldest, 0), i_to = a.window > 0 ? key - oldest + a.window : a.tokens;
-              const int from = key >= cap || i_from > a.tokens ? INT_MAX : i_from * a.G;
-              const int to_row = i_to >= a.tokens ? INT_MAX : i_to * a.G;
-#pragma unroll
-              for (int x = 0; x < CK; ++x)
-                if (c0 + x0 + x < from || c0 + x0 + x >= to_row) s[x] = -INFINITY;
-            }
+            for (int x = 0; x < CK; ++x)
+              if (c0 + x0 + x < from || c0 + x0 + x >= to_row) s[x] = -INFINITY;
           };
-          uint8_t* dst = sp + p * C::PBYTES + (krow >> 3) * 128 + (krow & 7) * 16;
-          // Weights of the tile, in bf16 for the product and into the sums; true when a score passes
-          // m by kGrow.
-          // sums: 0 where m was given up as too small, 1 everywhere.
-          auto weights = [&](bool sums) {
-            __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-            for (int x0 = 0; x0 < CW; x0 += CK) {
-              float s[CK];
-              scores(x0, s, true);
-#pragma unroll
-              for (int x = 0; x < CK; x += 8) {
-                uint32_t u[4];
-#pragma unroll
-                for (int y = 0; y < 8; y += 2) {
-                  const float e0 = ex2(s[x + y]), e1 = ex2(s[x + y + 1]);
-                  if (sums) {
-                    add2(l[x0 + x + y], l[x0 + x + y + 1], e0, e1);
-                  } else {
-                    if (ms.alpha[c0 + x0 + x + y] <= kLost) l[x0 + x + y] += e0;
-                    if (ms.alpha[c0 + x0 + x + y + 1] <= kLost) l[x0 + x + y + 1] += e1;
-                  }
-                  u[y / 2] = pack2(e0, e1);
-                  most = __hmax2(most, *reinterpret_cast<const __nv_bfloat162*>(&u[y / 2]));
-                }
-                *reinterpret_cast<uint4*>(dst + ((c0 + x0 + x) >> 3) * 2048) = make_uint4(u[0], u[1], u[2], u[3]);
-              }
-            }
-            return fmaxf(__low2float(most), __high2float(most)) > kMost;
-          };
-          wait(&ms.sfull[p], ph, fail);
-          tc_after();
-          if (n >= 2) wait(&ms.pvdone[p], ((n - 2) >> 1) & 1, fail);  // P(n - 2) has been read
-          bool set = first;
-          if (!first) {
-            // with the m there is; it holds for all but a few tiles
-            const bool over = weights(true);
-            if (whole) proxy_fence();
-            set = vote_any<kSoft>(over);
-          }
-          if (set) {
-            // set m: the rows' maxima over the 128 keys
-#pragma unroll
-            for (int x0 = 0; x0 < CW; x0 += CK) {
-              float s[CK];
-              scores(x0, s, false);
-#pragma unroll
-              for (int x = 0; x < CK; ++x) {
-                const float v = warp_max(s[x]);
-                if (lane == x) ms.red[quad][c0 + x0 + x] = v;
-              }
-            }
-            softmax_sync<kSoft>();
-            if (tid < NR) {
-              const float old = first ? kUnset : ms.m[tid];
-              const float v = fmaxf(fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid])), old);
-              ms.m[tid] = v;
-              ms.alpha[tid] = ex2(old - v);
-            }
-            softmax_sync<kSoft>();
-            if (!first) {
-              // The sums hold this tile's weights against the old m already.  Where m grew by so much
-              // that those may have overflowed, what was there before them is nothing against them.
-#pragma unroll
-              for (int x = 0; x < CW; ++x) l[x] = ms.alpha[c0 + x] > kLost ? l[x] * ms.alpha[c0 + x] : 0.f;
-              wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
-              tc_after();
+          ready(n);
+          bool set = first || over;
 #pragma unroll 1
-              for (int x = 0; x < C::H * CW; x += 16) {
-                const int hh = x / CW, y0 = x % CW;
-                float o[16];
-                ld16(to + hh * NR + c0 + y0, o);
-                ld_wait();
+          for (bool again = set;; again = true) {
+            if (again) {
+              // set m: the rows' maxima over the 128 keys
 #pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] *= ms.alpha[c0 + y0 + y];
-                st16(to + hh * NR + c0 + y0, o);
+              for (int x0 = 0; x0 < CW; x0 += CK) {
+                float s[CK];
+                scores(p, x0, s, false);
+                hide(x0, s);
+#pragma unroll
+                for (int x = 0; x < CK; ++x) {
+                  const float v = warp_max(s[x]);
+                  if (lane == x) ms.red[quad][c0 + x0 + x] = v;
+                }
               }
-              st_wait();
+              softmax_sync<kSoft>();
+              if (tid < NR) {
+                const float old = first ? kUnset : ms.m[tid];
+                const float v = fmaxf(fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid])), old);
+                ms.m[tid] = v;
+                ms.alpha[tid] = ex2(old - v);
+              }
+              softmax_sync<kSoft>();
+              if (!first) {
+                // The sums hold this tile's weights against the old m already.  Where m grew by so much
+                // that those may have overflowed, what was there before them is nothing against them.
+#pragma unroll
+                for (int x = 0; x < CW; ++x) l[x] = ms.alpha[c0 + x] > kLost ? l[x] * ms.alpha[c0 + x] : 0.f;
+                wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
+                tc_after();
+#pragma unroll 1
+                for (int x = 0; x < C::H * CW; x += 16) {
+                  const int hh = x / CW, y0 = x % CW;
+                  float o[16];
+                  ld16(to + hh * NR + c0 + y0, o);
+                  ld_wait();
+#pragma unroll
+                  for (int y = 0; y < 16; ++y) o[y] *= ms.alpha[c0 + y0 + y];
+                  st16(to + hh * NR + c0 + y0, o);
+                }
+                st_wait();
+              }
             }
-            weights(first);
+            const bool high = weights(p, hide, first || !again);
+            if (again) break;
+            if (whole) proxy_fence();
+            set = vote_any<kSoft>(high);
+            if (!set) break;
           }
           // Values at hidden keys may hold anything, and 0 times what is not finite is NaN.  Those that
           // no row sees become zeros; where some rows see a key and some do not, values that are not
@@ -909,14 +1060,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           if (!whole) {
             const bool gone = key < w.s.lo || key >= w.s.hi, mixed = w.s.i1 > w.s.i0;
             const bool some = !gone && mixed && (key > oldest || (a.window > 0 && key <= newest - a.window));
-            const int at = (n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
+            const int at = (E4M3 ? n : n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
             bool bad = false;
-            if constexpr (C::NS < 3 * C::H) {
-              // V(n)'s slots may still be held by V(n - 1) or K(n + 1): see those filled first, so that
-              // the slots' phases tell V(n)'s.  With more slots it was K(n) at the latest.
-              if (n >= 1) wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
-              if (n + 1 < count) wait(&ms.sfull[p ^ 1], ((n + 1) >> 1) & 1, fail);
-            }
+            // V(n)'s slots may still be held by V(n - 1), or in a ring for both by K(n + 1): see those filled
+            // first, so that the slots' phases tell V(n)'s.  With more slots it was an older tile.
+            if (C::NS < (E4M3 ? 2 : 3) * C::H && n >= 1) wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
+            if (!E4M3 && C::NS < 3 * C::H && n + 1 < count) wait(&ms.sfull[p ^ 1], ((n + 1) >> 1) & 1, fail);
 #pragma unroll 1
             for (int hh = 0; hh < C::H; ++hh) {
               const int slot = (at + hh) % C::NS;
@@ -981,7 +1130,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           wait(&ms.pvdone[p ^ 1], ((n - 1) >> 1) & 1, fail);
           tc_after();
           const int d_piece = n < count ? piece - 1 : piece;
-          const uint32_t from = tl + uint32_t(2 + (d_piece & 1) * C::H) * NR;
+          const uint32_t from = tl + uint32_t(2 * C::SN + (d_piece & 1) * C::H * NR);
 #pragma unroll 1
           for (int x = 0; x < C::H * CW; x += 16) {
             const int hh = x / CW, row0 = c0 + x % CW, col = hh * 128 + krow;
@@ -1025,7 +1174,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
               for (int y = 0; y < 16; ++y) v[y] = l[x + y];
               float t = transpose_sum<16>(v, lane);
               t += __shfl_xor_sync(0xffffffffu, t, 16);
-              if (lane < 16) ms.red[quad][c0 + x + lane] = t;
+              if (lane < 16) ms.sum[quad][c0 + x + lane] = t;
             }
             softmax_sync<kSoft>();
             const bool head = w.jbeg > 0, split = head || w.jend < w.s.nt;
@@ -1035,13 +1184,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
             d_part = split ? 2 * run + (head ? 0 : 1) : -1;
             pending = true;
             if (tid < NR) {
-              const float t = ms.red[0][tid] + ms.red[1][tid] + ms.red[2][tid] + ms.red[3][tid];
-              const float vs = E4M3 && a.kv.v_scale ? a.kv.v_scale[w.h] : 1.f;
+              const float t = ms.sum[0][tid] + ms.sum[1][tid] + ms.sum[2][tid] + ms.sum[3][tid];
               if (split && tid < d_rows)
                 reinterpret_cast<float2*>(a.ml)[(long long)d_part * NR + tid] = make_float2(ms.m[tid], t);
-              ms.inv[tid] = t == 0.f ? 0.f : vs / t;
+              ms.inv[tid] = t == 0.f ? 0.f : v_factor / t;
             }
-            softmax_sync<kSoft>();
+            // read after the two waits of the next piece's first tile
+            if (n + 1 == count) softmax_sync<kSoft>();
           }
           if (n + 1 < count) w.next(a, cap);
         }

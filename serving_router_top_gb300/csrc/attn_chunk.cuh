@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
             uint32_t u[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              scale_sub2(s[c + i], s[c + i + 1], f, m, m);
+              scale_sub2(s[c + i], s[c + i + 1], f, f, m, m);
               const float e0 = ex2(s[c + i]), e1 = ex2(s[c + i + 1]);
               add2(sum0, sum1, e0, e1);
               u[i / 2] = pack2(e0, e1);

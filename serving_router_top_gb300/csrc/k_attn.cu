@@ -35,12 +35,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // Tiles of a pool or of the query rows; what lies outside reads as zeros.
 bool encode(CUtensorMap* m, void* base, int e4m3, int rank, const cuuint64_t* dims, const cuuint64_t* pitches,
-            const cuuint32_t* box) {
+            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   return fn && fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base, dims, pitches,
                   box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace attn
@@ -125,6 +125,8 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   const int nr = attn::row_tile(kv->D, kv->e4m3, Hq / kv->Hkv, b->max_n > 1 ? b->max_n : 1);
   a.o = o;
   a.os = T > 1 ? o_stride : width;
+  a.q = q;
+  a.qs = T > 1 ? q_stride : width;
   a.G = Hq / kv->Hkv;
   a.window = window < attn::cap_of(a.kv) ? window : 0;  // one that holds every key is none
   const int tile = nr == attn::kChunkRows ? nr / 2 / a.G : nr / a.G;  // tokens of a row tile
@@ -141,9 +143,12 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   const cuuint64_t qdims[3] = {cuuint64_t(kv->D), cuuint64_t(Hq), cuuint64_t(T)};
   const cuuint64_t qpitches[2] = {cuuint64_t(kv->D) * 2, cuuint64_t(T > 1 ? q_stride : width) * 2};
   const cuuint32_t qbox[3] = {64, cuuint32_t(a.G), cuuint32_t(tile)};
-  if (!attn::encode(&a.mk, kv->k, kv->e4m3, 4, dims, pitches, boxes) ||
-      !attn::encode(&a.mv, kv->v, kv->e4m3, 4, dims, pitches, boxes) ||
-      !attn::encode(&a.mq, const_cast<uint16_t*>(q), 0, 3, qdims, qpitches, qbox))
+  // operands of the tensor core are swizzled by their rows; E4M3 values become one later
+  const CUtensorMapSwizzle k_swizzle = kv->e4m3 && kv->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle v_swizzle = kv->e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!attn::encode(&a.mk, kv->k, kv->e4m3, 4, dims, pitches, boxes, k_swizzle) ||
+      !attn::encode(&a.mv, kv->v, kv->e4m3, 4, dims, pitches, boxes, v_swizzle) ||
+      !attn::encode(&a.mq, const_cast<uint16_t*>(q), 0, 3, qdims, qpitches, qbox, CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_EINVAL;
   a.scale = scale;
   a.err = ws->error;
