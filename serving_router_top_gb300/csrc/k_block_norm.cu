@@ -16,19 +16,26 @@ struct Args {
   uint16_t* xn;
   const uint16_t *y, *w_post, *gate, *w_pre;
   long long xs, xos, xns, ys, gs;
-  int H, post, sig;
+  int T, H, post, sig;
   float scale, eps;
 };
 
-template <int N>
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Over a row's threads: a warp, or the CTA.
+template <bool WARP, int N>
+__device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (WARP) return v;
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float tot = 0.f;
+  if (N <= 256) {
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w) tot += red[w];
+    for (int w = 0; w < N / 32; ++w) tot += w < int(blockDim.x / 32) ? red[w] : 0.f;
+  } else {
+#pragma unroll 8
+    for (int w = 0; w < int(blockDim.x / 32); ++w) tot += red[w];
+  }
   return tot;
 }
 
@@ -44,18 +51,22 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float f[V]) {
   }
 }
 
-// One CTA of N threads per row; a thread holds P pieces of V columns.
-template <int N, int P, int V>
+// A row has a warp (a CTA's warps take a row each) or a CTA of at most N threads; a thread holds P
+// pieces of V columns.
+constexpr int kWarpRows = 4;
+template <bool WARP, int N, int P, int V>
 __global__ void __launch_bounds__(N) k_block_norm(const __grid_constant__ Args a) {
   pdl_trigger();
   pdl_wait();
   __shared__ float red[2][N / 32];
-  const long long t = blockIdx.x;
+  const int across = WARP ? 32 : blockDim.x;  // threads of a row
+  const long long t = WARP ? (long long)blockIdx.x * kWarpRows + threadIdx.y : blockIdx.x;
+  if (WARP && t >= a.T) return;
   float x[P][V], z[P][V];
   float ss = 0.f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int c = (threadIdx.x + p * N) * V;
+    const int c = (threadIdx.x + p * across) * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) x[p][i] = z[p][i] = 0.f;
     if (c < a.H) {
@@ -74,10 +85,10 @@ __global__ void __launch_bounds__(N) k_block_norm(const __grid_constant__ Args a
   }
   if (a.y) {
     float inv = 1.f;
-    if (a.post) inv = 1.0f / sqrtf(block_sum<N>(ss, red[0]) / float(a.H) + a.eps);
+    if (a.post) inv = 1.0f / sqrtf(row_sum<WARP, N>(ss, red[0]) / float(a.H) + a.eps);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int c = (threadIdx.x + p * N) * V;
+      const int c = (threadIdx.x + p * across) * V;
       if (c < a.H) {
         float w[V], g[V];
         if (a.post && a.w_post) {
@@ -98,7 +109,7 @@ __global__ void __launch_bounds__(N) k_block_norm(const __grid_constant__ Args a
   if (a.xo) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const int c = (threadIdx.x + p * N) * V;
+      const int c = (threadIdx.x + p * across) * V;
       if (c < a.H) {
         float* o = a.xo + t * a.xos + c;
         if (V == 8) {
@@ -116,10 +127,10 @@ __global__ void __launch_bounds__(N) k_block_norm(const __grid_constant__ Args a
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int i = 0; i < V; ++i) ss += x[p][i] * x[p][i];
-  const float inv = 1.0f / sqrtf(block_sum<N>(ss, red[1]) / float(a.H) + a.eps);
+  const float inv = 1.0f / sqrtf(row_sum<WARP, N>(ss, red[1]) / float(a.H) + a.eps);
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const int c = (threadIdx.x + p * N) * V;
+    const int c = (threadIdx.x + p * across) * V;
     if (c < a.H) {
       float w[V];
 #pragma unroll
@@ -168,17 +179,27 @@ extern "C" int moe_block_norm(const moe_block_norm_desc* d, const float* x, long
   a.x = x; a.xo = x_out; a.xn = xn;
   a.y = d->y; a.w_post = d->w_post; a.gate = d->gate; a.w_pre = d->w_pre;
   a.xs = x_stride; a.xos = x_out_stride; a.xns = xn_stride; a.ys = d->y_stride; a.gs = d->gate_stride;
-  a.H = H; a.post = d->post_norm ? 1 : 0; a.sig = d->gate_sigmoid ? 1 : 0;
+  a.T = T; a.H = H; a.post = d->post_norm ? 1 : 0; a.sig = d->gate_sigmoid ? 1 : 0;
   a.scale = d->res_scale; a.eps = d->eps;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
+  // One piece a thread as far as a CTA goes, in threads for the row's columns, not a power of two: T rows of
+  // H columns with a gate, 8192 x 2048 33.6 us (two pieces 36.5), 4096 x 4096 42.9 (44.4), 2048 x 8192 45.8
+  // (49.6), 1024 x 16384 57.9 with two (72.8 with four): 0.90, 0.82, 0.77 and 0.61 of a
+  // copy's rate.  A warp a row up to 512 columns: 8192 x 512 13.2 us (CTAs 23.1), 16384 x 256 12.1 (40.4), but
+  // 8192 x 1024 28.1 (CTAs 21.1) and 4 x 1024 4.5 (2.4).  Rows that are not aligned go a column at a time:
+  // 4096 x 4095 88.9 us with eight a thread (sixteen 111, four 102), 0.39 of a copy's rate.
+  auto threads = [&](int columns) { return dim3((((H - 1) / columns + 1) + 31) / 32 * 32); };
   if (vec) {
-    e = H <= 2048   ? launch_pdl(bnorm::k_block_norm<256, 1, 8>, dim3(T), dim3(256), 0, s, a)
-        : H <= 4096 ? launch_pdl(bnorm::k_block_norm<256, 2, 8>, dim3(T), dim3(256), 0, s, a)
-                    : launch_pdl(bnorm::k_block_norm<1024, 2, 8>, dim3(T), dim3(1024), 0, s, a);
+    e = H <= 512    ? launch_pdl(bnorm::k_block_norm<true, 32 * bnorm::kWarpRows, 2, 8>, dim3((T - 1) / bnorm::kWarpRows + 1),
+                                 dim3(32, bnorm::kWarpRows), 0, s, a)
+        : H <= 2048 ? launch_pdl(bnorm::k_block_norm<false, 256, 1, 8>, dim3(T), threads(8), 0, s, a)
+        : H <= 4096 ? launch_pdl(bnorm::k_block_norm<false, 512, 1, 8>, dim3(T), threads(8), 0, s, a)
+        : H <= 8192 ? launch_pdl(bnorm::k_block_norm<false, 1024, 1, 8>, dim3(T), threads(8), 0, s, a)
+                    : launch_pdl(bnorm::k_block_norm<false, 1024, 2, 8>, dim3(T), threads(16), 0, s, a);
   } else {
-    e = H <= 4096 ? launch_pdl(bnorm::k_block_norm<256, 16, 1>, dim3(T), dim3(256), 0, s, a)
-                  : launch_pdl(bnorm::k_block_norm<1024, 16, 1>, dim3(T), dim3(1024), 0, s, a);
+    e = H <= 4096 ? launch_pdl(bnorm::k_block_norm<false, 512, 8, 1>, dim3(T), threads(8), 0, s, a)
+                  : launch_pdl(bnorm::k_block_norm<false, 1024, 16, 1>, dim3(T), threads(16), 0, s, a);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }

@@ -62,6 +62,12 @@ CASES = [
     (2, 16383, 0, 0, True, True, "token", True, 1.0),
     (300, 264, 16, 8, True, True, "token", True, 1.0),
     (9, 512, 0, 0, False, False, None, False, 1.0),
+    (5, 8, 0, 0, True, True, "token", True, 1.0),
+    (6, 256, 8, 0, True, True, "row", True, 1.0),
+    (5, 520, 0, 0, True, True, "token", True, 1.0),
+    (3, 4104, 8, 8, True, True, "token", True, 1.0),
+    (3, 8192, 0, 0, True, True, "token", False, 1.0),
+    (3, 8200, 0, 0, True, True, "row", True, 1.0),
 ]
 
 

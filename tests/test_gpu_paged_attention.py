@@ -84,6 +84,36 @@ def test_peaked_scores(e4m3):
     check(Paged([1500, 300], [4, 2], 2, 128, 32, e4m3, seed=8, k_std=3.0), 16, q_std=8.0)
 
 
+@pytest.mark.parametrize("G,n", [(4, 1), (8, 7)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_of_any_size_against_e4m3_keys(D, G, n):
+    """Rows from 2^-125 up to 2^12 and zeros, columns 20 powers of two apart; infinities and NaN stay in their rows."""
+    g = torch.Generator().manual_seed(D + G)
+    P = Paged([700, 333], [n, n], 2, D, 32, True, seed=D)
+    q = strided_rows(P.T, 2 * G, D, 8, g)
+    q *= (2.0 ** -torch.randint(0, 21, (P.T, 1, D), generator=g)).to(torch.bfloat16)
+    size = torch.tensor([0, 12, -30, -64, -112, -125, -3, 8])
+    q *= (2.0 ** size[torch.randint(0, 8, (P.T, 2 * G, 1), generator=g)].double()).float().to(torch.bfloat16)
+    q[0, 0] = 0
+    q[0, 1, 5] = float("inf")
+    q[1, 2, 7] = float("nan")
+    scale = D ** -0.5
+    o = run(P, q, 2 * G, scale, 0, 8).cpu().double()
+    ref, tol = attention_ref(P, q, 2 * G, scale, 0)
+    assert o[0, 1].isnan().all() and o[1, 2].isnan().all()
+    fine = torch.ones(P.T, 2 * G, dtype=torch.bool)
+    fine[0, 1] = fine[1, 2] = False
+    # a column is off by 2^-22 of its row's largest at most; its score then by that of sum |k|, and a
+    # weight by twice the largest such; rows below 2^-103 score less than 2^-90 and count as zeros
+    for b in range(2):
+        for h in range(2):
+            k, v = P.rows("k", b, h).abs().sum(1).max(), P.rows("v", b, h).abs().amax(0)
+            rows, heads = slice(b * n, (b + 1) * n), slice(h * G, (h + 1) * G)
+            most = q[rows, heads].double().abs().amax(-1, keepdim=True)
+            tol[rows, heads] += 2 * 2.0 ** -22 * most * k * scale * v
+    assert ((o - ref).abs() <= tol)[fine].all()
+
+
 def test_scores_that_rise_along_the_cache():
     P = Paged([1200], [1], 1, 64, 16)
     for j in range(1200):  # key j scores about j / 16
