@@ -3,7 +3,7 @@
 //   x' = x + s * g * z,   xn = w_pre * x' * rsqrt(mean x'^2 + eps).
 // The row stays in registers between its two sums of squares (both fp32), so x
 // and y are read once and x' and xn written once, 12 bytes a column, and memory
-// bounds it: 8192 rows of 2048 columns, 201 MB, 34.1 us, 5.9 TB/s (88% of what a
+// bounds it: 8192 rows of 2048 columns, 201 MB, 32.4 us, 6.2 TB/s (93% of what a
 // copy reaches).  One rounding, of xn to bf16.
 #include "internal.h"
 
@@ -54,10 +54,11 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, float f[V]) {
 }
 
 // A row has a warp (a CTA's warps take a row each) or a CTA of at most N threads; a thread holds P
-// pieces of V columns.
+// pieces of V columns.  Registers for all of an SM's threads where there is one piece (8192 x 2048 34.1 us
+// with 37 registers, 32.4 with 32), and for four CTAs of 512 a column at a time (89, 81).
 constexpr int kWarpRows = 4;
 template <bool WARP, int N, int P, int V>
-__global__ void __launch_bounds__(N) k_block_norm(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(N, P == 1 ? 2048 / N : V == 1 && N == 512 ? 4 : 1) k_block_norm(const __grid_constant__ Args a) {
   pdl_trigger();
   pdl_wait();
   __shared__ float red[2][N / 32];
@@ -186,11 +187,11 @@ extern "C" int moe_block_norm(const moe_block_norm_desc* d, const float* x, long
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   // One piece a thread as far as a CTA goes, in threads for the row's columns, not a power of two: T rows of
-  // H columns with a gate, 8192 x 2048 34 us (two pieces 36.5), 4096 x 4096 42.9 (44.4), 2048 x 8192 45.8
-  // (49.6), 1024 x 16384 57.9 with two (72.8 with four): 0.90, 0.82, 0.77 and 0.61 of a
-  // copy's rate.  A warp a row up to 512 columns: 8192 x 512 13.2 us (CTAs 23.1), 16384 x 256 12.1 (40.4), but
-  // 8192 x 1024 28.1 (CTAs 21.1) and 4 x 1024 4.5 (2.4).  Rows that are not aligned go a column at a time:
-  // 4096 x 4095 88.9 us with eight a thread (sixteen 111, four 102), 0.39 of a copy's rate.
+  // H columns with a gate, 8192 x 2048 32.4 us (two pieces 36.5), 4096 x 4096 39.6 (44.4), 2048 x 8192 45.8
+  // (49.6), 1024 x 16384 57.5 with two (72.8 with four): 0.93, 0.89, 0.77 and 0.61 of a copy's rate.  A warp a
+  // row up to 512 columns: 8192 x 512 12.9 us (CTAs 23.1), 16384 x 256 12.2 (40.4), but 8192 x 1024 28.1 (CTAs
+  // 20.2) and 4 x 1024 4.5 (2.3).  Rows that are not aligned go a column at a time: 4096 x 4095 81 us with eight
+  // a thread (sixteen 111, four 102), 0.43 of a copy's rate.
   auto threads = [&](int columns) { return dim3((((H - 1) / columns + 1) + 31) / 32 * 32); };
   if (vec) {
     e = H <= 512    ? launch_pdl(bnorm::k_block_norm<true, 32 * bnorm::kWarpRows, 2, 8>, dim3((T - 1) / bnorm::kWarpRows + 1),
