@@ -63,7 +63,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 // Eight columns of one head to where they belong: head < Hq is a query, then keys, then values.
 template <bool E4M3>
-__device__ __forceinline__ void store8(const Args& a, int t, int head, int col, const float f[8], int D, long long at) {
+__device__ __forceinline__ void store8(const Args& a, int t, int head, int col, const float f[8], int D, long long at,
+                                       float scale) {
   if (head < a.Hq) {
     *reinterpret_cast<uint4*>(a.qo + (long long)t * a.qos + head * D + col) = pack8(f);
     return;
@@ -76,10 +77,12 @@ __device__ __forceinline__ void store8(const Args& a, int t, int head, int col, 
     *reinterpret_cast<uint4*>(dst + 2 * col) = pack8(f);
   } else {
     const float* sc = is_v ? a.kv.v_scale : a.kv.k_scale;
-    const float s = sc ? sc[h] : 1.0f;
+    // Times the scale's reciprocal: off by 2^-23 of the quotient before a rounding to 2^-4 of it.  A division
+    // for each column took 19.9 us instead of 17.1 for 4096 tokens of 32 + 2 x 4 heads of 128.
+    const float r = 1.0f / scale;
     uint2 u;
-    u.x = e4m3x2(f[0] / s, f[1] / s) | (e4m3x2(f[2] / s, f[3] / s) << 16);
-    u.y = e4m3x2(f[4] / s, f[5] / s) | (e4m3x2(f[6] / s, f[7] / s) << 16);
+    u.x = e4m3x2(f[0] * r, f[1] * r) | (e4m3x2(f[2] * r, f[3] * r) << 16);
+    u.y = e4m3x2(f[4] * r, f[5] * r) | (e4m3x2(f[6] * r, f[7] * r) << 16);
     *reinterpret_cast<uint2*>(dst + col) = u;
   }
 }
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   struct Item {
     int head, c0, c1, pair;  // its pairs are 8 pair .. 8 pair + 7; < 0: the columns stay as they are
     uint4 v0, v1;
+    float scale;  // of a key's or value's head, E4M3
   };
   auto fetch = [&](int it, Item& x) {
     x.head = -1;
@@ -121,6 +125,11 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
                                                    : a.v + (long long)t * a.vs + (head - a.Hq - a.kv.Hkv) * D;
     x.v0 = *reinterpret_cast<const uint4*>(src + x.c0);
     x.v1 = *reinterpret_cast<const uint4*>(src + x.c1);
+    if (E4M3) {
+      const bool is_v = head >= a.Hq + a.kv.Hkv;
+      const float* sc = is_v ? a.kv.v_scale : a.kv.k_scale;
+      x.scale = head >= a.Hq && sc ? sc[head - a.Hq - (is_v ? a.kv.Hkv : 0)] : 1.0f;
+    }
   };
   Item x[kMine];
 #pragma unroll
@@ -182,8 +191,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
         }
       }
     }
-    store8<E4M3>(a, t, x.head, x.c0, f0, D, at);
-    store8<E4M3>(a, t, x.head, x.c1, f1, D, at);
+    store8<E4M3>(a, t, x.head, x.c0, f0, D, at, x.scale);
+    store8<E4M3>(a, t, x.head, x.c1, f1, D, at, x.scale);
   };
 #pragma unroll
   for (int i = 0; i < kMine; ++i) put(x[i]);
