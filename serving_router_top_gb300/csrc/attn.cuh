@@ -1391,8 +1391,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_many(const __grid_constan
 // tile that holds a request's rows, and above 64 rows the two 128-row tiles of attn_chunk.cuh where it
 // applies.  A tile holds the heads of whole tokens.
 constexpr int kChunkRows = 256;
-inline int row_tile(int D, int e4m3, int G, int n) {
-  return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || e4m3 || D > 128 ? 64 : kChunkRows;
+inline int row_tile(int D, int G, int n) {
+  return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || D > 128 ? 64 : kChunkRows;
 }
 
 template <int D, int NR, bool E4M3>

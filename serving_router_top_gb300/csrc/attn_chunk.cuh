@@ -27,17 +27,8 @@ namespace chunk {
 
 constexpr float kGrow = 8.0f;  // log2
 
-template <int D>
-struct Cfg {
-  static constexpr int SLOT = kKeys * D * 2, QTILE = 128 * D * 2;
-  static constexpr int NS0 = (kSmem - misc_bytes(128) - 2 * QTILE) / SLOT, NS = NS0 > 8 ? 8 : NS0 / 2 * 2;  // even: K and V in turn
-  static constexpr int MMA = 8, LOAD = 9, THREADS = 32 * 11;  // warps 0-3 and 4-7: softmax of a row tile each
-  static constexpr int V = SLOT >= 32768 ? 2 : 3;             // as in attn.cuh, by the bytes of a tile
-  static_assert(NS >= 4, "shared memory of an SM");
-};
-
 struct Misc {
-  uint64_t full[8], empty[8], qfull, qfree, sfull[2], pfull[2], pvdone[2], ofree[2], drain;
+  uint64_t full[8], empty[8], rfull[8], rempty[8], qfull, qfree, sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
   int fail;
   PlanShared plan;
@@ -45,7 +36,19 @@ struct Misc {
   int nbad[4];  // keys of a tile with values that are not finite, of four tiles in turn
   uint8_t bad[4][kKeys];
 };
-static_assert(sizeof(Misc) <= misc_bytes(128), "misc");
+constexpr int kMisc = (sizeof(Misc) + 127) / 128 * 128;
+
+template <int D, bool E4M3>
+struct Cfg {
+  static constexpr int SLOT = kKeys * D * 2, QTILE = 128 * D * 2, RAW = E4M3 ? kKeys * D : 0;
+  // even: keys and values in turn.  E4M3: a ring of bf16 and one of the codes as they come.
+  static constexpr int FREE = kSmem - kMisc - 2 * QTILE, NS0 = E4M3 ? 4 : FREE / SLOT, NS = NS0 > 8 ? 8 : NS0 / 2 * 2;
+  static constexpr int NR0 = E4M3 ? (FREE - NS * SLOT) / (RAW + !E4M3) : 0, NRAW = NR0 > 8 ? 8 : NR0 / 2 * 2;
+  static constexpr int MMA = 8, LOAD = 9, CONVERT = 12;  // warps 0-3 and 4-7: softmax of a row tile each
+  static constexpr int THREADS = 32 * (E4M3 ? 16 : 11);
+  static constexpr int V = SLOT >= 32768 ? 2 : 3;  // as in attn.cuh, by the bytes of a tile
+  static_assert(NS >= 4 && (!E4M3 || NRAW >= 2), "shared memory of an SM");
+};
 
 // Four steps of 16 keys: A (P) from tensor memory, eight columns a step, B (V) 2048 bytes on.
 __device__ __forceinline__ void mma4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -88,13 +91,24 @@ __device__ __forceinline__ void turn4(float (&v)[16], int lane) {
       }
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_constant__ Args a) {
-  using C = Cfg<D>;
+// Registers a thread from here on, of a warpgroup.
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void leave_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid_constant__ Args a) {
+  using C = Cfg<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* sq = ring + C::NS * C::SLOT;
-  Misc& ms = *reinterpret_cast<Misc*>(sq + 2 * C::QTILE);
+  uint8_t* raw = sq + 2 * C::QTILE;  // E4M3: tiles as they come
+  Misc& ms = *reinterpret_cast<Misc*>(raw + C::NRAW * C::RAW);
   volatile int* fail = &ms.fail;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -104,8 +118,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   } else if (tid == 32 * C::LOAD) {
     for (int i = 0; i < C::NS; ++i) {
-      bar_init(&ms.full[i], 1);
+      bar_init(&ms.full[i], E4M3 ? 4 : 1);
       bar_init(&ms.empty[i], 1);
+    }
+    for (int i = 0; i < C::NRAW; ++i) {
+      bar_init(&ms.rfull[i], 1);
+      bar_init(&ms.rempty[i], 4);
     }
     bar_init(&ms.qfull, 1);
     bar_init(&ms.qfree, 1);
@@ -134,132 +152,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
     w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
     const int half = a.tokens / 2;  // tokens of a row tile
     auto both = [&]() { return w.s.i1 - w.s.i0 + 1 > half; };  // the unit has rows for the second row tile
-    if (warp == C::MMA) {
-      // -------------------------------------------------------- tensor cores
-      // D f32, A and B bf16, M = 128; S: N = 128 keys, both K-major; O: N = D, B (V) MN-major
-      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
-      constexpr uint32_t kIdescS = kBase | (uint32_t(kKeys >> 3) << 17), kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
-      Ring<C::NS> kr(0), vr(0);
-      vr.next();
-      int scores[2] = {0, 0}, pieces[2] = {0, 0}, qn = 0;  // S products and pieces of each row tile, pieces of the run
-      auto put_s = [&](int x) {  // S = Q K(n)^T; its columns hold the last P until that product is done
-        if (scores[x] > 0) wait(&ms.pvdone[x], (scores[x] - 1) & 1, fail);
-        ++scores[x];
-        tc_after();
-        const uint64_t qd = desc(su32(sq + x * C::QTILE), 16, 1024, 2), kd = desc(su32(ring + kr.slot * C::SLOT), 16, 1024, 2);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          mma4<2, 2>(taddr + x * 128, qd + k * (128 * 128 >> 4), kd + k * (kKeys * 128 >> 4), kIdescS, k > 0);
-        commit_to(&ms.sfull[x]);
-      };
-      auto begin = [&]() {  // the tile's keys are there, and the queries of its piece
-        if (w.j == w.jbeg) wait(&ms.qfull, qn++ & 1, fail);
-        wait(&ms.full[kr.slot], kr.phase, fail);
-      };
-      auto end = [&]() {
-        commit_to(&ms.empty[kr.slot]);
-        if (w.j + 1 == w.jend) commit_to(&ms.qfree);
-        kr.next();
-        kr.next();
-      };
-      begin();
-      put_s(0);
-      if (both()) put_s(1);
-      end();
-#pragma unroll 1
-      for (int n = 0; n < count; ++n) {
-        const bool first = w.j == w.jbeg, two = both(), more = n + 1 < count;
-        auto put_o = [&](int x) {  // O += P V(n)
-          wait(&ms.pfull[x], (scores[x] - 1) & 1, fail);
-          if (first && pieces[x]++ > 0) wait(&ms.ofree[x], (pieces[x] - 2) & 1, fail);
-          tc_after();
-          const uint64_t vd = desc(su32(ring + vr.slot * C::SLOT), kKeys * 128, 1024, 2);
-#pragma unroll
-          for (int k = 0; k < kKeys / 64; ++k)
-            mma4_ta(taddr + 256 + x * D, taddr + x * 128 + k * 32, vd + k * 512, kIdescO, !first || k > 0);
-          commit_to(&ms.pvdone[x]);
-        };
-        wait(&ms.full[vr.slot], vr.phase, fail);
-        put_o(0);
-        if (more) {
-          w.next(a, cap);
-          begin();
-          put_s(0);
-        }
-        if (two) put_o(1);
-        commit_to(&ms.empty[vr.slot]);
-        vr.next();
-        vr.next();
-        if (more) {
-          if (both()) put_s(1);
-          end();
-        }
-      }
-      commit_to(&ms.drain);
-      const unsigned long long t0 = now_ns();
-      for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(su32(&ms.drain))
-            : "memory");
-    } else if (warp >= C::LOAD) {
-      // -------------------------------------------------------- loads: keys and queries, values
-      const bool keys = warp == C::LOAD;
-      const KvView& kv = a.kv;
-      const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
-      const CUtensorMap* tm = keys ? &a.mk : &a.mv;
-      int* page = ms.page[keys ? 0 : 1];
-      Ring<C::NS> rg(1);
-      if (!keys) rg.next();
-      int qn = 0;
-#pragma unroll 1
-      for (int n = 0; n < count; ++n) {
-        if (keys && w.j == w.jbeg) {
-          if (qn > 0) wait(&ms.qfree, (qn - 1) & 1, fail);
-          ++qn;
-          if (lane == 0 && !*fail) {
-            const int tiles = both() ? 2 : 1;
-            expect(&ms.qfull, uint32_t(tiles * half * a.G * D * 2));
-            for (int x = 0; x < tiles; ++x)
-              for (int c = 0; c < D / 64; ++c)
-                load_rows(sq + x * C::QTILE + c * (128 * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0 + x * half,
-                          &ms.qfull);
-          }
-        }
-        const int key0 = (w.s.tile0 + w.j) * kKeys;
-        const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
-        for (int x = lane; x < boxes; x += 32) {
-          const int key = key0 + (x << box_shift);
-          int id = -2;
-          if (key < w.s.hi && key + (1 << box_shift) > w.s.lo) id = row[key >> kv.page_shift];
-          const bool ok = id >= 0 && id < kv.npages;
-          if (!ok && id != -2) set_error(a.err, MOE_ERANGE);
-          page[x] = ok ? id : kv.npages;  // past the end: zeros
-        }
-        __syncwarp();
-        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
-        wait(&ms.empty[rg.slot], rg.phase, fail);
-        if (!*fail) {
-          if (lane == 0) expect(&ms.full[rg.slot], C::SLOT);
-          __syncwarp();
-#pragma unroll 1
-          for (int x = lane; x < boxes * (D / 64); x += 32) {
-            const int p = x & (boxes - 1), c = x >> (7 - box_shift);
-            load_box(ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128, tm, c * 64, tok, w.h, page[p],
-                     &ms.full[rg.slot]);
-          }
-        }
-        __syncwarp();
-        rg.next();
-        rg.next();
-        if (n + 1 < count) w.next(a, cap);
-      }
-    } else {
+    if (warp < C::MMA) {
+      // A row a thread takes more than the 128 registers that 512 threads start with; the others need few.
+      static_assert(!E4M3 || 256 * (176 + 72) <= C::THREADS * 128, "registers of the launch");
+      if (E4M3) take_registers<176>();
       // -------------------------------------------------------- softmax, a row a thread
       const int x = warp >> 2, quad = warp & 3, krow = quad * 32 + lane;  // row tile; row in it, and key in a tile
       const uint32_t ts = taddr + (uint32_t(quad * 32) << 16) + x * 128, to = taddr + (uint32_t(quad * 32) << 16) + 256 + x * D;
-      const float factor = a.scale * 1.4426950408889634f;
+      float factor = a.scale * 1.4426950408889634f;
       const int mine = x * half + krow / a.G;  // the row's token in its unit
       float m = kUnset, l = 0.f;
       int spoiled_key0 = 0;
@@ -273,9 +173,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
         for (int e = 0; e < nbad; ++e) {
           const int key = spoiled_key0 + ms.bad[spoiled & 3][e];
           const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (key >> a.kv.page_shift)];
-          const uint16_t* v = reinterpret_cast<const uint16_t*>(
-              a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
-              (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride);
+          const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
+                             (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
           const bool sees = key <= pos && (a.window <= 0 || key > pos - a.window);
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -284,7 +183,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
             ld_wait();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float add = bf16_bits_to_f32(v[c + i]);
+              const float add = E4M3 ? f16x2_to_f32x2(e4m3x2_to_f16x2(v[c + i])).x
+                                     : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[c + i]);
               if (sees && !isfinite(add)) o[i] += add;
             }
             st16(to + c, o);
@@ -300,6 +200,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
         if (active) {
           const bool first = w.j == w.jbeg;
           if (first) m = kUnset, l = 0.f;
+          if (E4M3 && first) factor = a.scale * 1.4426950408889634f * (a.kv.k_scale ? a.kv.k_scale[w.h] : 1.f);
           const int newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
           const int pos = min(w.r.pos0 + w.s.i0 + mine, newest);
           const int key0 = (w.s.tile0 + w.j) * kKeys;
@@ -394,7 +295,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
             const int unit_row = x * half * a.G + krow, rows = min(half, w.s.i1 - w.s.i0 + 1 - x * half) * a.G;
             const long long part = (2ll * run + (head ? 0 : 1)) * kChunkRows + unit_row;
             if (split && krow < rows) reinterpret_cast<float2*>(a.ml)[part] = make_float2(m, l);
-            const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;  // a sum of zero is a row that sees no key; its O is zeros
+            const float vs = E4M3 && a.kv.v_scale ? a.kv.v_scale[w.h] : 1.f;
+            const float inv = split ? 1.f : l == 0.f ? 0.f : vs / l;  // a sum of zero is a row that sees no key; its O is zeros
             unsigned long long row = reinterpret_cast<unsigned long long>(a.part + part * D);
             if (!split)
               row = reinterpret_cast<unsigned long long>(a.o + (long long)(w.r.s0 + w.s.i0 + mine) * a.os +
@@ -428,6 +330,165 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
         }
         if (n + 1 < count) w.next(a, cap);
       }
+    } else {
+      if (E4M3) leave_registers<72>();
+      if (warp == C::MMA) {
+      // -------------------------------------------------------- tensor cores
+      // D f32, A and B bf16, M = 128; S: N = 128 keys, both K-major; O: N = D, B (V) MN-major
+      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
+      constexpr uint32_t kIdescS = kBase | (uint32_t(kKeys >> 3) << 17), kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
+      Ring<C::NS> kr(0), vr(0);
+      vr.next();
+      int scores[2] = {0, 0}, pieces[2] = {0, 0}, qn = 0;  // S products and pieces of each row tile, pieces of the run
+      auto put_s = [&](int x) {  // S = Q K(n)^T; its columns hold the last P until that product is done
+        if (scores[x] > 0) wait(&ms.pvdone[x], (scores[x] - 1) & 1, fail);
+        ++scores[x];
+        tc_after();
+        const uint64_t qd = desc(su32(sq + x * C::QTILE), 16, 1024, 2), kd = desc(su32(ring + kr.slot * C::SLOT), 16, 1024, 2);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          mma4<2, 2>(taddr + x * 128, qd + k * (128 * 128 >> 4), kd + k * (kKeys * 128 >> 4), kIdescS, k > 0);
+        commit_to(&ms.sfull[x]);
+      };
+      auto begin = [&]() {  // the tile's keys are there, and the queries of its piece
+        if (w.j == w.jbeg) wait(&ms.qfull, qn++ & 1, fail);
+        wait(&ms.full[kr.slot], kr.phase, fail);
+      };
+      auto end = [&]() {
+        commit_to(&ms.empty[kr.slot]);
+        if (w.j + 1 == w.jend) commit_to(&ms.qfree);
+        kr.next();
+        kr.next();
+      };
+      begin();
+      put_s(0);
+      if (both()) put_s(1);
+      end();
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        const bool first = w.j == w.jbeg, two = both(), more = n + 1 < count;
+        auto put_o = [&](int x) {  // O += P V(n)
+          wait(&ms.pfull[x], (scores[x] - 1) & 1, fail);
+          if (first && pieces[x]++ > 0) wait(&ms.ofree[x], (pieces[x] - 2) & 1, fail);
+          tc_after();
+          const uint64_t vd = desc(su32(ring + vr.slot * C::SLOT), kKeys * 128, 1024, 2);
+#pragma unroll
+          for (int k = 0; k < kKeys / 64; ++k)
+            mma4_ta(taddr + 256 + x * D, taddr + x * 128 + k * 32, vd + k * 512, kIdescO, !first || k > 0);
+          commit_to(&ms.pvdone[x]);
+        };
+        wait(&ms.full[vr.slot], vr.phase, fail);
+        put_o(0);
+        if (more) {
+          w.next(a, cap);
+          begin();
+          put_s(0);
+        }
+        if (two) put_o(1);
+        commit_to(&ms.empty[vr.slot]);
+        vr.next();
+        vr.next();
+        if (more) {
+          if (both()) put_s(1);
+          end();
+        }
+      }
+      commit_to(&ms.drain);
+      const unsigned long long t0 = now_ns();
+      for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(&ms.drain))
+            : "memory");
+    } else if (warp == C::LOAD || warp == C::LOAD + 1) {
+      // -------------------------------------------------------- loads: keys and queries, values
+      const bool keys = warp == C::LOAD;
+      const KvView& kv = a.kv;
+      const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
+      const CUtensorMap* tm = keys ? &a.mk : &a.mv;
+      int* page = ms.page[keys ? 0 : 1];
+      Ring<E4M3 ? C::NRAW : C::NS> rg(1);
+      if (!keys) rg.next();
+      int qn = 0;
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        if (keys && w.j == w.jbeg) {
+          if (qn > 0) wait(&ms.qfree, (qn - 1) & 1, fail);
+          ++qn;
+          if (lane == 0 && !*fail) {
+            const int tiles = both() ? 2 : 1;
+            expect(&ms.qfull, uint32_t(tiles * half * a.G * D * 2));
+            for (int x = 0; x < tiles; ++x)
+              for (int c = 0; c < D / 64; ++c)
+                load_rows(sq + x * C::QTILE + c * (128 * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0 + x * half,
+                          &ms.qfull);
+          }
+        }
+        const int key0 = (w.s.tile0 + w.j) * kKeys;
+        const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
+        for (int x = lane; x < boxes; x += 32) {
+          const int key = key0 + (x << box_shift);
+          int id = -2;
+          if (key < w.s.hi && key + (1 << box_shift) > w.s.lo) id = row[key >> kv.page_shift];
+          const bool ok = id >= 0 && id < kv.npages;
+          if (!ok && id != -2) set_error(a.err, MOE_ERANGE);
+          page[x] = ok ? id : kv.npages;  // past the end: zeros
+        }
+        __syncwarp();
+        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
+        uint64_t* full = (E4M3 ? ms.rfull : ms.full) + rg.slot;
+        wait((E4M3 ? ms.rempty : ms.empty) + rg.slot, rg.phase, fail);
+        if (!*fail) {
+          if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
+          __syncwarp();
+          constexpr int CHUNKS = E4M3 ? 1 : D / 64;
+#pragma unroll 1
+          for (int x = lane; x < boxes * CHUNKS; x += 32) {
+            const int p = x & (boxes - 1), c = x >> (7 - box_shift);
+            uint8_t* dst = E4M3 ? raw + rg.slot * C::RAW + (p << box_shift) * D
+                                : ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
+            load_box(dst, tm, c * 64, tok, w.h, page[p], full);
+          }
+        }
+        __syncwarp();
+        rg.next();
+        rg.next();
+        if (n + 1 < count) w.next(a, cap);
+      }
+    } else if (warp >= C::CONVERT) {
+      // -------------------------------------------------------- E4M3 codes -> bf16, in the ring's order
+      if constexpr (E4M3) {
+        const int vt = tid - 32 * C::CONVERT;
+        constexpr int CH = D / 8, STEP = 128 / CH;  // 8 codes a thread make one 16-byte piece
+        const int r0 = vt / CH, c = vt % CH;
+        Ring<C::NRAW> in(0);
+        Ring<C::NS> out(1);
+#pragma unroll 1
+        for (int n = 0; n < 2 * count; ++n) {
+          wait(&ms.rfull[in.slot], in.phase, fail);
+          wait(&ms.empty[out.slot], out.phase, fail);
+          const uint8_t* src = raw + in.slot * C::RAW + c * 8;
+          uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
+#pragma unroll 4
+          for (int i = 0; i < kKeys / STEP; ++i) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src + (r0 + i * STEP) * D);
+            uint32_t o[4];
+            e4m3x4_to_bf16x4(v.x, o);
+            e4m3x4_to_bf16x4(v.y, o + 2);
+            *reinterpret_cast<uint4*>(dst + sw128(r0 + i * STEP, c % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) {
+            arrive(&ms.full[out.slot]);
+            arrive(&ms.rempty[in.slot]);
+          }
+          in.next();
+          out.next();
+        }
+      }
+      }
     }
   }
   __syncthreads();
@@ -438,15 +499,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_chunk(const __grid_const
   }
 }
 
-template <int D>
+template <int D, bool E4M3>
 int launch(const Args& a, int ctas, cudaStream_t s) {
-  if (launch_pdl(k_chunk<D>, dim3(ctas), dim3(Cfg<D>::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
+  if (launch_pdl(k_chunk<D, E4M3>, dim3(ctas), dim3(Cfg<D, E4M3>::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
   return launch_pdl(k_join<D, 256>, dim3(ctas, join_y(256)), dim3(kJoinThreads), 0, s, a) == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
-template <int D>
+template <int D, bool E4M3>
 int opt_in() {
   return cudaFuncSetAttribute(k_join<D, 256>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
-                 cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
+                 cudaFuncSetAttribute(k_chunk<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
              ? MOE_OK
              : MOE_ECUDA;
 }

@@ -122,7 +122,7 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   if (T == 0 || b->B == 0) return MOE_OK;
   const long long width = (long long)Hq * kv->D;
   if (!rows_ok(q, q_stride, T, width) || !rows_ok(o, o_stride, T, width)) return MOE_EINVAL;
-  const int nr = attn::row_tile(kv->D, kv->e4m3, Hq / kv->Hkv, b->max_n > 1 ? b->max_n : 1);
+  const int nr = attn::row_tile(kv->D, Hq / kv->Hkv, b->max_n > 1 ? b->max_n : 1);
   a.o = o;
   a.os = T > 1 ? o_stride : width;
   a.q = q;
@@ -143,8 +143,10 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   const cuuint64_t qdims[3] = {cuuint64_t(kv->D), cuuint64_t(Hq), cuuint64_t(T)};
   const cuuint64_t qpitches[2] = {cuuint64_t(kv->D) * 2, cuuint64_t(T > 1 ? q_stride : width) * 2};
   const cuuint32_t qbox[3] = {64, cuuint32_t(a.G), cuuint32_t(tile)};
-  // operands of the tensor core are swizzled by their rows; E4M3 values become one later
-  const CUtensorMapSwizzle k_swizzle = kv->e4m3 && kv->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  // operands of the tensor core are swizzled by their rows; E4M3 values, and a chunk's keys, become one later
+  const CUtensorMapSwizzle k_swizzle = !kv->e4m3 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : nr == attn::kChunkRows ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                       : kv->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   const CUtensorMapSwizzle v_swizzle = kv->e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
   if (!attn::encode(&a.mk, kv->k, kv->e4m3, 4, dims, pitches, boxes, k_swizzle) ||
       !attn::encode(&a.mv, kv->v, kv->e4m3, 4, dims, pitches, boxes, v_swizzle) ||

@@ -10,14 +10,15 @@ int launch_d128(const Args& a, int e4m3, int nr, int sms, cudaStream_t s) {
     switch (nr) {
       case 16: return launch_one<128, 16, true>(a, sms, s);
       case 32: return launch_one<128, 32, true>(a, sms, s);
-      default: return launch_one<128, 64, true>(a, sms, s);
+      case 64: return launch_one<128, 64, true>(a, sms, s);
+      default: return chunk::launch<128, true>(a, sms, s);
     }
   } else {
     switch (nr) {
       case 16: return launch_one<128, 16, false>(a, sms, s);
       case 32: return launch_one<128, 32, false>(a, sms, s);
       case 64: return launch_one<128, 64, false>(a, sms, s);
-      default: return chunk::launch<128>(a, sms, s);
+      default: return chunk::launch<128, false>(a, sms, s);
     }
   }
 }
@@ -26,7 +27,8 @@ int opt_in_d128() {
   return opt_in<128, 16, false>() ||
                  opt_in<128, 32, false>() ||
                  opt_in<128, 64, false>() ||
-                 chunk::opt_in<128>() ||
+                 chunk::opt_in<128, false>() ||
+                 chunk::opt_in<128, true>() ||
                  opt_in<128, 16, true>() ||
                  opt_in<128, 32, true>() ||
                  opt_in<128, 64, true>()

@@ -153,23 +153,25 @@ def test_any_scale(scale, n):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G", [1, 3, 8, 20, 64])
 @pytest.mark.parametrize("window", [0, 70])
-def test_chunks(D, G, window):
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunks(D, G, window, e4m3):
     """Row tiles of two 128s: whole and ragged ones, one of the two empty, several units and splits."""
     per = 128 // G
     ns = [2 * per, per + 1, per, 4 * per + 3, 1]
     lens = [n + e for n, e in zip(ns, [700, 0, 129, 1300, 255])]
-    check(Paged(lens, ns, 2, D, 32, lead=3, seed=G), 2 * G, window)
+    check(Paged(lens, ns, 2, D, 32, e4m3, lead=3, seed=G), 2 * G, window)
 
 
-def test_chunks_with_peaked_scores():
-    check(Paged([900, 600], [90, 300], 2, 128, 32, seed=8, k_std=3.0), 16, q_std=8.0)
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunks_with_peaked_scores(e4m3):
+    check(Paged([900, 600], [90, 300], 2, 128, 32, e4m3, seed=8, k_std=3.0), 16, q_std=8.0)
 
 
-@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("value,e4m3", [(float("nan"), False), (float("inf"), False), (float("nan"), True)])
 @pytest.mark.parametrize("window", [0, 30])
 @pytest.mark.parametrize("D", [64, 128])
-def test_what_a_chunk_s_token_does_not_see_does_not_reach_it(value, window, D):
-    P = Paged([300], [100], 1, D, 16)  # positions 200 .. 299, 8 heads: rows of both tiles
+def test_what_a_chunk_s_token_does_not_see_does_not_reach_it(value, window, D, e4m3):
+    P = Paged([300], [100], 1, D, 16, e4m3)  # positions 200 .. 299, 8 heads: rows of both tiles
     for at in (250, 299, 130):
         P.v[int(P.table[0, at // 16]), 0, at % 16, at % D] = value
     q = strided_rows(P.T, 8, D, 0, torch.Generator().manual_seed(0))
@@ -187,8 +189,9 @@ def test_what_a_chunk_s_token_does_not_see_does_not_reach_it(value, window, D):
     assert near[..., clean].all()
 
 
-def test_chunks_give_the_same_bits_every_time():
-    P = Paged([4000, 500], [333, 200], 2, 128, 64)
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunks_give_the_same_bits_every_time(e4m3):
+    P = Paged([4000, 500], [333, 200], 2, 128, 64, e4m3)
     pages, bt = P.device()
     q = strided_rows(P.T, 16, 128, 0, torch.Generator().manual_seed(0)).cuda()
     ws, first, o = moe.AttnWorkspace(16, 2, 128), torch.empty_like(q), torch.empty_like(q)
