@@ -1,5 +1,5 @@
 // Attention over a paged cache on the tcgen05 tensor cores (new tokens, verify
-// windows, prompt chunks over E4M3 or of 256 columns) and the join of what it splits.
+// windows, prompt chunks of 256 columns) and the join of what it splits.
 //
 // Mathematics.  For one key head, the query rows of a row tile are R = (token,
 // head of the group) pairs, up to NR of them, and the keys come in tiles of 128:
@@ -1389,7 +1389,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_many(const __grid_constan
 
 // Rows of a unit for calls of about n new tokens a request and G query heads a key head: the smallest
 // tile that holds a request's rows, and above 64 rows the two 128-row tiles of attn_chunk.cuh where it
-// applies.  A tile holds the heads of whole tokens.
+// applies, from the first size on: 8 requests of 9 tokens of 8 heads (72 rows) over 4000 E4M3 keys, 128
+// columns 28.6 us (33.8 in 64-row tiles), 64 columns 21.3 (25.8).  A tile holds the heads of whole tokens.
 constexpr int kChunkRows = 256;
 inline int row_tile(int D, int G, int n) {
   return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || D > 128 ? 64 : kChunkRows;

@@ -16,7 +16,11 @@
 //
 // What bounds it: that chain, S, weights, O, of two row tiles in turn, 3000 clocks for 256 rows by 128
 // keys of 128 columns, with the tensor pipe busy 47% of the time.  Two chunks of up to 512 tokens of 32
-// heads over up to 6000 keys: 72.5 us with the join, 966 TFLOP/s.
+// heads over up to 6000 keys: 72.7 us with the join, 964 TFLOP/s; with 64 columns 64 us.
+//
+// E4M3: four warps turn the tiles into bf16, exactly, in the ring's order.  A tile serves 256 rows here, so
+// that is hidden but for 0.3 of a tile's time: the same chunks 83.8 us, 65.9 with 64 columns (attn.cuh's form at
+// 64 rows 166.7 and 129.3).
 #pragma once
 
 #include "attn.cuh"
@@ -152,7 +156,166 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
     w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
     const int half = a.tokens / 2;  // tokens of a row tile
     auto both = [&]() { return w.s.i1 - w.s.i0 + 1 > half; };  // the unit has rows for the second row tile
-    if (warp < C::MMA) {
+    if (warp >= C::MMA) {
+      if (E4M3) leave_registers<72>();
+      if (warp == C::MMA) {
+      // -------------------------------------------------------- tensor cores
+      // D f32, A and B bf16, M = 128; S: N = 128 keys, both K-major; O: N = D, B (V) MN-major
+      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
+      constexpr uint32_t kIdescS = kBase | (uint32_t(kKeys >> 3) << 17), kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
+      Ring<C::NS> kr(0), vr(0);
+      vr.next();
+      int scores[2] = {0, 0}, pieces[2] = {0, 0}, qn = 0;  // S products and pieces of each row tile, pieces of the run
+      auto put_s = [&](int x) {  // S = Q K(n)^T; its columns hold the last P until that product is done
+        if (scores[x] > 0) wait(&ms.pvdone[x], (scores[x] - 1) & 1, fail);
+        ++scores[x];
+        tc_after();
+        const uint64_t qd = desc(su32(sq + x * C::QTILE), 16, 1024, 2), kd = desc(su32(ring + kr.slot * C::SLOT), 16, 1024, 2);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          mma4<2, 2>(taddr + x * 128, qd + k * (128 * 128 >> 4), kd + k * (kKeys * 128 >> 4), kIdescS, k > 0);
+        commit_to(&ms.sfull[x]);
+      };
+      auto begin = [&]() {  // the tile's keys are there, and the queries of its piece
+        if (w.j == w.jbeg) wait(&ms.qfull, qn++ & 1, fail);
+        wait(&ms.full[kr.slot], kr.phase, fail);
+      };
+      auto end = [&]() {
+        commit_to(&ms.empty[kr.slot]);
+        if (w.j + 1 == w.jend) commit_to(&ms.qfree);
+        kr.next();
+        kr.next();
+      };
+      begin();
+      put_s(0);
+      if (both()) put_s(1);
+      end();
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        const bool first = w.j == w.jbeg, two = both(), more = n + 1 < count;
+        auto put_o = [&](int x) {  // O += P V(n)
+          wait(&ms.pfull[x], (scores[x] - 1) & 1, fail);
+          if (first && pieces[x]++ > 0) wait(&ms.ofree[x], (pieces[x] - 2) & 1, fail);
+          tc_after();
+          const uint64_t vd = desc(su32(ring + vr.slot * C::SLOT), kKeys * 128, 1024, 2);
+#pragma unroll
+          for (int k = 0; k < kKeys / 64; ++k)
+            mma4_ta(taddr + 256 + x * D, taddr + x * 128 + k * 32, vd + k * 512, kIdescO, !first || k > 0);
+          commit_to(&ms.pvdone[x]);
+        };
+        wait(&ms.full[vr.slot], vr.phase, fail);
+        put_o(0);
+        if (more) {
+          w.next(a, cap);
+          begin();
+          put_s(0);
+        }
+        if (two) put_o(1);
+        commit_to(&ms.empty[vr.slot]);
+        vr.next();
+        vr.next();
+        if (more) {
+          if (both()) put_s(1);
+          end();
+        }
+      }
+      commit_to(&ms.drain);
+      const unsigned long long t0 = now_ns();
+      for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(&ms.drain))
+            : "memory");
+    } else if (warp == C::LOAD || warp == C::LOAD + 1) {
+      // -------------------------------------------------------- loads: keys and queries, values
+      const bool keys = warp == C::LOAD;
+      const KvView& kv = a.kv;
+      const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
+      const CUtensorMap* tm = keys ? &a.mk : &a.mv;
+      int* page = ms.page[keys ? 0 : 1];
+      Ring<E4M3 ? C::NRAW : C::NS> rg(1);
+      if (!keys) rg.next();
+      int qn = 0;
+#pragma unroll 1
+      for (int n = 0; n < count; ++n) {
+        if (keys && w.j == w.jbeg) {
+          if (qn > 0) wait(&ms.qfree, (qn - 1) & 1, fail);
+          ++qn;
+          if (lane == 0 && !*fail) {
+            const int tiles = both() ? 2 : 1;
+            expect(&ms.qfull, uint32_t(tiles * half * a.G * D * 2));
+            for (int x = 0; x < tiles; ++x)
+              for (int c = 0; c < D / 64; ++c)
+                load_rows(sq + x * C::QTILE + c * (128 * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0 + x * half,
+                          &ms.qfull);
+          }
+        }
+        const int key0 = (w.s.tile0 + w.j) * kKeys;
+        const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
+        for (int x = lane; x < boxes; x += 32) {
+          const int key = key0 + (x << box_shift);
+          int id = -2;
+          if (key < w.s.hi && key + (1 << box_shift) > w.s.lo) id = row[key >> kv.page_shift];
+          const bool ok = id >= 0 && id < kv.npages;
+          if (!ok && id != -2) set_error(a.err, MOE_ERANGE);
+          page[x] = ok ? id : kv.npages;  // past the end: zeros
+        }
+        __syncwarp();
+        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
+        uint64_t* full = (E4M3 ? ms.rfull : ms.full) + rg.slot;
+        wait((E4M3 ? ms.rempty : ms.empty) + rg.slot, rg.phase, fail);
+        if (!*fail) {
+          if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
+          __syncwarp();
+          constexpr int CHUNKS = E4M3 ? 1 : D / 64;
+#pragma unroll 1
+          for (int x = lane; x < boxes * CHUNKS; x += 32) {
+            const int p = x & (boxes - 1), c = x >> (7 - box_shift);
+            uint8_t* dst = E4M3 ? raw + rg.slot * C::RAW + (p << box_shift) * D
+                                : ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
+            load_box(dst, tm, c * 64, tok, w.h, page[p], full);
+          }
+        }
+        __syncwarp();
+        rg.next();
+        rg.next();
+        if (n + 1 < count) w.next(a, cap);
+      }
+    } else if (warp >= C::CONVERT) {
+      // -------------------------------------------------------- E4M3 codes -> bf16, in the ring's order
+      if constexpr (E4M3) {
+        const int vt = tid - 32 * C::CONVERT;
+        constexpr int CH = D / 8, STEP = 128 / CH;  // 8 codes a thread make one 16-byte piece
+        const int r0 = vt / CH, c = vt % CH;
+        Ring<C::NRAW> in(0);
+        Ring<C::NS> out(1);
+#pragma unroll 1
+        for (int n = 0; n < 2 * count; ++n) {
+          wait(&ms.rfull[in.slot], in.phase, fail);
+          wait(&ms.empty[out.slot], out.phase, fail);
+          const uint8_t* src = raw + in.slot * C::RAW + c * 8;
+          uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
+#pragma unroll 4
+          for (int i = 0; i < kKeys / STEP; ++i) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src + (r0 + i * STEP) * D);
+            uint32_t o[4];
+            e4m3x4_to_bf16x4(v.x, o);
+            e4m3x4_to_bf16x4(v.y, o + 2);
+            *reinterpret_cast<uint4*>(dst + sw128(r0 + i * STEP, c % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) {
+            arrive(&ms.full[out.slot]);
+            arrive(&ms.rempty[in.slot]);
+          }
+          in.next();
+          out.next();
+        }
+      }
+      }
+    } else {
       // A row a thread takes more than the 128 registers that 512 threads start with; the others need few.
       static_assert(!E4M3 || 256 * (176 + 72) <= C::THREADS * 128, "registers of the launch");
       if (E4M3) take_registers<176>();
@@ -329,165 +492,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
           ++k;
         }
         if (n + 1 < count) w.next(a, cap);
-      }
-    } else {
-      if (E4M3) leave_registers<72>();
-      if (warp == C::MMA) {
-      // -------------------------------------------------------- tensor cores
-      // D f32, A and B bf16, M = 128; S: N = 128 keys, both K-major; O: N = D, B (V) MN-major
-      constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
-      constexpr uint32_t kIdescS = kBase | (uint32_t(kKeys >> 3) << 17), kIdescO = kBase | (uint32_t(D >> 3) << 17) | (1u << 16);
-      Ring<C::NS> kr(0), vr(0);
-      vr.next();
-      int scores[2] = {0, 0}, pieces[2] = {0, 0}, qn = 0;  // S products and pieces of each row tile, pieces of the run
-      auto put_s = [&](int x) {  // S = Q K(n)^T; its columns hold the last P until that product is done
-        if (scores[x] > 0) wait(&ms.pvdone[x], (scores[x] - 1) & 1, fail);
-        ++scores[x];
-        tc_after();
-        const uint64_t qd = desc(su32(sq + x * C::QTILE), 16, 1024, 2), kd = desc(su32(ring + kr.slot * C::SLOT), 16, 1024, 2);
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          mma4<2, 2>(taddr + x * 128, qd + k * (128 * 128 >> 4), kd + k * (kKeys * 128 >> 4), kIdescS, k > 0);
-        commit_to(&ms.sfull[x]);
-      };
-      auto begin = [&]() {  // the tile's keys are there, and the queries of its piece
-        if (w.j == w.jbeg) wait(&ms.qfull, qn++ & 1, fail);
-        wait(&ms.full[kr.slot], kr.phase, fail);
-      };
-      auto end = [&]() {
-        commit_to(&ms.empty[kr.slot]);
-        if (w.j + 1 == w.jend) commit_to(&ms.qfree);
-        kr.next();
-        kr.next();
-      };
-      begin();
-      put_s(0);
-      if (both()) put_s(1);
-      end();
-#pragma unroll 1
-      for (int n = 0; n < count; ++n) {
-        const bool first = w.j == w.jbeg, two = both(), more = n + 1 < count;
-        auto put_o = [&](int x) {  // O += P V(n)
-          wait(&ms.pfull[x], (scores[x] - 1) & 1, fail);
-          if (first && pieces[x]++ > 0) wait(&ms.ofree[x], (pieces[x] - 2) & 1, fail);
-          tc_after();
-          const uint64_t vd = desc(su32(ring + vr.slot * C::SLOT), kKeys * 128, 1024, 2);
-#pragma unroll
-          for (int k = 0; k < kKeys / 64; ++k)
-            mma4_ta(taddr + 256 + x * D, taddr + x * 128 + k * 32, vd + k * 512, kIdescO, !first || k > 0);
-          commit_to(&ms.pvdone[x]);
-        };
-        wait(&ms.full[vr.slot], vr.phase, fail);
-        put_o(0);
-        if (more) {
-          w.next(a, cap);
-          begin();
-          put_s(0);
-        }
-        if (two) put_o(1);
-        commit_to(&ms.empty[vr.slot]);
-        vr.next();
-        vr.next();
-        if (more) {
-          if (both()) put_s(1);
-          end();
-        }
-      }
-      commit_to(&ms.drain);
-      const unsigned long long t0 = now_ns();
-      for (uint32_t ok = 0; !ok && now_ns() - t0 < 2 * kWaitNs;)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(su32(&ms.drain))
-            : "memory");
-    } else if (warp == C::LOAD || warp == C::LOAD + 1) {
-      // -------------------------------------------------------- loads: keys and queries, values
-      const bool keys = warp == C::LOAD;
-      const KvView& kv = a.kv;
-      const int box_shift = min(kv.page_shift, 7), boxes = kKeys >> box_shift;  // keys in a box, boxes in a tile
-      const CUtensorMap* tm = keys ? &a.mk : &a.mv;
-      int* page = ms.page[keys ? 0 : 1];
-      Ring<E4M3 ? C::NRAW : C::NS> rg(1);
-      if (!keys) rg.next();
-      int qn = 0;
-#pragma unroll 1
-      for (int n = 0; n < count; ++n) {
-        if (keys && w.j == w.jbeg) {
-          if (qn > 0) wait(&ms.qfree, (qn - 1) & 1, fail);
-          ++qn;
-          if (lane == 0 && !*fail) {
-            const int tiles = both() ? 2 : 1;
-            expect(&ms.qfull, uint32_t(tiles * half * a.G * D * 2));
-            for (int x = 0; x < tiles; ++x)
-              for (int c = 0; c < D / 64; ++c)
-                load_rows(sq + x * C::QTILE + c * (128 * 128), &a.mq, c * 64, w.h * a.G, w.r.s0 + w.s.i0 + x * half,
-                          &ms.qfull);
-          }
-        }
-        const int key0 = (w.s.tile0 + w.j) * kKeys;
-        const int32_t* row = kv.page_table + (long long)w.b * kv.table_stride;
-        for (int x = lane; x < boxes; x += 32) {
-          const int key = key0 + (x << box_shift);
-          int id = -2;
-          if (key < w.s.hi && key + (1 << box_shift) > w.s.lo) id = row[key >> kv.page_shift];
-          const bool ok = id >= 0 && id < kv.npages;
-          if (!ok && id != -2) set_error(a.err, MOE_ERANGE);
-          page[x] = ok ? id : kv.npages;  // past the end: zeros
-        }
-        __syncwarp();
-        const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
-        uint64_t* full = (E4M3 ? ms.rfull : ms.full) + rg.slot;
-        wait((E4M3 ? ms.rempty : ms.empty) + rg.slot, rg.phase, fail);
-        if (!*fail) {
-          if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
-          __syncwarp();
-          constexpr int CHUNKS = E4M3 ? 1 : D / 64;
-#pragma unroll 1
-          for (int x = lane; x < boxes * CHUNKS; x += 32) {
-            const int p = x & (boxes - 1), c = x >> (7 - box_shift);
-            uint8_t* dst = E4M3 ? raw + rg.slot * C::RAW + (p << box_shift) * D
-                                : ring + rg.slot * C::SLOT + c * (kKeys * 128) + (p << box_shift) * 128;
-            load_box(dst, tm, c * 64, tok, w.h, page[p], full);
-          }
-        }
-        __syncwarp();
-        rg.next();
-        rg.next();
-        if (n + 1 < count) w.next(a, cap);
-      }
-    } else if (warp >= C::CONVERT) {
-      // -------------------------------------------------------- E4M3 codes -> bf16, in the ring's order
-      if constexpr (E4M3) {
-        const int vt = tid - 32 * C::CONVERT;
-        constexpr int CH = D / 8, STEP = 128 / CH;  // 8 codes a thread make one 16-byte piece
-        const int r0 = vt / CH, c = vt % CH;
-        Ring<C::NRAW> in(0);
-        Ring<C::NS> out(1);
-#pragma unroll 1
-        for (int n = 0; n < 2 * count; ++n) {
-          wait(&ms.rfull[in.slot], in.phase, fail);
-          wait(&ms.empty[out.slot], out.phase, fail);
-          const uint8_t* src = raw + in.slot * C::RAW + c * 8;
-          uint8_t* dst = ring + out.slot * C::SLOT + (c / 8) * (kKeys * 128);
-#pragma unroll 4
-          for (int i = 0; i < kKeys / STEP; ++i) {
-            const uint2 v = *reinterpret_cast<const uint2*>(src + (r0 + i * STEP) * D);
-            uint32_t o[4];
-            e4m3x4_to_bf16x4(v.x, o);
-            e4m3x4_to_bf16x4(v.y, o + 2);
-            *reinterpret_cast<uint4*>(dst + sw128(r0 + i * STEP, c % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          proxy_fence();
-          __syncwarp();
-          if (lane == 0) {
-            arrive(&ms.full[out.slot]);
-            arrive(&ms.rempty[in.slot]);
-          }
-          in.next();
-          out.next();
-        }
-      }
       }
     }
   }
