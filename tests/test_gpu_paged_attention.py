@@ -62,6 +62,11 @@ CASES = [
     ([9000], [1], 12, 1, 256, 64, 0, False, "hnd"),
     ([30000], [1], 10, 1, 256, 64, 0, True, "kv"),
     ([30011], [2], 12, 2, 64, 64, 0, False, "nhd"),
+    ([300, 131], [1, 3], 8, 2, 64, 2, 0, True, "hnd"),
+    ([300, 131], [50, 9], 16, 2, 64, 2, 0, True, "hnd"),
+    ([300, 131], [1, 4], 8, 2, 64, 8, 90, True, "nhd"),
+    ([257, 140], [2, 1], 8, 2, 128, 1, 0, True, "kv"),
+    ([257, 140], [70, 1], 8, 1, 128, 1, 33, True, "hnd"),
     ([7, 130, 12, 300, 1, 64, 90, 2] * 20, [1, 4, 2, 1, 1, 3, 1, 2] * 20, 8, 2, 64, 16, 0, False, "hnd"),
 ]
 
