@@ -621,19 +621,21 @@ def block_norm_desc(y=None, post_norm: bool = False, w_post=None, gate=None, gat
                          res_scale=res_scale, w_pre=w_pre, eps=eps)
 
 
+def _columns(t, T: int, H: int, size: int, what: str):
+    """Address and row stride of [T, H] rows with contiguous columns."""
+    if t.shape == (T, H) and t.element_size() == size:
+        row, col = t.stride()
+        if col == 1 or H == 1:
+            return t.data_ptr(), row
+    raise ValueError(f"{what}: {'fp32' if size == 4 else 'bf16'} [{T}, {H}], columns contiguous, got {list(t.shape)} {t.dtype} "
+                     f"strides {t.stride()}")
+
+
 def moe_block_norm(desc: BlockNormDesc, x, x_out, xn, T: int, H: int, stream=None) -> None:
     """x_out (fp32) = x + res_scale * gate * post-norm(y); xn (bf16) = pre-norm of the next block of x_out."""
-    rows = (T, H)
-    xp = xs = op = os_ = np_ = ns = None
-    ok = x.shape == rows and x.element_size() == 4 and desc.H in (None, H) and desc.T in (None, T)
-    if ok:
-        xp, xs = x.data_ptr(), x.stride(0)
-        if x_out is not None:
-            ok = x_out.shape == rows and x_out.element_size() == 4
-            op, os_ = x_out.data_ptr(), x_out.stride(0)
-        if xn is not None:
-            ok = ok and xn.shape == rows and xn.element_size() == 2
-            np_, ns = xn.data_ptr(), xn.stride(0)
-    if not ok:
-        raise ValueError(f"moe_block_norm: x, x_out fp32 and xn bf16 are [{T}, {H}], as are y, gate and the weights")
-    _check(load().moe_block_norm(desc.ref, xp, xs, op, os_ or 0, np_, ns or 0, T, H, _stream(stream)), "moe_block_norm")
+    if desc.H not in (None, H) or desc.T not in (None, T):
+        raise ValueError(f"moe_block_norm: y, gate and the weights are [{T}, {H}]")
+    xp, xs = _columns(x, T, H, 4, "x")
+    op, os_ = (None, 0) if x_out is None else _columns(x_out, T, H, 4, "x_out")
+    np_, ns = (None, 0) if xn is None else _columns(xn, T, H, 2, "xn")
+    _check(load().moe_block_norm(desc.ref, xp, xs, op, os_, np_, ns, T, H, _stream(stream)), "moe_block_norm")
