@@ -8,6 +8,7 @@ first call raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from typing import Optional
 
@@ -459,6 +460,13 @@ def moe_cache_apply_swaps(cache: Cache, plan_dev, n_dev, compute=None, copy=None
 
 # ------------------------------------------------- the attention half of a layer
 
+@functools.cache
+def _row_types():
+    """The types of a rows argument by its element size: fp32; bf16, or its bits as integers."""
+    import torch
+    return {4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16)}
+
+
 class KvPages:
     """A layer's key and value page pools: torch tensors [npages, Hkv, page, D], bf16 (or their
     bits as int16) or float8_e4m3fn with the scales of each head (fp32 [Hkv]); any strides with
@@ -554,7 +562,7 @@ class AttnWorkspace:
 
 def _heads(t, shape, what: str):
     """Address and token stride of [T, H, D] bf16 rows whose heads follow one another."""
-    if t.shape == shape and t.element_size() == 2:
+    if t.shape == shape and t.dtype in _row_types()[2]:
         tok, head, col = t.stride()
         if col == 1 and (head == shape[2] or shape[1] <= 1):
             return t.data_ptr(), tok
@@ -596,12 +604,12 @@ class BlockNormDesc:
 
     def __init__(self, **kw):
         self.tensors = kw
-        y, gate = kw["y"], kw["gate"]
+        y, gate, bf16 = kw["y"], kw["gate"], _row_types()[2]
         for t in (y, gate):
-            if t is not None and (t.dim() != 2 or t.element_size() != 2 or t.stride(1) != 1):
+            if t is not None and (t.dim() != 2 or t.dtype not in bf16 or t.stride(1) != 1):
                 raise ValueError("block_norm_desc: y is bf16 [T, H], gate bf16 [T, H] or [1, H], columns contiguous")
         for t in (kw["w_post"], kw["w_pre"]):
-            if t is not None and (t.dim() != 1 or t.element_size() != 2 or not t.is_contiguous()):
+            if t is not None and (t.dim() != 1 or t.dtype not in bf16 or not t.is_contiguous()):
                 raise ValueError("block_norm_desc: the weights are contiguous bf16 [H]")
         self.T = None if y is None else y.shape[0]
         widths = {t.shape[-1] for t in (y, gate, kw["w_post"], kw["w_pre"]) if t is not None}
@@ -623,7 +631,7 @@ def block_norm_desc(y=None, post_norm: bool = False, w_post=None, gate=None, gat
 
 def _columns(t, T: int, H: int, size: int, what: str):
     """Address and row stride of [T, H] rows with contiguous columns."""
-    if t.shape == (T, H) and t.element_size() == size:
+    if t.shape == (T, H) and t.dtype in _row_types()[size]:
         row, col = t.stride()
         if col == 1 or H == 1:
             return t.data_ptr(), row

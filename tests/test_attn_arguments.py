@@ -27,3 +27,49 @@ def test_norm_columns_are_contiguous(no_call):
     for rows in [(apart(x), x, y), (x, apart(x), y), (x, x, apart(y)), (torch.zeros(64, 3).t(), x, y)]:
         with pytest.raises(ValueError):
             moe.moe_block_norm(d, *rows, 3, 64)
+
+
+HALF = torch.float16
+
+
+def kv(pool=BF, T=3):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros(3, 2, 16, 64, dtype=pool)
+    return moe.KvPages(k, k.clone()), moe.KvBatch(i(3), i(2), i(2, 4), T, 2)
+
+
+@pytest.mark.parametrize("at", range(4))
+@pytest.mark.parametrize("dtype", [HALF, torch.float32])
+def test_append_takes_bf16_rows(no_call, at, dtype):
+    pages, batch = kv()
+    rows = [torch.zeros(3, 2, 64, dtype=BF) for _ in range(4)]
+    rows[at] = rows[at].to(dtype)
+    with pytest.raises(ValueError):
+        moe.moe_kv_append(pages, batch, None, *rows)
+
+
+class Workspace:
+    Hq, handle = 4, None
+
+
+@pytest.mark.parametrize("at", range(2))
+@pytest.mark.parametrize("dtype", [HALF, torch.float32])
+def test_attention_takes_bf16_rows(no_call, at, dtype):
+    pages, batch = kv()
+    rows = [torch.zeros(3, 4, 64, dtype=BF) for _ in range(2)]
+    rows[at] = rows[at].to(dtype)
+    with pytest.raises(ValueError):
+        moe.moe_paged_attention(pages, batch, *rows, Workspace(), 1.0)
+
+
+def test_norm_takes_fp32_and_bf16_rows(no_call):
+    x, y, w = torch.zeros(3, 64), torch.zeros(3, 64, dtype=BF), torch.zeros(64, dtype=BF)
+    for kw in [dict(y=y.half()), dict(y=y, gate=y.half()), dict(y=y, post_norm=True, w_post=w.half()),
+               dict(y=y, w_pre=w.half())]:
+        with pytest.raises(ValueError):
+            moe.block_norm_desc(**kw)
+    bits = [t.view(b) for t, b in ((y, torch.int16), (y, torch.uint16), (w, torch.int16))]
+    d = moe.block_norm_desc(y=bits[0], gate=bits[1], post_norm=True, w_post=w, w_pre=bits[2])
+    for rows in [(x.int(), x, y), (x, x.int(), y), (x, x, y.half())]:
+        with pytest.raises(ValueError):
+            moe.moe_block_norm(d, *rows, 3, 64)
