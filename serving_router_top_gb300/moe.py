@@ -467,6 +467,13 @@ def _row_types():
     return {4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16)}
 
 
+def _on_gpu(*tensors) -> bool:
+    return all(t is None or t.is_cuda for t in tensors)
+
+
+_ELSEWHERE = "the attention half's kernels read and write GPU tensors; an argument is on another device"
+
+
 class KvPages:
     """A layer's key and value page pools: torch tensors [npages, Hkv, page, D], bf16 (or their
     bits as int16) or float8_e4m3fn with the scales of each head (fp32 [Hkv]); any strides with
@@ -485,6 +492,7 @@ class KvPages:
         npages, self.Hkv, page, self.D = k.shape
         self.c = moe_kv_pages(k.data_ptr(), v.data_ptr(), 1 if k.dtype == torch.float8_e4m3fn else 0, self.Hkv, self.D,
                               page, npages, k.stride(0), k.stride(1), k.stride(2), _ptr(k_scale), _ptr(v_scale))
+        self.on_gpu = _on_gpu(k, v, k_scale, v_scale)
         self.ref = C.addressof(self.c)
 
 
@@ -504,6 +512,7 @@ class KvBatch:
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.c = moe_kv_batch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), B, T, max_n,
                               page_table.shape[1])
+        self.on_gpu = _on_gpu(q_start, kv_len, page_table)
         self.ref = C.addressof(self.c)
 
 
@@ -581,6 +590,9 @@ def moe_kv_append(pages: KvPages, batch: KvBatch, rope: Optional[Rope], q, q_out
         op, os_ = _heads(q_out, (T, Hq, D), "q_out")
     kp, ks = _heads(k, kv, "k")
     vp, vs = _heads(v, kv, "v")
+    if not (pages.on_gpu and batch.on_gpu and k.is_cuda and v.is_cuda and (q is None or q.is_cuda and q_out.is_cuda)
+            and (err is None or isinstance(err, int) or err.is_cuda)):
+        raise ValueError(_ELSEWHERE)
     _check(load().moe_kv_append(pages.ref, batch.ref, None if rope is None else rope.handle, qp, qs, op, os_, Hq, kp, ks,
                                 vp, vs, _ptr(err), _stream(stream)), "moe_kv_append")
 
@@ -591,6 +603,8 @@ def moe_paged_attention(pages: KvPages, batch: KvBatch, q, o, ws: AttnWorkspace,
     rows = (batch.c.T, ws.Hq, pages.D)
     qp, qs = _heads(q, rows, "q")
     op, os_ = _heads(o, rows, "o")
+    if not (pages.on_gpu and batch.on_gpu and q.is_cuda and o.is_cuda):
+        raise ValueError(_ELSEWHERE)
     _check(load().moe_paged_attention(pages.ref, batch.ref, qp, qs, ws.Hq, op, os_, scale, window, ws.handle,
                                       _stream(stream)), "moe_paged_attention")
 
@@ -620,6 +634,7 @@ class BlockNormDesc:
             _ptr(y), 0 if y is None else y.stride(0), 1 if kw["post_norm"] else 0, _ptr(kw["w_post"]), _ptr(gate),
             0 if gate is None or gate.shape[0] == 1 else gate.stride(0), 1 if kw["gate_sigmoid"] else 0,
             kw["res_scale"], _ptr(kw["w_pre"]), kw["eps"])
+        self.on_gpu = _on_gpu(y, gate, kw["w_post"], kw["w_pre"])
         self.ref = C.addressof(self.c)
 
 
@@ -646,4 +661,6 @@ def moe_block_norm(desc: BlockNormDesc, x, x_out, xn, T: int, H: int, stream=Non
     xp, xs = _columns(x, T, H, 4, "x")
     op, os_ = (None, 0) if x_out is None else _columns(x_out, T, H, 4, "x_out")
     np_, ns = (None, 0) if xn is None else _columns(xn, T, H, 2, "xn")
+    if not (desc.on_gpu and x.is_cuda and (x_out is None or x_out.is_cuda) and (xn is None or xn.is_cuda)):
+        raise ValueError(_ELSEWHERE)
     _check(load().moe_block_norm(desc.ref, xp, xs, op, os_, np_, ns, T, H, _stream(stream)), "moe_block_norm")

@@ -25,7 +25,7 @@ def test_norm_columns_are_contiguous(no_call):
     x, y = torch.zeros(3, 64), torch.zeros(3, 64, dtype=BF)
     d = moe.block_norm_desc(y=y)
     for rows in [(apart(x), x, y), (x, apart(x), y), (x, x, apart(y)), (torch.zeros(64, 3).t(), x, y)]:
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="got"):
             moe.moe_block_norm(d, *rows, 3, 64)
 
 
@@ -44,7 +44,7 @@ def test_append_takes_bf16_rows(no_call, at, dtype):
     pages, batch = kv()
     rows = [torch.zeros(3, 2, 64, dtype=BF) for _ in range(4)]
     rows[at] = rows[at].to(dtype)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="got"):
         moe.moe_kv_append(pages, batch, None, *rows)
 
 
@@ -58,7 +58,7 @@ def test_attention_takes_bf16_rows(no_call, at, dtype):
     pages, batch = kv()
     rows = [torch.zeros(3, 4, 64, dtype=BF) for _ in range(2)]
     rows[at] = rows[at].to(dtype)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="got"):
         moe.moe_paged_attention(pages, batch, *rows, Workspace(), 1.0)
 
 
@@ -71,5 +71,18 @@ def test_norm_takes_fp32_and_bf16_rows(no_call):
     bits = [t.view(b) for t, b in ((y, torch.int16), (y, torch.uint16), (w, torch.int16))]
     d = moe.block_norm_desc(y=bits[0], gate=bits[1], post_norm=True, w_post=w, w_pre=bits[2])
     for rows in [(x.int(), x, y), (x, x.int(), y), (x, x, y.half())]:
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="got"):
             moe.moe_block_norm(d, *rows, 3, 64)
+
+
+def test_tensors_of_the_host_are_refused(no_call):
+    pages, batch = kv()
+    q = torch.zeros(3, 4, 64, dtype=BF)
+    k = torch.zeros(3, 2, 64, dtype=BF)
+    x, y = torch.zeros(3, 64), torch.zeros(3, 64, dtype=BF)
+    for call in (lambda: moe.moe_kv_append(pages, batch, None, q, q, k, k),
+                 lambda: moe.moe_kv_append(pages, batch, None, None, None, k, k),
+                 lambda: moe.moe_paged_attention(pages, batch, q, q, Workspace(), 1.0),
+                 lambda: moe.moe_block_norm(moe.block_norm_desc(y=y), x, x, y, 3, 64)):
+        with pytest.raises(ValueError, match="another device"):
+            call()
