@@ -19,7 +19,7 @@ runs a prompt and decode windows of a small model and prints the times.
 from __future__ import annotations
 
 import dataclasses
-from typing import List, Sequence
+from typing import Dict, List, Sequence
 
 import torch
 
@@ -70,12 +70,21 @@ class Pages:
 
     def reserve(self, request: int, length: int) -> None:
         """Pages for `length` tokens of a request."""
-        need = -(-length // self.page)
-        if need > self.table.shape[1] or need - self.held[request] > len(self.free):
-            raise RuntimeError(f"no pages for {length} tokens of request {request}")
-        for j in range(self.held[request], need):
-            self.table[request, j] = self.free.pop()
-        self.held[request] = max(self.held[request], need)
+        self.reserve_all({request: length})
+
+    def reserve_all(self, lengths: Dict[int, int]) -> None:
+        """Pages for that many tokens of each request, or none for any of them."""
+        left = len(self.free)
+        for request, length in lengths.items():
+            need = -(-length // self.page)
+            left -= max(need - self.held[request], 0)
+            if need > self.table.shape[1] or left < 0:
+                raise RuntimeError(f"no pages for {length} tokens of request {request}")
+        for request, length in lengths.items():
+            need = -(-length // self.page)
+            for j in range(self.held[request], need):
+                self.table[request, j] = self.free.pop()
+            self.held[request] = max(self.held[request], need)
 
     def upload(self) -> None:
         self.device.copy_(self.table)
@@ -102,10 +111,13 @@ class Decoder:
         self.lens = [0] * requests
 
     def batch(self, new: Sequence[int]) -> moe.KvBatch:
-        """The next call's requests: new[r] tokens of request r (pages are reserved for them)."""
-        for r, n in enumerate(new):
-            self.lens[r] += n
-            self.pages.reserve(r, self.lens[r])
+        """The next call's requests: new[r] tokens of request r (pages are reserved for them).  A call
+        that raises leaves lengths and pages as they were."""
+        if len(new) != len(self.lens) or min(new) < 0 or sum(new) > self.maxT:
+            raise ValueError(f"new tokens of {len(self.lens)} requests, at most {self.maxT} in all, got {list(new)}")
+        lens = [have + n for have, n in zip(self.lens, new)]
+        self.pages.reserve_all(dict(enumerate(lens)))
+        self.lens = lens
         self.pages.upload()
         start = torch.tensor([0] + list(new), dtype=torch.int32).cumsum(0).to(torch.int32)
         return moe.KvBatch(start.cuda(), torch.tensor(self.lens, dtype=torch.int32).cuda(), self.pages.device,
