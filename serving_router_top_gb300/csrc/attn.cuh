@@ -1035,8 +1035,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
               if (tid < NR) {
                 const float old = first ? kUnset : ms.m[tid];
                 const float v = fmaxf(fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid])), old);
-                ms.m[tid] = v;
-                ms.alpha[tid] = ex2(old - v);
+                // Rows past the unit's own are another request's, or what shared memory held: their weights are
+                // nothing, whatever they score, so they never ask for a new m of the rows beside them.
+                const bool own = tid < (w.s.i1 - w.s.i0 + 1) * a.G;
+                ms.m[tid] = own ? v : INFINITY;
+                ms.alpha[tid] = own ? ex2(old - v) : 1.f;
               }
               softmax_sync<kSoft>();
               if (!first) {
