@@ -179,19 +179,25 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None  # device index -> the handle of its current stream
+_raw_stream = _device = None  # device index -> the handle of its current stream; the current device
+
+
+def _find_stream() -> None:
+    global _raw_stream, _device
+    import torch
+    torch.cuda.current_device()  # sets CUDA up
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    # torch.cuda.current_stream() builds a Stream object, 3 us a call on a Grace core
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return stream.cuda_stream or None
-    global _raw_stream
-    import torch
     if _raw_stream is None:
-        # torch.cuda.current_stream() builds a Stream object, 3 us a call on a Grace core
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return _raw_stream(torch.cuda.current_device()) or None
+        _find_stream()
+    return _raw_stream(_device()) or None
 
 
 class _CudaArray:
@@ -462,9 +468,9 @@ def moe_cache_apply_swaps(cache: Cache, plan_dev, n_dev, compute=None, copy=None
 
 @functools.cache
 def _row_types():
-    """The types of a rows argument by its element size: fp32; bf16, or its bits as integers."""
+    """The types of row arguments: fp32; bf16, or its bits as integers."""
     import torch
-    return {4: (torch.float32,), 2: (torch.bfloat16, torch.int16, torch.uint16)}
+    return (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16)
 
 
 def _on_gpu(*tensors) -> bool:
@@ -571,7 +577,7 @@ class AttnWorkspace:
 
 def _heads(t, shape, what: str):
     """Address and token stride of [T, H, D] bf16 rows whose heads follow one another."""
-    if t.shape == shape and t.dtype in _row_types()[2]:
+    if t.shape == shape and t.dtype in _row_types()[1]:
         tok, head, col = t.stride()
         if col == 1 and (head == shape[2] or shape[1] <= 1):
             return t.data_ptr(), tok
@@ -618,7 +624,7 @@ class BlockNormDesc:
 
     def __init__(self, **kw):
         self.tensors = kw
-        y, gate, bf16 = kw["y"], kw["gate"], _row_types()[2]
+        y, gate, bf16 = kw["y"], kw["gate"], _row_types()[1]
         for t in (y, gate):
             if t is not None and (t.dim() != 2 or t.dtype not in bf16 or t.stride(1) != 1):
                 raise ValueError("block_norm_desc: y is bf16 [T, H], gate bf16 [T, H] or [1, H], columns contiguous")
@@ -644,23 +650,25 @@ def block_norm_desc(y=None, post_norm: bool = False, w_post=None, gate=None, gat
                          res_scale=res_scale, w_pre=w_pre, eps=eps)
 
 
-def _columns(t, T: int, H: int, size: int, what: str):
+def _columns(t, rows, types, what: str):
     """Address and row stride of [T, H] rows with contiguous columns."""
-    if t.shape == (T, H) and t.dtype in _row_types()[size]:
+    if t.shape == rows and t.dtype in types:
         row, col = t.stride()
-        if col == 1 or H == 1:
+        if col == 1 or rows[1] == 1:
             return t.data_ptr(), row
-    raise ValueError(f"{what}: {'fp32' if size == 4 else 'bf16'} [{T}, {H}], columns contiguous, got {list(t.shape)} {t.dtype} "
-                     f"strides {t.stride()}")
+    raise ValueError(f"{what}: {types[0]} {list(rows)}, columns contiguous, got {list(t.shape)} {t.dtype} strides {t.stride()}")
 
 
 def moe_block_norm(desc: BlockNormDesc, x, x_out, xn, T: int, H: int, stream=None) -> None:
     """x_out (fp32) = x + res_scale * gate * post-norm(y); xn (bf16) = pre-norm of the next block of x_out."""
     if desc.H not in (None, H) or desc.T not in (None, T):
         raise ValueError(f"moe_block_norm: y, gate and the weights are [{T}, {H}]")
-    xp, xs = _columns(x, T, H, 4, "x")
-    op, os_ = (None, 0) if x_out is None else _columns(x_out, T, H, 4, "x_out")
-    np_, ns = (None, 0) if xn is None else _columns(xn, T, H, 2, "xn")
+    rows = (T, H)
+    fp32, bf16 = _row_types()
+    xp, xs = _columns(x, rows, fp32, "x")
+    # in place: looked at already
+    op, os_ = (xp, xs) if x_out is x else (None, 0) if x_out is None else _columns(x_out, rows, fp32, "x_out")
+    np_, ns = (None, 0) if xn is None else _columns(xn, rows, bf16, "xn")
     if not (desc.on_gpu and x.is_cuda and (x_out is None or x_out.is_cuda) and (xn is None or xn.is_cuda)):
         raise ValueError(_ELSEWHERE)
     _check(load().moe_block_norm(desc.ref, xp, xs, op, os_, np_, ns, T, H, _stream(stream)), "moe_block_norm")
