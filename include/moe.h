@@ -574,7 +574,8 @@ int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
  * g = Hq / Hkv, token at position p, query head h reads key head h / g:
  *   s_j = scale * q . k_j over the keys j <= p (and j > p - window if window > 0),
  *   o = sum_j exp(s_j) v_j / sum_j exp(s_j).
- * A token that sees no key (p < 0) gets zeros.  What lies in the pages outside
+ * A token that sees no key (p < 0) gets zeros, as does a row whose scores are
+ * all -infinity.  What lies in the pages outside
  * a request's kv_len keys is never used, whatever it holds, and pages wholly
  * before every window of a call need no valid table entry.
  *   q, o  bf16 [T][Hq][D]; strides between tokens as in moe_kv_append; o must not

@@ -62,7 +62,7 @@ namespace moe {
 namespace attn {
 
 constexpr int kKeys = 128;                    // keys in a tile
-constexpr float kUnset = -1e30f;              // m of a row that has seen no key
+constexpr float kUnset = -3.402823466e38f;    // m of a row that has seen no key: no finite score is below it
 constexpr float kMost = 256.0f;               // m is set again when a weight passes this
 constexpr float kLost = 0x1p-100f;            // sums from before m grew by this factor are nothing to those after
 constexpr unsigned long long kWaitNs = 1000000000ull;
