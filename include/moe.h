@@ -575,9 +575,10 @@ int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
  *   s_j = scale * q . k_j over the keys j <= p (and j > p - window if window > 0),
  *   o = sum_j exp(s_j) v_j / sum_j exp(s_j).
  * A token that sees no key (p < 0) gets zeros, as does a row whose scores are
- * all -infinity.  What lies in the pages outside
- * a request's kv_len keys is never used, whatever it holds, and pages wholly
- * before every window of a call need no valid table entry.
+ * all -infinity.  Scores are of a size below 2^30: fp32 has steps of 64 there,
+ * and a row past it may come out as zeros or NaN.  What lies in the pages
+ * outside a request's kv_len keys is never used, whatever it holds, and pages
+ * wholly before every window of a call need no valid table entry.
  *   q, o  bf16 [T][Hq][D]; strides between tokens as in moe_kv_append; o must not
  *         overlap q.
  * Scores, softmax sums and outputs accumulate in fp32; the weights exp(s - m)
