@@ -32,8 +32,8 @@ namespace chunk {
 constexpr float kGrow = 8.0f;  // log2
 // In tiles that every row sees whole, a score less m is one multiply-add: the part of the product below m's last
 // bit stays in it.  In the other tiles, whose hidden scores are -infinity, the product is rounded first.  The two
-// forms of a score differ by half of its last bit, and from this size on (base 2, 2^-5) only the second is used.
-constexpr float kWide = 0x1p20f;
+// forms of a score differ by half of its last bit, and from this size on (base 2, 2^-11) only the second is used.
+constexpr float kWide = 0x1p14f;
 __device__ __forceinline__ bool is_wide(float m) { return fabsf(m) >= kWide && m > kUnset; }
 
 struct Misc {

@@ -14,7 +14,7 @@ def _gpu():
     require_gpu()
 
 
-@pytest.mark.parametrize("size", [s * 2.0 ** e for s in (1, -1) for e in (-30, 12, 21, 24, 26, 28)])
+@pytest.mark.parametrize("size", [s * 2.0 ** e for s in (1, -1) for e in (-30, 12, 15, 17, 18, 19, 21, 24, 26, 28)])
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("G,n,L,window", [(4, 1, 300, 0), (4, 1, 9000, 0), (8, 4, 700, 0), (8, 3, 700, 150), (8, 20, 900, 0),
