@@ -535,8 +535,8 @@ typedef struct moe_attn_ws moe_attn_ws; /* scratch of the attention calls, error
  * (i, i + rot/2), or (2i, 2i + 1) when interleaved, turned by the angle
  * p * f_i: (u, w) -> (u cos - w sin, w cos + u sin).  f_i = inv_freq_host[i]
  * (double [rot/2], finite) or, with NULL, theta^(-2i/rot).  The angle is kept
- * as a 64-bit fixed-point fraction of a turn: exact to 2^-33 turn at every
- * 32-bit position.  rot a multiple of 16 in [16, 256]; theta > 0 and finite.
+ * as a 64-bit fixed-point fraction of a turn: that of the double f_i, of a size
+ * below 2^64, to 2^-33 turn at every 32-bit position.  rot a multiple of 16 in [16, 256]; theta > 0 and finite.
  * Synchronous (allocates the table). */
 int moe_rope_create(moe_rope** out, int rot, int interleaved, double theta, const double* inv_freq_host);
 int moe_rope_destroy(moe_rope* r);

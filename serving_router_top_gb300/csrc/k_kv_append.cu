@@ -6,8 +6,8 @@
 // p * f_i in fp32 is off by p * 2^-24 (0.06 rad at a million tokens), and fp64
 // runs at a small fraction of the fp32 rate here.  So f_i is kept as a 64-bit
 // fixed-point fraction of a turn: p times it, modulo 2^64, is the angle's
-// fraction of a turn with an error of at most p * 2^-65 (plus the 53 bits of
-// the given f_i), and only its top bits become a float, for sincospif.
+// fraction of a turn with an error of at most p * 2^-65, and only its top bits
+// become a float, for sincospif.
 #include <limits.h>
 #include <math.h>
 
@@ -212,6 +212,30 @@ cudaError_t launch(int D, int T, cudaStream_t s, const Args& a) {
   }
 }
 
+// f / 2 pi, whole turns off, as a 64-bit fraction to nearest.  In integers: divided in a double it is off by 2^-53 of
+// itself, 2^-25 of a turn at position 2^31 for f = 1.  192 bits of 1 / 2 pi are enough for any |f| below 2^64.
+uint64_t turns_of(double f) {
+  constexpr uint64_t kInv[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};  // 2^192 / (2 pi), low word first
+  int ex = 0;
+  const uint64_t m = uint64_t(ldexp(frexp(fabs(f), &ex), 53));  // |f| = m 2^(ex - 53)
+  uint64_t w[5] = {};  // m 2^192 / (2 pi)
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < 3; ++i) {
+    carry += (unsigned __int128)m * kInv[i];
+    w[i] = uint64_t(carry);
+    carry >>= 64;
+  }
+  w[3] = uint64_t(carry);
+  const int low = 128 - (ex - 53);  // its bits from `low` on are the fraction
+  auto bits = [&](int at) {         // 64 bits from bit `at` on
+    const int i = at / 64, s = at % 64;
+    return i > 3 ? 0 : s ? w[i] >> s | w[i + 1] << (64 - s) : w[i];
+  };
+  if (m == 0 || low < 1) return 0;
+  const uint64_t frac = bits(low) + (bits(low - 1) & 1);
+  return f < 0 ? 0 - frac : frac;
+}
+
 }  // namespace append
 }  // namespace moe
 
@@ -224,11 +248,7 @@ extern "C" int moe_rope_create(moe_rope** out, int rot, int interleaved, double 
   for (int i = 0; i < rot / 2; ++i) {
     const double f = inv_freq_host ? inv_freq_host[i] : pow(theta, -2.0 * i / rot);
     if (!isfinite(f)) return MOE_EINVAL;
-    // the fraction of a turn in [0, 1): whole turns do nothing at whole positions
-    const double turn = f / 6.283185307179586476925286766559;
-    const double frac = turn - floor(turn);
-    const double scaled = ldexp(frac, 64);
-    turns[i] = scaled >= 18446744073709551616.0 ? 0 : uint64_t(scaled);
+    turns[i] = append::turns_of(f);
   }
   moe_rope* r = static_cast<moe_rope*>(calloc(1, sizeof(moe_rope)));
   if (!r) return MOE_ENOMEM;
