@@ -103,10 +103,12 @@ extern "C" int moe_attn_ws_get_view(const moe_attn_ws* w, moe_attn_ws_view* v) {
 
 extern "C" int moe_attn_sync_status(moe_attn_ws* w, moe_stream_t stream) {
   if (!w) return MOE_EINVAL;
-  MOE_CUDA_TRY(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+  // all on the caller's stream: a reset elsewhere could run after the stream's next call has recorded its error
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int32_t e = 0;
-  MOE_CUDA_TRY(cudaMemcpy(&e, w->error, 4, cudaMemcpyDeviceToHost));
-  MOE_CUDA_TRY(cudaMemset(w->error, 0, 4));
+  MOE_CUDA_TRY(cudaMemcpyAsync(&e, w->error, 4, cudaMemcpyDeviceToHost, s));
+  MOE_CUDA_TRY(cudaMemsetAsync(w->error, 0, 4, s));
+  MOE_CUDA_TRY(cudaStreamSynchronize(s));
   return e;
 }
 
