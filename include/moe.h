@@ -547,8 +547,8 @@ int moe_rope_destroy(moe_rope* r);
  * of 8, at least heads * D (not checked for T <= 1); all pointers 16-byte
  * aligned.  q may be NULL (Hq 0), rope NULL (nothing
  * turns).  Rotation in fp32, one rounding to the stored type: bf16 to nearest
- * even; E4M3(x * (1 / scale)), the product in fp32, to nearest even, saturating
- * at 448, NaN kept.
+ * even; E4M3(x / scale), the quotient rounded in fp32, to nearest even,
+ * saturating at 448, NaN kept.
  * A position outside [0, page * table_stride), or a page id outside
  * [0, npages), records MOE_ERANGE in err_dev (int32[1], may be NULL) and
  * nothing is stored for that token.  Two tokens must not share a place.

@@ -76,12 +76,11 @@ __device__ __forceinline__ void store8(const Args& a, int t, int head, int col, 
   if (!E4M3) {
     *reinterpret_cast<uint4*>(dst + 2 * col) = pack8(f);
   } else {
-    // Times the scale's reciprocal: off by 2^-23 of the quotient before a rounding to 2^-4 of it.  A division
-    // for each column took 19.9 us instead of 17.1 for 4096 tokens of 32 + 2 x 4 heads of 128.
-    const float r = 1.0f / scale;
+    // A division for each column, as the code is that of x / scale: times the scale's reciprocal, ties and the
+    // smallest scales go elsewhere.  4096 tokens of 32 + 2 x 4 heads of 128 take 17.9 us, with the reciprocal 16.6.
     uint2 u;
-    u.x = e4m3x2(f[0] * r, f[1] * r) | (e4m3x2(f[2] * r, f[3] * r) << 16);
-    u.y = e4m3x2(f[4] * r, f[5] * r) | (e4m3x2(f[6] * r, f[7] * r) << 16);
+    u.x = e4m3x2(f[0] / scale, f[1] / scale) | (e4m3x2(f[2] / scale, f[3] / scale) << 16);
+    u.y = e4m3x2(f[4] / scale, f[5] / scale) | (e4m3x2(f[6] / scale, f[7] / scale) << 16);
     *reinterpret_cast<uint2*>(dst + col) = u;
   }
 }
