@@ -1116,7 +1116,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
               const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
                                  (long long)(k & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
               float add = 0.f;
-              if (col < D) {
+              // pages that are not there read as zeros, also where a wait gave up and the slot holds something else
+              if (col < D && id >= 0 && id < a.kv.npages) {
                 if (E4M3) add = f16x2_to_f32x2(e4m3x2_to_f16x2(v[col])).x;
                 else add = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[col]);
               }

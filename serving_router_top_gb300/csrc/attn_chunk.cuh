@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     ms.fail = 0;
+    for (int i = 0; i < 4; ++i) ms.nbad[i] = 0;
   }
   pdl_wait();
   constexpr int V = C::V;
@@ -340,7 +341,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
 #pragma unroll 1
         for (int e = 0; e < nbad; ++e) {
           const int key = spoiled_key0 + ms.bad[spoiled & 3][e];
+          if (key >= w.s.hi) continue;  // only where a wait gave up: a place of the list not written yet
           const int id = a.kv.page_table[(long long)w.b * a.kv.table_stride + (key >> a.kv.page_shift)];
+          if (id < 0 || id >= a.kv.npages) continue;  // the same: the slot of a page that reads as zeros
           const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
                              (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
           const bool sees = key <= pos && (a.window <= 0 || key > pos - a.window);
