@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           const int slot = !E4M3 ? rg.slot : keys ? kr.slot : rr.slot;
           uint64_t* full = (!E4M3 ? ms.full : keys ? ms.kfull : ms.rfull) + slot;
           wait((!E4M3 ? ms.empty : keys ? ms.kempty : ms.rempty) + slot, !E4M3 ? rg.phase : keys ? kr.phase : rr.phase, fail);
-          if (*fail) break;
+          if (__any_sync(0xffffffffu, *fail)) break;  // for the warp: its lanes meet below
           if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
           __syncwarp();
           constexpr int CHUNKS = E4M3 ? 1 : C::DS / 64;

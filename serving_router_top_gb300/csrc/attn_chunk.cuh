@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
         const int tok = key0 & ((1 << kv.page_shift) - 1);  // of a page larger than a tile
         uint64_t* full = (E4M3 ? ms.rfull : ms.full) + rg.slot;
         wait((E4M3 ? ms.rempty : ms.empty) + rg.slot, rg.phase, fail);
-        if (!*fail) {
+        if (!__any_sync(0xffffffffu, *fail)) {  // for the warp: its lanes meet inside
           if (lane == 0) expect(full, E4M3 ? C::RAW : C::SLOT);
           __syncwarp();
           constexpr int CHUNKS = E4M3 ? 1 : D / 64;
