@@ -65,7 +65,7 @@ constexpr int kKeys = 128;                    // keys in a tile
 constexpr float kUnset = -3.402823466e38f;    // m of a row that has seen no key: no finite score is below it
 constexpr float kMost = 256.0f;               // m is set again when a weight passes this
 constexpr float kLost = 0x1p-100f;            // sums from before m grew by this factor are nothing to those after
-constexpr unsigned long long kWaitNs = 1000000000ull;
+constexpr unsigned long long kWaitNs = 1000000000ull, kLandNs = 2000000ull;
 constexpr int kSmem = 232448;                 // shared memory of one CTA on an SM, and of each of two
 constexpr int kSmem2 = 115712;
 constexpr int misc_bytes(int nr) { return (2192 + 60 * nr + 127) / 128 * 128; }  // barriers, row statistics, schedule
@@ -266,6 +266,13 @@ __device__ __forceinline__ void wait(uint64_t* b, uint32_t par, volatile int* fa
     if (*fail) return;
     if (i == 15) t0 = now_ns();
     else if (now_ns() - t0 > kWaitNs) *fail = 1;
+  }
+}
+// What a CTA does last when a wait gave up.  Tiles that nobody took may be on their way: nothing more is asked for
+// once the flag is up, so after this time, a thousand times a copy's, they have landed and the shared memory can go.
+__device__ __forceinline__ void give_up(int32_t* err) {
+  set_error(err, MOE_ETIMEOUT);
+  for (const unsigned long long t0 = now_ns(); now_ns() - t0 < kLandNs;) {
   }
 }
 // A box of 64 columns (or a slot's codes) of a page from its place `tok` on -> dst, counted on b.
@@ -1214,7 +1221,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
     }
   }
   __syncthreads();
-  if (tid == 0 && *fail) set_error(a.err, MOE_ETIMEOUT);
+  if (tid == 0 && *fail) give_up(a.err);
   if (warp == kMmaWarp) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(C::COLS));

@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
     }
   }
   __syncthreads();
-  if (tid == 0 && *fail) set_error(a.err, MOE_ETIMEOUT);
+  if (tid == 0 && *fail) give_up(a.err);
   if (warp == C::MMA) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(512));
