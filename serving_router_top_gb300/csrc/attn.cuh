@@ -588,11 +588,12 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr int kMmaWarp = C::SW, kLoadWarp = C::SW + 1, kSoft = 32 * C::SW;  // loads: keys, then values
 
-  pdl_trigger();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ms.taddr)),
                  "n"(C::COLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    // not before: a kernel further on that takes tensor memory too could hold what this one waits for
+    pdl_trigger();
   } else if (tid == 32 * kLoadWarp) {
     for (int i = 0; i < C::NS; ++i) {
       bar_init(&ms.full[i], E4M3 ? C::CV : 1);

@@ -121,10 +121,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
   volatile int* fail = &ms.fail;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  pdl_trigger();
   if (warp == C::MMA) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&ms.taddr)), "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    // not before: a kernel further on that takes tensor memory too could hold what this one waits for
+    pdl_trigger();
   } else if (tid == 32 * C::LOAD) {
     for (int i = 0; i < C::NS; ++i) {
       bar_init(&ms.full[i], E4M3 ? 4 : 1);
