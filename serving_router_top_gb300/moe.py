@@ -575,9 +575,9 @@ class AttnWorkspace:
         return self.view.error
 
 
-def _heads(t, shape, what: str):
+def _heads(t, shape, types, what: str):
     """Address and token stride of [T, H, D] bf16 rows whose heads follow one another."""
-    if t.shape == shape and t.dtype in _row_types()[1]:
+    if t.dtype in types and t.shape == shape:
         tok, head, col = t.stride()
         if col == 1 and (head == shape[2] or shape[1] <= 1):
             return t.data_ptr(), tok
@@ -587,28 +587,34 @@ def _heads(t, shape, what: str):
 
 def moe_kv_append(pages: KvPages, batch: KvBatch, rope: Optional[Rope], q, q_out, k, v, err=None, stream=None) -> None:
     """Rotate q into q_out and the keys by position; write keys and values into their pages."""
-    T, D = batch.c.T, pages.D
+    T, D, bf16 = batch.c.T, pages.D, _row_types()[1]
     kv = (T, pages.Hkv, D)
+    kp, ks = _heads(k, kv, bf16, "k")
+    vp, vs = _heads(v, kv, bf16, "v")
+    on_gpu = pages.on_gpu and batch.on_gpu and k.is_cuda and v.is_cuda
     Hq, qp, qs, op, os_ = 0, None, 0, None, 0
     if q is not None:
         Hq = q.shape[1]
-        qp, qs = _heads(q, (T, Hq, D), "q")
-        op, os_ = _heads(q_out, (T, Hq, D), "q_out")
-    kp, ks = _heads(k, kv, "k")
-    vp, vs = _heads(v, kv, "v")
-    if not (pages.on_gpu and batch.on_gpu and k.is_cuda and v.is_cuda and (q is None or q.is_cuda and q_out.is_cuda)
-            and (err is None or isinstance(err, int) or err.is_cuda)):
+        rows = (T, Hq, D)
+        qp, qs = _heads(q, rows, bf16, "q")
+        # in place: looked at already
+        op, os_ = (qp, qs) if q_out is q else _heads(q_out, rows, bf16, "q_out")
+        on_gpu = on_gpu and q.is_cuda and q_out.is_cuda
+    if err is not None and not isinstance(err, int):
+        on_gpu = on_gpu and err.is_cuda
+        err = err.data_ptr()
+    if not on_gpu:
         raise ValueError(_ELSEWHERE)
     _check(load().moe_kv_append(pages.ref, batch.ref, None if rope is None else rope.handle, qp, qs, op, os_, Hq, kp, ks,
-                                vp, vs, _ptr(err), _stream(stream)), "moe_kv_append")
+                                vp, vs, err, _stream(stream)), "moe_kv_append")
 
 
 def moe_paged_attention(pages: KvPages, batch: KvBatch, q, o, ws: AttnWorkspace, scale: float, window: int = 0,
                         stream=None) -> None:
     """o (bf16 [T, Hq, D]) = attention of every new token over its request's pages."""
-    rows = (batch.c.T, ws.Hq, pages.D)
-    qp, qs = _heads(q, rows, "q")
-    op, os_ = _heads(o, rows, "o")
+    rows, bf16 = (batch.c.T, ws.Hq, pages.D), _row_types()[1]
+    qp, qs = _heads(q, rows, bf16, "q")
+    op, os_ = _heads(o, rows, bf16, "o")
     if not (pages.on_gpu and batch.on_gpu and q.is_cuda and o.is_cuda):
         raise ValueError(_ELSEWHERE)
     _check(load().moe_paged_attention(pages.ref, batch.ref, qp, qs, ws.Hq, op, os_, scale, window, ws.handle,
