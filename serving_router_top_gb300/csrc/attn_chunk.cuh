@@ -30,11 +30,6 @@ namespace attn {
 namespace chunk {
 
 constexpr float kGrow = 8.0f;  // log2
-// In tiles that every row sees whole, a score less m is one multiply-add: the part of the product below m's last
-// bit stays in it.  In the other tiles, whose hidden scores are -infinity, the product is rounded first.  The two
-// forms of a score differ by half of its last bit, and from this size on (base 2, 2^-11) only the second is used.
-constexpr float kWide = 0x1p14f;
-__device__ __forceinline__ bool is_wide(float m) { return fabsf(m) >= kWide && m > kUnset; }
 
 struct Misc {
   uint64_t full[8], empty[8], rfull[8], rempty[8], qfull, qfree, sfull[2], pfull[2], pvdone[2], ofree[2], drain;
@@ -386,20 +381,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
           ld_wait();
           float f = factor;
           if (!whole || factor <= 0.f) {
+            // Hidden scores stay -infinity where the factor is positive.  It is multiplied in with m, in one
+            // multiply-add as in whole tiles: the product's part below m's last bit, which that keeps, is then the
+            // same in all of a row's weights.  With factors that are not, every tile takes the product first.
+            const float once = factor > 0.f ? 1.f : factor;
+            f = factor > 0.f ? factor : 1.f;
             const int from = a.window > 0 ? pos - a.window + 1 - key0 : INT_MIN, to_key = min(pos + 1, cap) - key0;
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] = i < from || i >= to_key ? -INFINITY : s[i] * factor;
-            f = 1.f;
+            for (int i = 0; i < kKeys; ++i) s[i] = i < from || i >= to_key ? -INFINITY : s[i] * once;
           }
           float top = -INFINITY, top1 = -INFINITY;  // the row's largest score
 #pragma unroll
           for (int i = 0; i < kKeys; i += 2) top = fmaxf(top, s[i]), top1 = fmaxf(top1, s[i + 1]);
           top = fmaxf(top, top1) * f;
-          if (f != 1.f && __any_sync(0xffffffffu, is_wide(top))) {
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] *= f;
-            f = 1.f;
-          }
           const bool grow = top > m + kGrow;  // true for the first that a row sees: m is unset
           if (__any_sync(0xffffffffu, grow)) {
             const float old = m;
