@@ -585,7 +585,8 @@ int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
  * are rounded to 16 bits for the product with v; over E4M3 pools a column of q
  * below 2^-14 of its row's largest is rounded to 2^-22 of that.  A key in a page whose id is
  * outside [0, npages) reads as zeros and records MOE_ERANGE in the workspace's
- * error word; so does kv_len beyond page * table_stride or 2^29, cut there.
+ * error word; so does kv_len beyond page * table_stride or 2^29, whose keys end
+ * there, and q_start that decreases, with which nothing is computed.
  * max_n only picks the kernel.  The result does not vary between runs.  scale
  * finite; window >= 0, 0 for none.  Calls with (T + B) * Hkv * (page *
  * table_stride / 128 + 4) < 2^31 are taken; larger ones may be MOE_EINVAL.

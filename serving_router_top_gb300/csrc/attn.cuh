@@ -133,7 +133,7 @@ __device__ __forceinline__ Req load_req(const KvView& kv, int b) {
   const int s0 = kv.q_start[b], s1 = kv.q_start[b + 1];
   r.kv = max(kv.kv_len[b], 0);
   r.s0 = min(max(s0, 0), kv.T);
-  r.n = min(max(s1, r.s0), kv.T) - r.s0;
+  r.n = min(s1, kv.T) - r.s0;  // below zero where the starts decrease
   r.pos0 = r.kv - r.n;
   return r;
 }
@@ -431,12 +431,14 @@ __device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.kv.B, per = (B + THREADS - 1) / THREADS;
   int2 mine = make_int2(0, 0);  // places and tiles of this thread's requests
+  bool falls = false;           // q_start decreases: the requests could then have more rows than the count has room for
   Req r = {};
   Load ld = {};  // the last of them
   for (int i = 0; i < per; ++i) {
     const int b = tid * per + i;
     if (b < B) {
       r = load_req(a.kv, b);
+      falls |= r.n < 0;
       if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
       ld = head_load(r, a.tokens, a.window, cap);
       mine.x += a.kv.Hkv * (ld.tiles + V * ld.units);
@@ -452,22 +454,25 @@ __device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh)
       before.y += y1;
     }
   }
-  if (lane == 31) sh.scan[warp] = before;
+  falls = __any_sync(0xffffffffu, falls);
+  if (lane == 31) sh.scan[warp] = falls ? make_int2(INT_MIN, 0) : before;
   before.x -= mine.x;
   before.y -= mine.y;
   tc_before();
   __syncthreads();
   tc_after();
   const int2 sum = lane < THREADS / 32 ? sh.scan[lane] : make_int2(0, 0);
+  falls = __any_sync(0xffffffffu, sum.x == INT_MIN);
+  if (falls && blockIdx.x == 0 && tid == 0) set_error(a.err, MOE_ERANGE);
   before.x += __reduce_add_sync(0xffffffffu, lane < warp ? sum.x : 0);
   before.y += __reduce_add_sync(0xffffffffu, lane < warp ? sum.y : 0);
   Plan p;
   const int run = blockIdx.x;
-  p.total = __reduce_add_sync(0xffffffffu, sum.x);
+  p.total = falls ? 0 : __reduce_add_sync(0xffffffffu, sum.x);
   p.runs = min(int(gridDim.x), p.total);
   p.x0 = run < p.runs ? cut_at(p.total, p.runs, run) : p.total;
   p.x1 = run < p.runs ? cut_at(p.total, p.runs, run + 1) : p.total;
-  if (mine.x > 0) {  // a cut falls into the requests of one thread
+  if (mine.x > 0 && !falls) {  // a cut falls into the requests of one thread
 #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
       int x = (e ? p.x1 : p.x0) - before.x, t = before.y, b = tid * per;

@@ -37,3 +37,19 @@ def test_status_of_a_stream_beside_a_busy_default_stream():
             assert moe.moe_attn_sync_status(ws) == moe.MOE_OK
     assert not busy.query()  # the default stream is still at work: neither the copy nor the reset went through it
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("G,n", [(2, 4), (8, 40)])
+def test_request_starts_that_decrease_are_reported(G, n):
+    """Nothing is computed: the schedule's count holds rows of requests that follow one another."""
+    P = Paged([100, 90, 80], [n, n, n], 1, 64, 16)
+    pages, bt = P.device()
+    q = strided_rows(P.T, G, 64, 0, torch.Generator().manual_seed(0)).contiguous().cuda()
+    ws, o = moe.AttnWorkspace(G, 1, 64), torch.full((P.T, G, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    start = torch.tensor([0, 2 * n, n, 3 * n], dtype=torch.int32).cuda()
+    moe.moe_paged_attention(pages, moe.KvBatch(start, bt.kv_len, bt.page_table, P.T, n), q, o, ws, 0.125)
+    assert moe.moe_attn_sync_status(ws) == moe.MOE_ERANGE
+    assert (o == 9).all()
+    moe.moe_paged_attention(pages, bt, q, o, ws, 0.125)
+    assert moe.moe_attn_sync_status(ws) == moe.MOE_OK
+    assert (o != 9).any(2).all()
