@@ -500,7 +500,8 @@ int moe_cache_apply_lru(moe_cache* c, const moe_swap* plan_dev, const int32_t* n
  * at position p = kv_len[b] - n_b + i.  Position p lives in page
  * page_table[b * table_stride + p / page], place p % page.  n_b = 0 is allowed;
  * q_start is non-decreasing with q_start[0] >= 0 and q_start[B] <= T; rows
- * outside [q_start[0], q_start[B]) are neither read nor written. */
+ * outside [q_start[0], q_start[B]) may be read, change no result and are not
+ * written. */
 
 /* The page pools of one layer's keys and values (device memory of the caller).
  * Element (page, head, place, column) is at page * page_stride + head *
@@ -524,7 +525,8 @@ typedef struct {
   const int32_t* kv_len;     /* int32 [B] device                                           */
   const int32_t* page_table; /* int32 [B][table_stride] device                             */
   int B, T;                  /* requests; token rows                                       */
-  int max_n;                 /* about the largest n_b: picks a tile size, never the result */
+  int max_n;                 /* about the largest n_b: picks the kernel and its tiles, and with
+                                them the order of sums: a result's last bits, no more   */
   int table_stride;          /* entries of a row: a request holds at most page times this  */
 } moe_kv_batch;
 
@@ -587,7 +589,8 @@ int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
  * outside [0, npages) reads as zeros and records MOE_ERANGE in the workspace's
  * error word; so does kv_len beyond page * table_stride or 2^29, whose keys end
  * there, and q_start that decreases, with which nothing is computed.
- * max_n only picks the kernel.  The result does not vary between runs.  scale
+ * max_n picks the kernel, whatever the requests hold.  The same arguments give the
+ * same bits in every run; the rows of one request reach no other's.  scale
  * finite; window >= 0, 0 for none.  Calls with (T + B) * Hkv * (page *
  * table_stride / 128 + 4) < 2^31 are taken; larger ones may be MOE_EINVAL.
  * Asynchronous on `stream`; one stream drives a workspace at a time. */

@@ -32,8 +32,8 @@
 // the largest, thousands of which can be half the sum.  With keys converted too,
 // the conversions' traffic through shared memory and their turns in the ring took
 // longer than the memory: one token of 32 requests of 4096 keys, 128 columns, 63.1
-// us with both converted, 51.4 us now; 64 columns 53.6 and 45.1; 16 windows of four
-// up to 32768 keys, 256 columns, 50.7 and 48.2.
+// us with both converted, 51.9 us now; 64 columns 53.6 and 46.5; 16 windows of four
+// up to 32768 keys, 256 columns, 50.7 and 48.6.
 //
 // Movement.  Two warps, one for keys and one for values, ask the copy engine for
 // the tiles (a page, or 128 keys of a larger one, by 64 columns a box, swizzled for
@@ -41,7 +41,7 @@
 // read as zeros.  E4M3 values land as they are and are turned into bf16 by warps of
 // their own, which also write the queries' terms.
 //
-// What bounds it: memory.  One token over 131071 keys (268 MB) 47.0 us, 5.7 TB/s with
+// What bounds it: memory.  One token over 131071 keys (268 MB) 47.5 us, 5.7 TB/s with
 // the join; 32 requests of 4096 keys 84 us, 6.4 TB/s, 95% of what a copy reaches.
 // Short units add a softmax's chain at each end, about three tiles' time.
 //
@@ -117,8 +117,9 @@ struct Cfg {
   // What a unit costs beside its tiles, in tiles.  64 requests of 3 to 8192 tokens with 128 columns (64 KB
   // of keys and values a tile): 1, 2, 3 and 4 give 50.1, 44.9, 46.4 and 48.9 us; 48 with 64 columns (32 KB)
   // and a window of 1000: 33.5, 27.8, 25.9 and 26.8 us (at one run an SM).  E4M3, whose ends cost more beside
-  // tiles of half the bytes: 16 windows over up to 32768 keys of 256 columns (64 KB) 50.5 us with 2, 48.0
-  // with 3, 49.3 with 4.
+  // tiles of half the bytes, with 2, 3 and 4: 64 requests of 3 to 8192 tokens, 64 columns (16 KB) 44.2, 40.1
+  // and 39.2 us, 128 columns 45.6, 41.4 and 40.8, 256 columns 36.9, 35.3 and 37.6; 16 windows of four over up
+  // to 32768 keys 26.5, 24.6 and 24.0, 29.4, 27.0 and 26.2, 42.7, 39.8 and 39.0.  3 is within 3% of the best.
   static constexpr int V = !E4M3 && SLOT * H * 2 >= 65536 ? 2 : 3;
   static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
 };

@@ -16,10 +16,10 @@
 //
 // What bounds it: that chain, S, weights, O, of two row tiles in turn, 3000 clocks for 256 rows by 128
 // keys of 128 columns, with the tensor pipe busy 47% of the time.  Two chunks of up to 512 tokens of 32
-// heads over up to 6000 keys: 72.7 us with the join, 964 TFLOP/s; with 64 columns 64 us.
+// heads over up to 6000 keys: 73.1 us with the join, 959 TFLOP/s; with 64 columns 63 us.
 //
 // E4M3: four warps turn the tiles into bf16, exactly, in the ring's order.  A tile serves 256 rows here, so
-// that is hidden but for 0.3 of a tile's time: the same chunks 83.8 us, 65.9 with 64 columns (attn.cuh's form at
+// that is hidden but for 0.3 of a tile's time: the same chunks 83.7 us, 67.0 with 64 columns (attn.cuh's form at
 // 64 rows 166.7 and 129.3).
 #pragma once
 
