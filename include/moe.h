@@ -572,6 +572,15 @@ int moe_attn_ws_get_view(const moe_attn_ws* ws, moe_attn_ws_view* out);
 /* Synchronise `stream`, return the workspace's device error word and reset it. */
 int moe_attn_sync_status(moe_attn_ws* ws, moe_stream_t stream);
 
+/* Fault-injection hook for tests of the attention kernels' bounded waits: with
+ * stage 1 (the queries of a piece), 2 (the weights of a tile) or 3 (the slots of
+ * keys and values) that stage's barriers wait for one arrival more, which never
+ * comes.  Its waits give up after a second, MOE_ETIMEOUT is recorded in the
+ * workspace's error word, the call's outputs are undefined (nothing else is
+ * written) and the context stays usable.  Stage 0 restores normal operation; another
+ * is MOE_EINVAL.  Host-side setting, no stream work. */
+int moe_attn_ws_set_wait_test(moe_attn_ws* ws, int stage);
+
 /* Attention of every new token over its request's pages.  With group
  * g = Hq / Hkv, token at position p, query head h reads key head h / g:
  *   s_j = scale * q . k_j over the keys j <= p (and j > p - window if window > 0),

@@ -78,6 +78,7 @@ struct Args {
   long long qs, os;
   int G, window, tokens;   // query heads a key head; visible keys (0: all); tokens in a row tile
   float scale;
+  int phantom;  // a test of the waits: 1 the queries', 2 the weights', 3 the slots' barriers want an arrival that never comes
   int32_t* err;
   float* part;  // [2 * runs][NR][D] pieces: head piece of run c at 2c, tail piece at 2c + 1
   float* ml;    // [2 * runs][NR][2] their m and sums
@@ -603,22 +604,22 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
   } else if (tid == 32 * kLoadWarp) {
     for (int i = 0; i < C::NS; ++i) {
       bar_init(&ms.full[i], E4M3 ? C::CV : 1);
-      bar_init(&ms.empty[i], 1);
+      bar_init(&ms.empty[i], 1 + (a.phantom == 3));
     }
     for (int i = 0; i < C::NK; ++i) {
       bar_init(&ms.kfull[i], 1);
-      bar_init(&ms.kempty[i], 1);
+      bar_init(&ms.kempty[i], 1 + (a.phantom == 3));
     }
     for (int i = 0; i < C::NRAW; ++i) {
       bar_init(&ms.rfull[i], 1);
       bar_init(&ms.rempty[i], C::CV);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&ms.qfull[i], E4M3 ? C::CV : 1);
+      bar_init(&ms.qfull[i], (E4M3 ? C::CV : 1) + (a.phantom == 1));
       bar_init(&ms.qfree[i], 1);
       bar_init(&ms.factors[i], 1);
       bar_init(&ms.sfull[i], 1);
-      bar_init(&ms.pfull[i], C::SW);
+      bar_init(&ms.pfull[i], C::SW + (a.phantom == 2));
       bar_init(&ms.pvdone[i], 1);
       bar_init(&ms.ofree[i], C::SW);
     }

@@ -124,17 +124,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
   } else if (tid == 32 * C::LOAD) {
     for (int i = 0; i < C::NS; ++i) {
       bar_init(&ms.full[i], E4M3 ? 4 : 1);
-      bar_init(&ms.empty[i], 1);
+      bar_init(&ms.empty[i], 1 + (a.phantom == 3));
     }
     for (int i = 0; i < C::NRAW; ++i) {
       bar_init(&ms.rfull[i], 1);
       bar_init(&ms.rempty[i], 4);
     }
-    bar_init(&ms.qfull, 1);
+    bar_init(&ms.qfull, 1 + (a.phantom == 1));
     bar_init(&ms.qfree, 1);
     for (int i = 0; i < 2; ++i) {
       bar_init(&ms.sfull[i], 1);
-      bar_init(&ms.pfull[i], 4);
+      bar_init(&ms.pfull[i], 4 + (a.phantom == 2));
       bar_init(&ms.pvdone[i], 1);
       bar_init(&ms.ofree[i], 4);
     }

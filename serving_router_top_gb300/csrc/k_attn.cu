@@ -4,7 +4,7 @@
 #include "attn.cuh"
 
 struct moe_attn_ws {
-  int Hq, Hkv, D, sms;
+  int Hq, Hkv, D, sms, phantom;
   int32_t* error;
   float *part, *ml;
   int4* join;
@@ -101,6 +101,12 @@ extern "C" int moe_attn_ws_get_view(const moe_attn_ws* w, moe_attn_ws_view* v) {
   return MOE_OK;
 }
 
+extern "C" int moe_attn_ws_set_wait_test(moe_attn_ws* w, int stage) {
+  if (!w || stage < 0 || stage > 3) return MOE_EINVAL;
+  w->phantom = stage;
+  return MOE_OK;
+}
+
 extern "C" int moe_attn_sync_status(moe_attn_ws* w, moe_stream_t stream) {
   if (!w) return MOE_EINVAL;
   // all on the caller's stream: a reset elsewhere could run after the stream's next call has recorded its error
@@ -155,6 +161,7 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
       !attn::encode(&a.mq, const_cast<uint16_t*>(q), 0, 3, qdims, qpitches, qbox, CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_EINVAL;
   a.scale = scale;
+  a.phantom = ws->phantom;
   a.err = ws->error;
   a.part = ws->part;
   a.ml = ws->ml;

@@ -32,7 +32,7 @@ EXPORTED = (
     "moe_ws_set_fused_heat", "cache_lru_plan", "moe_cache_apply_lru", "moe_ws_set_decode_path",
     "moe_ws_set_wait_test", "moe_nvfp4_split", "moe_layers_forward_streamed", "moe_rope_create", "moe_rope_destroy",
     "moe_kv_append", "moe_attn_ws_create", "moe_attn_ws_destroy", "moe_attn_ws_get_view", "moe_attn_sync_status",
-    "moe_paged_attention", "moe_block_norm",
+    "moe_paged_attention", "moe_block_norm", "moe_attn_ws_set_wait_test",
 )
 
 
@@ -148,6 +148,7 @@ def load() -> C.CDLL:
         "moe_attn_ws_destroy": (I, [P]),
         "moe_attn_ws_get_view": (I, [P, C.POINTER(moe_attn_ws_view)]),
         "moe_attn_sync_status": (I, [P, P]),
+        "moe_attn_ws_set_wait_test": (I, [P, I]),
         "moe_paged_attention": (I, [P, P, P, Q, I, P, Q, F, I, P, P]),
         "moe_block_norm": (I, [P, P, Q, P, Q, P, Q, I, I, P]),
     }
@@ -573,6 +574,10 @@ class AttnWorkspace:
     @property
     def error_ptr(self) -> int:
         return self.view.error
+
+    def set_wait_test(self, stage: int) -> None:
+        """Fault-injection hook for tests of the bounded waits (see include/moe.h)."""
+        _check(load().moe_attn_ws_set_wait_test(self.handle, int(stage)), "moe_attn_ws_set_wait_test")
 
 
 def _heads(t, shape, types, what: str):

@@ -86,3 +86,9 @@ def test_tensors_of_the_host_are_refused(no_call):
                  lambda: moe.moe_block_norm(moe.block_norm_desc(y=y), x, x, y, 3, 64)):
         with pytest.raises(ValueError, match="another device"):
             call()
+
+
+def test_wait_test_stages():
+    from serving_router_top_gb300 import build
+    build.build()
+    assert moe.load().moe_attn_ws_set_wait_test(None, 0) == moe.MOE_EINVAL
