@@ -607,6 +607,117 @@ int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const uin
                         uint16_t* o, long long o_stride, float scale, int window, moe_attn_ws* ws,
                         moe_stream_t stream);
 
+/* --------------------------------------------- a step of drafted token trees
+ * Drafted tokens may branch: a request's new tokens are the nodes of a tree.
+ * Node i is the request's i-th new row and follows its parent; node 0 is the
+ * request's last token, whose successors were drafted.  The step: append and
+ * attention of the nodes in every layer, moe_verify_drafts on the target's
+ * probabilities, moe_kv_compact on the nodes it kept.  With base = kv_len - n,
+ * node i lies in place base + i of the cache and is at position base + depth_i. */
+typedef struct {
+  const int32_t* parent; /* int32 [T] device: the parent's index among its request's nodes,
+                            below the node's own; -1 for a root (depth 0)                */
+  int32_t* depth;        /* int32 [T] device                                             */
+  uint32_t* above;       /* uint32 [T][words] device: bit j of row i: node j is node i or above it */
+  uint32_t* below;       /* uint32 [T][words] device: bit j of row i: node j is node i or below it */
+  int words;             /* 1..8; a request has at most 32 * words nodes                 */
+} moe_tree;
+
+/* Fills depth, above and below from parent, once for all layers of a step.  A parent
+ * that is not below its node's index is taken as -1; so are all nodes of a request
+ * past 32 * words, whose masks are empty; both record MOE_ERANGE in err_dev
+ * (int32[1], may be NULL).  Rows outside [q_start[0], q_start[B]) are left as they
+ * are.  Asynchronous on `stream`. */
+int moe_tree_prepare(const moe_kv_batch* b, const moe_tree* tree, int32_t* err_dev, moe_stream_t stream);
+
+/* Norms of each head's query and key rows: w * x / sqrt(mean(x^2) + eps) over D columns. */
+typedef struct {
+  const uint16_t* w_q; /* bf16 [D] or NULL: ones; 16-byte aligned */
+  const uint16_t* w_k;
+  float eps;           /* > 0 and finite                          */
+} moe_head_norm;
+
+/* moe_kv_append with the heads of queries and keys normalised first (norm NULL:
+ * not), and at a tree's positions (tree NULL: a request's tokens follow one
+ * another; only tree->depth is read).  Norm and rotation in fp32, one rounding
+ * to the stored type.  Everything else as in moe_kv_append. */
+int moe_kv_append_norm(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const moe_rope* rope,
+                       const moe_head_norm* norm, const uint16_t* q, long long q_stride, uint16_t* q_out,
+                       long long q_out_stride, int Hq, const uint16_t* k, long long k_stride, const uint16_t* v,
+                       long long v_stride, int32_t* err_dev, moe_stream_t stream);
+
+/* moe_paged_attention of tree nodes: node i sees the keys of its request before
+ * the tree (places below base), itself and the nodes above it, as tree->above and
+ * tree->below say; with a window > 0, of those the ones at a position above its
+ * own less the window.  What other nodes' places hold takes no part.  The masks
+ * are moe_tree_prepare's for the same batch, each the other's transpose; with
+ * others a row may see what either of them says.  Everything else as in
+ * moe_paged_attention. */
+int moe_tree_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const uint16_t* q,
+                       long long q_stride, int Hq, uint16_t* o, long long o_stride, float scale, int window,
+                       moe_attn_ws* ws, moe_stream_t stream);
+
+/* What the target's probabilities keep of drafted trees, and the next token.  From
+ * node 0 on, at node v with R = the target's row of v and s = 1, its children c in
+ * the order of their indices, x their token:
+ *   drafted by chance (draft given):  c is kept if u_c * s * q(x) < R(x), q the draft's
+ *     row of v; else R = max(R - s * q, 0), s = sum R;
+ *   picked (draft NULL):              c is kept if u_c * s < R(x); else s = s - R(x), R(x) = 0;
+ * the walk goes on at a kept child.  Where none is kept, the request's next token is
+ * the first j with sum_{i <= j} R(i) > u_last * sum R; where sum R is 0, of the
+ * target's own row; -1 where that has none.  With u uniform and children drawn from
+ * q independently of one another (or picked before u is known), kept tokens and next
+ * token are distributed as the target's.
+ * Rows are probabilities: an entry below 0 or NaN counts as 0, one above 1 as 1; sums
+ * above 4 count as 4.  Sums are kept in fixed point, 2^-60 a unit: no order of sums
+ * changes a result.  A u below 0 or NaN counts as 0, from 1 on as the largest below 1. */
+typedef struct {
+  const float* target;    /* fp32 [T][V] device, one row a node                           */
+  long long target_stride; /* elements between rows, at least V (not checked for T <= 1)  */
+  const float* draft;     /* fp32 [T][V] device: row v is what v's children were drawn from; or NULL */
+  long long draft_stride;
+  const int32_t* token;   /* int32 [T] device: the drafted tokens; node 0's is not used. One
+                             outside [0, V) is never kept                                 */
+  const int32_t* parent;  /* int32 [T] device, as in moe_tree; a node that node 0 is not above is
+                             never reached, nor one whose parent is not below its own index */
+  const float* u;         /* fp32 [T] device: a random number a node; node 0's is not used */
+  const float* u_last;    /* fp32 [B] device                                              */
+  int V;                  /* 1 .. 2^24                                                    */
+} moe_verify_desc;
+
+/* path int32 [B][path_stride]: the kept nodes in their order, node 0 first, then -1; at
+ * most path_stride of them (the walk ends there as at a node without children).
+ * count int32 [B]: how many; 0 for a request without nodes.  token int32 [B]: the
+ * next token, -1 for a request without nodes.  Of b, q_start, B, T and max_n are used.
+ * Nodes past 256 of a request are never reached and record MOE_ERANGE in err_dev
+ * (int32[1], may be NULL), as does q_start that decreases.  path_stride >= 1, fp32
+ * arrays 4-byte aligned.  Asynchronous on `stream`. */
+int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d, int32_t* path, int path_stride, int32_t* count,
+                      int32_t* token, int32_t* err_dev, moe_stream_t stream);
+
+/* The kept nodes' keys and values to the front of their tree, in the pools of L
+ * layers (kv [L] host, of one geometry: all but the pointers and scales are the
+ * same): place base + path[b][d] goes to place base + d for d < count[b].  path
+ * int32 [B][path_stride] and count int32 [B] device, as moe_verify_drafts writes
+ * them: indices rise and are below n_b, else MOE_ERANGE is recorded in err_dev
+ * (int32[1], may be NULL) and the request's path ends before the first that does
+ * not; count is cut to path_stride.  A place past the table or in a page outside
+ * [0, npages) also records MOE_ERANGE and is neither read nor written.
+ * kv_len_out int32 [B] device or NULL: base + the kept nodes, the request's
+ * tokens from here on; not b->kv_len itself.  Two requests must not share a page
+ * of their trees.  L <= 4096.  Asynchronous on `stream`. */
+int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch* b, const int32_t* path, int path_stride,
+                   const int32_t* count, int32_t* kv_len_out, int32_t* err_dev, moe_stream_t stream);
+
+/* Pages copied in the pools of L layers (kv as above): the first tokens[i] places of
+ * page src[i], all where tokens is NULL, to page dst[i], i < n (int32 [n] device,
+ * n <= 2^20).  A page may be a source several times; one that is a destination is
+ * neither one again nor a source.  An id outside [0, npages) records MOE_ERANGE in
+ * err_dev (int32[1], may be NULL) and nothing is copied for it; tokens outside
+ * [0, page] count as the nearest.  Asynchronous on `stream`. */
+int moe_kv_copy_pages(const moe_kv_pages* kv, int L, const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                      int n, int32_t* err_dev, moe_stream_t stream);
+
 /* The norms around a block, its gate and its residual add in one pass:
  *   z  = post_norm ? w_post * y / sqrt(mean(y^2) + eps) : y
  *   x_out = x + res_scale * g * z,   g = gate, sigmoid(gate) or 1

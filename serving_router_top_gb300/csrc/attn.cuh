@@ -83,6 +83,9 @@ struct Args {
   float* part;  // [2 * runs][NR][D] pieces: head piece of run c at 2c, tail piece at 2c + 1
   float* ml;    // [2 * runs][NR][2] their m and sums
   int4* join;   // [runs] where run c's first piece is the second of a unit: token, key head, rows, pieces (else 0)
+  const uint32_t *above, *below;  // trees: masks of the nodes above and below each, rows of `words`
+  const int32_t* depth;
+  int words;
 };
 
 template <int D, int NR, bool E4M3>
@@ -142,12 +145,14 @@ __device__ __forceinline__ Req load_req(const KvView& kv, int b) {
 struct Span {  // the keys that a row tile's tokens i0 .. i1 see between them: [lo, hi), in nt tiles from tile0
   int i0, i1, lo, hi, tile0, nt;
 };
+// TREE: a node's position is below that of a chain's token in its place, but not before the tree's first.
+template <bool TREE>
 __device__ __forceinline__ Span span_of(const Req& r, int rt, int tokens, int window, int cap) {
   Span s;
   s.i0 = rt * tokens;
   s.i1 = min(s.i0 + tokens, r.n) - 1;
   s.hi = min(max(r.pos0 + s.i1 + 1, 0), cap);
-  s.lo = window > 0 ? min(max(r.pos0 + s.i0 - window + 1, 0), s.hi) : 0;
+  s.lo = window > 0 ? min(max(r.pos0 + (TREE ? 0 : s.i0) - window + 1, 0), s.hi) : 0;
   s.tile0 = s.lo / kKeys;
   s.nt = max((s.hi + kKeys - 1) / kKeys - s.tile0, 1);  // a tile even where nothing is seen: its rows get zeros
   return s;
@@ -162,9 +167,10 @@ __host__ __device__ inline int cap_of(const KvView& kv) {
 struct Load {
   int tiles, units;
 };
+template <bool TREE>
 __device__ __forceinline__ Load head_load(const Req& r, int tokens, int window, int cap) {
   Load w = {0, 0};
-  for (; w.units * tokens < r.n; ++w.units) w.tiles += span_of(r, w.units, tokens, window, cap).nt;
+  for (; w.units * tokens < r.n; ++w.units) w.tiles += span_of<TREE>(r, w.units, tokens, window, cap).nt;
   return w;
 }
 // First place of run c: `total` places in `runs` runs whose lengths differ by one at most.
@@ -178,14 +184,14 @@ __device__ __forceinline__ int run_of(int total, int runs, int x) {
 }
 
 // A walk over the tiles of a run: the same in every role.  A unit takes V places before its tiles.
-template <int V>
+template <int V, bool TREE>
 struct Walk {
   Req r;
   Span s;
   int b, h, rt, j, jbeg, jend;
   int rest;  // places of the run after this unit
   __device__ __forceinline__ void unit(const Args& a, int cap, int off, int places) {
-    s = span_of(r, rt, a.tokens, a.window, cap);
+    s = span_of<TREE>(r, rt, a.tokens, a.window, cap);
     jbeg = j = max(off - V, 0);
     jend = min(max(off + places - V, 0), s.nt);
     rest = off + places - (s.nt + V);
@@ -215,13 +221,13 @@ struct Walk {
   }
 };
 // Place x of a request: its key head, row tile and place in their unit, and the request's tiles before it.
-template <int V>
+template <int V, bool TREE>
 __device__ __forceinline__ int find_place(const Args& a, const Req& r, const Load& per, int cap, int x, int4* unit) {
   const int cost = per.tiles + V * per.units, h = x / cost;
   int t = h * per.tiles, rt = 0;
   x -= h * cost;
   for (;; ++rt) {
-    const int nt = span_of(r, rt, a.tokens, a.window, cap).nt;
+    const int nt = span_of<TREE>(r, rt, a.tokens, a.window, cap).nt;
     if (x < nt + V) break;
     x -= nt + V;
     t += nt;
@@ -428,7 +434,7 @@ struct Plan {
 };
 // The run: all units of the call, end to end, cut into equal parts.  Called by every thread of the CTA;
 // its two barriers also end the CTA's set-up.
-template <int V, int THREADS>
+template <int V, int THREADS, bool TREE>
 __device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.kv.B, per = (B + THREADS - 1) / THREADS;
@@ -442,7 +448,7 @@ __device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh)
       r = load_req(a.kv, b);
       falls |= r.n < 0;
       if (blockIdx.x == 0 && r.n > 0 && r.kv > cap) set_error(a.err, MOE_ERANGE);
-      ld = head_load(r, a.tokens, a.window, cap);
+      ld = head_load<TREE>(r, a.tokens, a.window, cap);
       mine.x += a.kv.Hkv * (ld.tiles + V * ld.units);
       mine.y += a.kv.Hkv * ld.tiles;
     }
@@ -481,14 +487,14 @@ __device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh)
       if (x < 0 || x >= mine.x) continue;
       for (; per > 1; ++b) {
         r = load_req(a.kv, b);
-        ld = head_load(r, a.tokens, a.window, cap);
+        ld = head_load<TREE>(r, a.tokens, a.window, cap);
         const int c = a.kv.Hkv * (ld.tiles + V * ld.units);
         if (x < c) break;
         x -= c;
         t += a.kv.Hkv * ld.tiles;
       }
       int4 unit = make_int4(b, 0, 0, 0);
-      sh.tiles[e] = t + find_place<V>(a, r, ld, cap, x, &unit);
+      sh.tiles[e] = t + find_place<V, TREE>(a, r, ld, cap, x, &unit);
       if (e == 0) sh.first = unit;
     }
   }
@@ -498,8 +504,8 @@ __device__ __forceinline__ Plan plan_run(const Args& a, int cap, PlanShared& sh)
   return p;
 }
 // What the join needs of the unit that a run's first piece, begun at tile jbeg, is the second piece of.
-template <int V>
-__device__ __forceinline__ int4 join_record(const Args& a, const Plan& p, const Walk<V>& w) {
+template <int V, bool TREE>
+__device__ __forceinline__ int4 join_record(const Args& a, const Plan& p, const Walk<V, TREE>& w) {
   // the unit's tiles take the places from `at` on; its first piece is the run's that has place `at`
   const int run = blockIdx.x, at = p.x0 - w.jbeg;
   if (w.jbeg == 0 || cut_at(p.total, p.runs, run - 1) > at) return make_int4(0, 0, 0, 0);
@@ -547,6 +553,20 @@ __device__ __forceinline__ void drop_not_finite(uint8_t* slot, int key) {
   }
 }
 
+// ------------------------------------------------------------------ trees
+// Of the 32 nodes from 32 w on: bits of a node's row of a mask.  Before the first are keys that every node sees.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int words, int w) {
+  return w < 0 ? 0xffffffffu : w < words ? row[w] : 0u;
+}
+// Whether node i of a request sees a key.
+__device__ __forceinline__ bool tree_sees(const Args& a, const Req& r, int i, int key) {
+  const int node = key - r.pos0;
+  if (node >= r.n) return false;
+  if (!(mask_word(a.above + (long long)(r.s0 + i) * a.words, a.words, node >> 5) >> (node & 31) & 1)) return false;
+  if (a.window <= 0) return true;
+  return (node < 0 ? node : a.depth[r.s0 + node]) > a.depth[r.s0 + i] - a.window;
+}
+
 // A place in a ring of N slots.
 template <int N>
 struct Ring {
@@ -579,7 +599,7 @@ __device__ __forceinline__ float transpose_sum(float (&v)[W], int lane) {
   }
 }
 
-template <int D, int NR, bool E4M3>
+template <int D, int NR, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::OCC) k_attn(const __grid_constant__ Args a) {
   using C = Cfg<D, NR, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -634,13 +654,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
 
   constexpr int V = C::V;
   const int cap = cap_of(a.kv);
-  const Plan plan = plan_run<V, C::THREADS>(a, cap, ms.plan);
+  const Plan plan = plan_run<V, C::THREADS, TREE>(a, cap, ms.plan);
   const uint32_t taddr = ms.taddr;
   const int run = blockIdx.x, count = plan.count;
   if (count == 0 && tid == 0) a.join[run] = make_int4(0, 0, 0, 0);
 
   if (count > 0) {
-    Walk<V> w;
+    Walk<V, TREE> w;
     w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- tensor cores
@@ -820,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
         Ring<C::NS> out(1);
         int qn = -1;
         // The rows of a piece as two terms, a warp a row, and the factors of their scores.
-        auto queries = [&](const Walk<V>& k) {
+        auto queries = [&](const Walk<V, TREE>& k) {
           ++qn;
           if (qn >= C::QB) wait(&ms.qfree[qn % C::QB], (qn / C::QB - 1) & 1, fail);
           // eight columns a thread: L threads a row, `AT` rows at a time
@@ -918,7 +938,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
       int piece = -1, d_token = 0, d_head = 0, d_rows = 0, d_part = -1;
       bool pending = false;
       int newest = 0, oldest = 0, whole0 = 0, whole1 = 0;
-      if (tid == 0) a.join[run] = join_record<V>(a, plan, w);
+      if (tid == 0) a.join[run] = join_record(a, plan, w);
       // Rows x0 .. x0 + CK - 1 of tile n (p = n & 1): scores in log2 units, less m where asked.
       auto scores = [&](int p, int x0, float* s, bool less_m) {
 #pragma unroll
@@ -1013,14 +1033,45 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
             if (E4M3) wait(&ms.factors[piece & 1], (piece >> 1) & 1, fail);
             // the row tile's tokens; the tiles of which every row sees every key
             newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
-            whole1 = max(min(oldest + 1, cap), 0) / kKeys - w.s.tile0;
+            whole1 = max(min(TREE ? w.r.pos0 : oldest + 1, cap), 0) / kKeys - w.s.tile0;
             whole0 = a.window > 0 ? max(newest - a.window + kKeys, 0) / kKeys - w.s.tile0 : 0;
           }
           const uint32_t to = tl + uint32_t(2 * C::SN + (piece & 1) * C::H * NR);  // O of this piece
           const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
           const bool whole = w.j >= whole0 && w.j < whole1;
+          // A tree's tile: bit i is set where the key is the unit's node i or above it, and the key's position less
+          // that of the tree's first, which a node's depth must be below by less than the window.
+          uint64_t nodes = 0;
+          int at_depth = 0;
+          if constexpr (TREE) {
+            const int node = key - w.r.pos0;
+            if (!whole && key < cap) {
+              if (node < 0) {
+                nodes = ~0ull;
+                at_depth = node;
+              } else if (node < w.r.n) {
+                const uint32_t* row = a.below + (long long)(w.r.s0 + node) * a.words;
+                const int from = w.s.i0 >> 5, sh = w.s.i0 & 31;
+                const uint32_t w0 = mask_word(row, a.words, from), w1 = mask_word(row, a.words, from + 1),
+                               w2 = mask_word(row, a.words, from + 2);
+                nodes = __funnelshift_r(w0, w1, sh) | uint64_t(__funnelshift_r(w1, w2, sh)) << 32;
+                if (a.window > 0) at_depth = a.depth[w.r.s0 + node];
+              }
+            }
+          }
           auto hide = [&](int x0, float* s) {
             if (whole) return;
+            if constexpr (TREE) {
+              int i = (c0 + x0) / a.G, g = c0 + x0 - i * a.G;
+#pragma unroll
+              for (int x = 0; x < CK; ++x) {
+                bool sees = nodes >> i & 1;
+                if (a.window > 0) sees = sees && at_depth > a.depth[w.r.s0 + min(w.s.i0 + i, w.s.i1)] - a.window;
+                if (!sees) s[x] = -INFINITY;
+                if (++g == a.G) g = 0, ++i;
+              }
+              return;
+            }
             // rows are in the order of their tokens: rows from .. to - 1 see this key
             const int i_from = max(key - oldest, 0), i_to = a.window > 0 ? key - oldest + a.window : a.tokens;
             const int from = key >= cap || i_from > a.tokens ? INT_MAX : i_from * a.G;
@@ -1088,8 +1139,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           // finite are taken out of the tile and added to the rows that do see them.
           bool spoiled = false;
           if (!whole) {
-            const bool gone = key < w.s.lo || key >= w.s.hi, mixed = w.s.i1 > w.s.i0;
-            const bool some = !gone && mixed && (key > oldest || (a.window > 0 && key <= newest - a.window));
+            const bool gone = key < w.s.lo || key >= w.s.hi, mixed = TREE || w.s.i1 > w.s.i0;
+            const bool some = !gone && mixed && ((TREE ? key >= w.r.pos0 : key > oldest) || (a.window > 0 && key <= newest - a.window));
             const int at = (E4M3 ? n : n + 1 == count ? 2 * count - 1 : 2 * n + 2) * C::H;  // V(n)'s place in the ring's order
             bool bad = false;
             // V(n)'s slots may still be held by V(n - 1), or in a ring for both by K(n + 1): see those filled
@@ -1145,7 +1196,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
                   const int pos = oldest + (c0 + x + y) / a.G;
-                  if (k <= pos && (a.window <= 0 || k > pos - a.window)) o[y] += add;
+                  if (TREE ? add != 0.f && tree_sees(a, w.r, min(pos - w.r.pos0, w.s.i1), k)
+                           : k <= pos && (a.window <= 0 || k > pos - a.window))
+                    o[y] += add;
                 }
                 st16(to + hh * NR + c0 + x, o);
               }
@@ -1415,7 +1468,14 @@ inline int row_tile(int D, int G, int n) {
   return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || D > 128 ? 64 : kChunkRows;
 }
 
-template <int D, int NR, bool E4M3>
+// The join of NR-row tiles, which is the same for every kernel: one of a file for each D.
+template <int D>
+int launch_join(const Args& a, int nr, bool many, int ctas, cudaStream_t s);
+template <> int launch_join<64>(const Args&, int, bool, int, cudaStream_t);
+template <> int launch_join<128>(const Args&, int, bool, int, cudaStream_t);
+template <> int launch_join<256>(const Args&, int, bool, int, cudaStream_t);
+
+template <int D, int NR, bool E4M3, bool TREE>
 int launch_one(const Args& a, int sms, cudaStream_t s) {
   using C = Cfg<D, NR, E4M3>;
   // So few units that each is cut into more than sixteen pieces even at one run an SM: one run then, as
@@ -1423,19 +1483,13 @@ int launch_one(const Args& a, int sms, cudaStream_t s) {
   // at two runs an SM, 49.6 at one, 46.9 with this join.
   const bool many = NR == 16 && (long long)a.kv.B * a.kv.Hkv * 16 < sms && cap_of(a.kv) > 16 * kKeys;
   const int ctas = many ? sms : sms * C::OCC;
-  if (launch_pdl(k_attn<D, NR, E4M3>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, a) != cudaSuccess) return MOE_ECUDA;
-  const cudaError_t e = NR == 16 && many ? launch_pdl(k_join_many<D>, dim3(ctas, a.G < 16 ? a.G : 16), dim3(kJoinThreads), 0, s, a)
-                                         : launch_pdl(k_join<D, NR>, dim3(ctas, join_y(NR)), dim3(kJoinThreads), 0, s, a);
-  if (e != cudaSuccess) return MOE_ECUDA;
-  return MOE_OK;
+  if (launch_pdl(k_attn<D, NR, E4M3, TREE>, dim3(ctas), dim3(C::THREADS), C::SMEM, s, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_join<D>(a, NR, many, ctas, s);
 }
-template <int D, int NR, bool E4M3>
+template <int D, int NR, bool E4M3, bool TREE>
 int opt_in() {
-  // the join keeps the split of L1 and shared memory that the kernel before it had
-  return cudaFuncSetAttribute(k_join<D, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
-                 cudaFuncSetAttribute(k_join_many<D>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
-                 cudaFuncSetAttribute(k_attn<D, NR, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NR, E4M3>::SMEM) ==
-                     cudaSuccess
+  return cudaFuncSetAttribute(k_attn<D, NR, E4M3, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<D, NR, E4M3>::SMEM) == cudaSuccess
              ? MOE_OK
              : MOE_ECUDA;
 }

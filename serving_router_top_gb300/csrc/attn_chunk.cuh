@@ -95,6 +95,31 @@ __device__ __forceinline__ void turn4(float (&v)[16], int lane) {
       }
 }
 
+// Bit j of seen: node i sees key key0 + j.
+__device__ __forceinline__ void tree_keys(const Args& a, const Req& r, int i, int key0, int cap, uint32_t* seen) {
+  const uint32_t* row = a.above + (long long)(r.s0 + i) * a.words;
+  const int node0 = key0 - r.pos0, deep = a.window > 0 ? a.depth[r.s0 + i] : 0;
+  const int from = a.window > 0 ? r.pos0 + deep - a.window + 1 - key0 : INT_MIN;  // of the keys before the tree
+  uint32_t low = mask_word(row, a.words, node0 >> 5);
+#pragma unroll
+  for (int k = 0; k < kKeys / 32; ++k) {
+    const uint32_t high = mask_word(row, a.words, (node0 >> 5) + k + 1);
+    uint32_t m = __funnelshift_r(low, high, node0 & 31);
+    low = high;
+    // keys past the request's or the table's end, and keys before the tree and the window
+    const int end = min(cap, r.kv) - key0 - 32 * k, begin = min(from, -node0) - 32 * k;
+    m = end >= 32 ? m : end <= 0 ? 0u : m & ((1u << end) - 1);
+    m = begin <= 0 ? m : begin >= 32 ? 0u : m & (0xffffffffu << begin);
+    if (a.window > 0 && deep >= a.window) {  // a window smaller than the tree is deep: nodes, one by one
+      for (uint32_t rest = m; rest; rest &= rest - 1) {
+        const int node = node0 + 32 * k + __ffs(rest) - 1;
+        if (node >= 0 && a.depth[r.s0 + node] <= deep - a.window) m &= ~(rest & -rest);
+      }
+    }
+    seen[k] = m;
+  }
+}
+
 // Registers a thread from here on, of a warpgroup.
 template <int N>
 __device__ __forceinline__ void take_registers() {
@@ -105,7 +130,7 @@ __device__ __forceinline__ void leave_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid_constant__ Args a) {
   using C = Cfg<D, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -148,13 +173,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
   pdl_wait();
   constexpr int V = C::V;
   const int cap = cap_of(a.kv);
-  const Plan plan = plan_run<V, C::THREADS>(a, cap, ms.plan);
+  const Plan plan = plan_run<V, C::THREADS, TREE>(a, cap, ms.plan);
   const uint32_t taddr = ms.taddr;
   const int run = blockIdx.x, count = plan.count;
   if (count == 0 && tid == 0) a.join[run] = make_int4(0, 0, 0, 0);
 
   if (count > 0) {
-    Walk<V> w;
+    Walk<V, TREE> w;
     w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
     const int half = a.tokens / 2;  // tokens of a row tile
     auto both = [&]() { return w.s.i1 - w.s.i0 + 1 > half; };  // the unit has rows for the second row tile
@@ -342,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
           if (id < 0 || id >= a.kv.npages) continue;  // the same: the slot of a page that reads as zeros
           const uint8_t* v = a.kv.v + id * a.kv.page_stride + w.h * a.kv.head_stride +
                              (long long)(key & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
-          const bool sees = key <= pos && (a.window <= 0 || key > pos - a.window);
+          const bool sees = TREE ? tree_sees(a, w.r, pos - w.r.pos0, key) : key <= pos && (a.window <= 0 || key > pos - a.window);
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -360,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
         if (nbad) st_wait();
         spoiled = -1;
       };
-      if (tid == 0) a.join[run] = join_record<V>(a, plan, w);
+      if (tid == 0) a.join[run] = join_record(a, plan, w);
 #pragma unroll 1
       for (int n = 0; n < count; ++n) {
         const bool active = x == 0 || both();
@@ -371,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
           const int newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
           const int pos = min(w.r.pos0 + w.s.i0 + mine, newest);
           const int key0 = (w.s.tile0 + w.j) * kKeys;
-          const bool whole = key0 + kKeys <= min(oldest + 1, cap) && (a.window <= 0 || key0 > newest - a.window);
+          const bool whole = key0 + kKeys <= min(TREE ? w.r.pos0 : oldest + 1, cap) && (a.window <= 0 || key0 > newest - a.window);
           wait(&ms.sfull[x], k & 1, fail);
           tc_after();
           if (spoiled >= 0) restore();  // S follows the product of the tile before it
@@ -386,9 +411,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
             // same in all of a row's weights.  With factors that are not, every tile takes the product first.
             const float once = factor > 0.f ? 1.f : factor;
             f = factor > 0.f ? factor : 1.f;
-            const int from = a.window > 0 ? pos - a.window + 1 - key0 : INT_MIN, to_key = min(pos + 1, cap) - key0;
+            if constexpr (TREE) {
+              uint32_t seen[kKeys / 32];  // of the tile's keys, by this row
+              tree_keys(a, w.r, pos - w.r.pos0, key0, cap, seen);
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] = i < from || i >= to_key ? -INFINITY : s[i] * once;
+              for (int i = 0; i < kKeys; ++i) s[i] = seen[i / 32] >> (i % 32) & 1 ? s[i] * once : -INFINITY;
+            } else {
+              const int from = a.window > 0 ? pos - a.window + 1 - key0 : INT_MIN, to_key = min(pos + 1, cap) - key0;
+#pragma unroll
+              for (int i = 0; i < kKeys; ++i) s[i] = i < from || i >= to_key ? -INFINITY : s[i] * once;
+            }
           }
           float top = -INFINITY, top1 = -INFINITY;  // the row's largest score
 #pragma unroll
@@ -432,13 +464,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
           // Values at hidden keys, as in attn.cuh: zeros where no row sees the key; where some do, what is
           // not finite leaves the tile and goes to their rows below.  The first row tile's threads, one a
           // key, do it for both: its product comes first.
-          const bool mixed = !whole && w.s.i1 > w.s.i0;
+          const bool mixed = !whole && (TREE || w.s.i1 > w.s.i0);
           if (!whole && x == 0) {
             if (mixed && krow == 0) ms.nbad[n & 3] = 0;
             if (mixed) asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
             const int key = key0 + krow, slot = (2 * n + 1) % C::NS;
             const bool gone = key < w.s.lo || key >= w.s.hi;
-            const bool some = !gone && mixed && (key > oldest || (a.window > 0 && key <= newest - a.window));
+            const bool some = !gone && mixed && ((TREE ? key >= w.r.pos0 : key > oldest) || (a.window > 0 && key <= newest - a.window));
             wait(&ms.full[slot], uint32_t((2 * n + 1) / C::NS) & 1, fail);  // V(n - NS / 2) has been used
             uint8_t* row = ring + slot * C::SLOT;
             if (gone) {
@@ -511,17 +543,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
   }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE>
 int launch(const Args& a, int ctas, cudaStream_t s) {
-  if (launch_pdl(k_chunk<D, E4M3>, dim3(ctas), dim3(Cfg<D, E4M3>::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
-  return launch_pdl(k_join<D, 256>, dim3(ctas, join_y(256)), dim3(kJoinThreads), 0, s, a) == cudaSuccess ? MOE_OK : MOE_ECUDA;
+  if (launch_pdl(k_chunk<D, E4M3, TREE>, dim3(ctas), dim3(Cfg<D, E4M3>::THREADS), kSmem, s, a) != cudaSuccess) return MOE_ECUDA;
+  return launch_join<D>(a, kChunkRows, false, ctas, s);
 }
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE>
 int opt_in() {
-  return cudaFuncSetAttribute(k_join<D, 256>, cudaFuncAttributePreferredSharedMemoryCarveout, 100) == cudaSuccess &&
-                 cudaFuncSetAttribute(k_chunk<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
-             ? MOE_OK
-             : MOE_ECUDA;
+  return cudaFuncSetAttribute(k_chunk<D, E4M3, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess ? MOE_OK
+                                                                                                                   : MOE_ECUDA;
 }
 
 }  // namespace chunk

@@ -1,4 +1,4 @@
-// moe_paged_attention: checks, workspace and launch (the kernels are in attn.cuh).
+// moe_paged_attention and moe_tree_attention: checks, workspace and launch (the kernels are in attn.cuh).
 #include <cudaTypedefs.h>
 
 #include "attn.cuh"
@@ -15,6 +15,12 @@ namespace attn {
 int launch_d64(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
 int launch_d128(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
 int launch_d256(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
+int launch_tree_d64(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
+int launch_tree_d128(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
+int launch_tree_d256(const Args& a, int e4m3, int nr, int sms, cudaStream_t s);
+int opt_in_tree_d64();
+int opt_in_tree_d128();
+int opt_in_tree_d256();
 int opt_in_d64();
 int opt_in_d128();
 int opt_in_d256();
@@ -59,7 +65,8 @@ extern "C" int moe_attn_ws_create(moe_attn_ws** out, int Hq, int Hkv, int D) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1 ||
-      (D == 64 ? attn::opt_in_d64() : D == 128 ? attn::opt_in_d128() : attn::opt_in_d256()) != MOE_OK) {
+      (D == 64 ? attn::opt_in_d64() : D == 128 ? attn::opt_in_d128() : attn::opt_in_d256()) != MOE_OK ||
+      (D == 64 ? attn::opt_in_tree_d64() : D == 128 ? attn::opt_in_tree_d128() : attn::opt_in_tree_d256()) != MOE_OK) {
     cudaGetLastError();
     free(w);
     return MOE_ECUDA;
@@ -118,10 +125,11 @@ extern "C" int moe_attn_sync_status(moe_attn_ws* w, moe_stream_t stream) {
   return e;
 }
 
-extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const uint16_t* q, long long q_stride,
-                                   int Hq, uint16_t* o, long long o_stride, float scale, int window, moe_attn_ws* ws,
-                                   moe_stream_t stream) {
-  using namespace moe;
+namespace moe {
+namespace {
+// Both calls; tree null: a request's new tokens follow one another.
+int attend(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const uint16_t* q, long long q_stride, int Hq,
+           uint16_t* o, long long o_stride, float scale, int window, moe_attn_ws* ws, moe_stream_t stream) {
   attn::Args a = {};
   const int rc = kv_view(kv, b, &a.kv);
   if (rc) return rc;
@@ -160,6 +168,12 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
       !attn::encode(&a.mv, kv->v, kv->e4m3, 4, dims, pitches, boxes, v_swizzle) ||
       !attn::encode(&a.mq, const_cast<uint16_t*>(q), 0, 3, qdims, qpitches, qbox, CU_TENSOR_MAP_SWIZZLE_128B))
     return MOE_EINVAL;
+  if (tree) {
+    a.above = tree->above;
+    a.below = tree->below;
+    a.depth = tree->depth;
+    a.words = tree->words;
+  }
   a.scale = scale;
   a.phantom = ws->phantom;
   a.err = ws->error;
@@ -168,8 +182,24 @@ extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b
   a.join = ws->join;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (kv->D) {
-    case 64: return attn::launch_d64(a, kv->e4m3, nr, ws->sms, s);
-    case 128: return attn::launch_d128(a, kv->e4m3, nr, ws->sms, s);
-    default: return attn::launch_d256(a, kv->e4m3, nr, ws->sms, s);
+    case 64: return (tree ? attn::launch_tree_d64 : attn::launch_d64)(a, kv->e4m3, nr, ws->sms, s);
+    case 128: return (tree ? attn::launch_tree_d128 : attn::launch_d128)(a, kv->e4m3, nr, ws->sms, s);
+    default: return (tree ? attn::launch_tree_d256 : attn::launch_d256)(a, kv->e4m3, nr, ws->sms, s);
   }
+}
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_paged_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const uint16_t* q, long long q_stride,
+                                   int Hq, uint16_t* o, long long o_stride, float scale, int window, moe_attn_ws* ws,
+                                   moe_stream_t stream) {
+  return moe::attend(kv, b, nullptr, q, q_stride, Hq, o, o_stride, scale, window, ws, stream);
+}
+
+extern "C" int moe_tree_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const uint16_t* q,
+                                  long long q_stride, int Hq, uint16_t* o, long long o_stride, float scale, int window,
+                                  moe_attn_ws* ws, moe_stream_t stream) {
+  if (!b || !tree || tree->words < 1 || tree->words > 8) return MOE_EINVAL;
+  if (b->B > 0 && b->T > 0 && (!tree->above || !tree->below || !tree->depth)) return MOE_EINVAL;
+  return moe::attend(kv, b, tree, q, q_stride, Hq, o, o_stride, scale, window, ws, stream);
 }

@@ -33,6 +33,11 @@ struct Args {
   long long qs, qos, ks, vs;
   int Hq;
   int32_t* err;
+  // moe_kv_append_norm alone
+  const int32_t* depth;  // of the rows in their trees, or null: they follow one another
+  int norm;
+  const uint16_t *wq, *wk;
+  float eps;
 };
 
 __device__ __forceinline__ void unpack8(uint4 u, float f[8]) {
@@ -93,13 +98,17 @@ __device__ __forceinline__ void store8(const Args& a, int t, int head, int col, 
 // one or three items a thread 32.0 and 28.4 us.
 constexpr int kMine = 2;
 
-template <bool E4M3, int D>
+// NORM: moe_kv_append_norm.  The lanes that hold a head's columns are neighbours (4, 8 or 16 of them, and a thread's
+// items all have the same columns), so its sum of squares is two to four exchanges between lanes, and the weights
+// are in registers before the request is found.  rsqrtf is within 2 units of fp32, as are the sum's roundings: far
+// below the one rounding that follows.
+template <bool E4M3, int D, bool NORM>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant__ Args a) {
   constexpr int kItems = D / 16;
   // cos, sin of each pair's angle: pair 8 j + i at [i][j], as the lanes of a head read them (64 bytes
   // apart, those met in four banks, and the prompt chunk took 32.2 us)
   __shared__ float2 cs[8][kMaxPairs / 8];
-  __shared__ int owner, position;
+  __shared__ int owner, position, begins;
   pdl_trigger();
   pdl_wait();
   const int t = blockIdx.x, step = blockDim.x, pairs = a.rot / 2;
@@ -132,6 +141,23 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   Item x[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) fetch(threadIdx.x + i * step, x[i]);
+  uint4 w[2][2];  // weights of this thread's columns: of the queries, of the keys
+  int deep = 0;
+  if constexpr (NORM) {
+    const int j = threadIdx.x % kItems;
+    const bool halves = 16 * j < a.rot && !a.interleaved;
+    const int c0 = halves ? 8 * j : 16 * j, c1 = halves ? pairs + 8 * j : 16 * j + 8;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint16_t* src = z ? a.wk : a.wq;
+      w[z][0] = w[z][1] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+      if (src) {
+        w[z][0] = *reinterpret_cast<const uint4*>(src + c0);
+        w[z][1] = *reinterpret_cast<const uint4*>(src + c1);
+      }
+    }
+    if (a.depth) deep = a.depth[t];
+  }
 
   // the request whose rows t is one of
   bool found = false;
@@ -139,6 +165,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
     const int s0 = a.kv.q_start[b], s1 = a.kv.q_start[b + 1], len = a.kv.kv_len[b];
     if (s0 <= t && t < s1) {
       owner = b;
+      if (NORM) begins = s0;
       position = int(min(max((long long)len - (s1 - t), (long long)INT_MIN), (long long)INT_MAX));
       found = true;
     }
@@ -149,9 +176,14 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   int id = -1;
   if (pos >= 0 && (pos >> a.kv.page_shift) < a.kv.table_stride)
     id = a.kv.page_table[(long long)b * a.kv.table_stride + (pos >> a.kv.page_shift)];
+  // the angles' position: a node's place is not it
+  int turned = pos;
+  if constexpr (NORM) {
+    if (a.depth) turned = int(min(max((long long)pos - (t - begins) + deep, (long long)INT_MIN), (long long)INT_MAX));
+  }
   for (int i = threadIdx.x; i < pairs; i += step) {
     // a signed fraction of a turn in [-1/2, 1/2); sincospif takes half turns
-    const long long frac = (long long)(uint64_t(int64_t(pos)) * a.turns[i]);
+    const long long frac = (long long)(uint64_t(int64_t(turned)) * a.turns[i]);
     float c, s;
     sincospif(float(frac) * 0x1p-63f, &s, &c);
     cs[i & 7][i >> 3] = make_float2(c, s);
@@ -167,6 +199,23 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
     float f0[8], f1[8];
     unpack8(x.v0, f0);
     unpack8(x.v1, f1);
+    if constexpr (NORM) {
+      if (a.norm && x.head < a.Hq + a.kv.Hkv) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], sum));
+        const unsigned mates = ((1u << kItems) - 1) << ((threadIdx.x & 31) / kItems * kItems);
+#pragma unroll
+        for (int o = 1; o < kItems; o <<= 1) sum += __shfl_xor_sync(mates, sum, o);
+        const float inv = rsqrtf(sum * (1.f / D) + a.eps);
+        const int z = x.head >= a.Hq;
+        float w0[8], w1[8];
+        unpack8(z ? w[1][0] : w[0][0], w0);
+        unpack8(z ? w[1][1] : w[0][1], w1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f0[i] *= inv * w0[i], f1[i] *= inv * w1[i];
+      }
+    }
     if (x.pair >= 0) {
       if (!a.interleaved) {
 #pragma unroll
@@ -200,14 +249,14 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   }
 }
 
-template <bool E4M3>
+template <bool E4M3, bool NORM>
 cudaError_t launch(int D, int T, cudaStream_t s, const Args& a) {
   const int n = (a.Hq + 2 * a.kv.Hkv) * (D / 16), each = (n + kMine - 1) / kMine;
   const dim3 block(each >= kMaxThreads ? kMaxThreads : (each + 31) / 32 * 32);
   switch (D) {
-    case 64: return launch_pdl(k_kv_append<E4M3, 64>, dim3(T), block, 0, s, a);
-    case 128: return launch_pdl(k_kv_append<E4M3, 128>, dim3(T), block, 0, s, a);
-    default: return launch_pdl(k_kv_append<E4M3, 256>, dim3(T), block, 0, s, a);
+    case 64: return launch_pdl(k_kv_append<E4M3, 64, NORM>, dim3(T), block, 0, s, a);
+    case 128: return launch_pdl(k_kv_append<E4M3, 128, NORM>, dim3(T), block, 0, s, a);
+    default: return launch_pdl(k_kv_append<E4M3, 256, NORM>, dim3(T), block, 0, s, a);
   }
 }
 
@@ -274,12 +323,15 @@ extern "C" int moe_rope_destroy(moe_rope* r) {
   return MOE_OK;
 }
 
-extern "C" int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q,
-                             long long q_stride, uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k,
-                             long long k_stride, const uint16_t* v, long long v_stride, int32_t* err_dev,
-                             moe_stream_t stream) {
-  using namespace moe;
-  append::Args a = {};
+namespace moe {
+namespace append {
+
+// The checks of both calls; `a` is filled and `work` tells whether there is anything to launch.
+int checked(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q, long long q_stride,
+            uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k, long long k_stride, const uint16_t* v,
+            long long v_stride, int32_t* err_dev, Args* out, bool* work) {
+  Args& a = *out;
+  *work = false;
   const int rc = kv_view(kv, b, &a.kv);
   if (rc) return rc;
   const int T = b->T, D = kv->D;
@@ -302,7 +354,50 @@ extern "C" int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, cons
   a.vs = v_stride;
   a.Hq = Hq;
   a.err = err_dev;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((kv->e4m3 ? append::launch<true>(D, T, s, a) : append::launch<false>(D, T, s, a)) != cudaSuccess) return MOE_ECUDA;
+  *work = true;
   return MOE_OK;
+}
+
+}  // namespace append
+}  // namespace moe
+
+extern "C" int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q,
+                             long long q_stride, uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k,
+                             long long k_stride, const uint16_t* v, long long v_stride, int32_t* err_dev,
+                             moe_stream_t stream) {
+  using namespace moe;
+  append::Args a = {};
+  bool work;
+  const int rc = append::checked(kv, b, rope, q, q_stride, q_out, q_out_stride, Hq, k, k_stride, v, v_stride, err_dev, &a, &work);
+  if (rc || !work) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return (kv->e4m3 ? append::launch<true, false>(kv->D, b->T, s, a) : append::launch<false, false>(kv->D, b->T, s, a)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ECUDA;
+}
+
+extern "C" int moe_kv_append_norm(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const moe_rope* rope,
+                                  const moe_head_norm* norm, const uint16_t* q, long long q_stride, uint16_t* q_out,
+                                  long long q_out_stride, int Hq, const uint16_t* k, long long k_stride, const uint16_t* v,
+                                  long long v_stride, int32_t* err_dev, moe_stream_t stream) {
+  using namespace moe;
+  append::Args a = {};
+  if (norm && (!(norm->eps > 0.f) || !isfinite(norm->eps) || (reinterpret_cast<uintptr_t>(norm->w_q) & 15) ||
+               (reinterpret_cast<uintptr_t>(norm->w_k) & 15)))
+    return MOE_EINVAL;
+  bool work;
+  const int rc = append::checked(kv, b, rope, q, q_stride, q_out, q_out_stride, Hq, k, k_stride, v, v_stride, err_dev, &a, &work);
+  if (rc || !work) return rc;
+  if (tree && !tree->depth) return MOE_EINVAL;
+  a.depth = tree ? tree->depth : nullptr;
+  a.norm = norm != nullptr;
+  if (norm) {
+    a.wq = norm->w_q;
+    a.wk = norm->w_k;
+    a.eps = norm->eps;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return (kv->e4m3 ? append::launch<true, true>(kv->D, b->T, s, a) : append::launch<false, true>(kv->D, b->T, s, a)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ECUDA;
 }

@@ -1,0 +1,196 @@
+// Keys and values that move inside a cache, in every layer's pools at once: the kept nodes of drafted trees to
+// the front of their tree, and copies of pages.
+//
+// What bounds them: memory for copies, and for kept nodes, whose few rows are a megabyte a layer at most, the
+// chain count, path, table, row, store.  One launch holds the pools of 128 layers, so a step pays for that chain once.
+#include "paged.cuh"
+
+namespace moe {
+namespace move {
+
+constexpr int kPools = 256;    // of a launch: keys and values of 128 layers
+constexpr int kMaxLayers = 4096;
+
+struct Args {
+  KvView kv;  // geometry and requests; its k and v are not used
+  int vecs;   // 16-byte pieces of a head's row
+  const int32_t *path, *count;
+  int path_stride;
+  int32_t *len, *err;
+  const int32_t *src, *dst, *tokens;
+  int blocks;  // of a page
+  uint8_t* pool[kPools];
+};
+
+// ------------------------------------------------------------------ kept nodes
+// A CTA per request and pool.  A thread moves one 16-byte column of a head through all kept nodes in their order,
+// kAhead loads before their stores: as kept indices rise, path[d] >= d, and no place is written before the thread has
+// read it.
+constexpr int kThreads = 256, kSteps = 256, kAhead = 8;
+
+__global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Args a) {
+  __shared__ long long from[kSteps], to[kSteps];
+  __shared__ int bad;
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const KvView& kv = a.kv;
+  const int s0 = min(max(kv.q_start[b], 0), kv.T), n = max(min(kv.q_start[b + 1], kv.T) - s0, 0);
+  const long long base = (long long)kv.kv_len[b] - n;
+  int want = a.count[b];
+  want = min(max(want, 0), min(n, a.path_stride));
+  const int32_t* path = a.path + (long long)b * a.path_stride;
+  const bool speaks = blockIdx.y == 0 && tid == 0;
+  uint8_t* pool = a.pool[blockIdx.y];
+  auto place = [&](long long p) -> long long {  // byte offset of a position in the pool, < 0: there is none
+    if (p < 0 || (p >> kv.page_shift) >= kv.table_stride) return -1;
+    const int id = kv.page_table[(long long)b * kv.table_stride + (p >> kv.page_shift)];
+    return id >= 0 && id < kv.npages ? id * kv.page_stride + (p & ((1 << kv.page_shift) - 1)) * kv.tok_stride : -1;
+  };
+  int kept = want;
+  for (int d0 = 0; d0 < kept; d0 += kSteps) {
+    if (tid == 0) bad = want;
+    __syncthreads();
+    const int d = d0 + tid;
+    int node = 0;
+    if (d < kept) {
+      node = path[d];
+      if (node < 0 || node >= n || (d > 0 && node <= path[d - 1])) atomicMin(&bad, d);
+    }
+    __syncthreads();
+    kept = min(kept, bad);
+    if (d < kept) {
+      from[tid] = to[tid] = -1;
+      if (node != d) {
+        from[tid] = place(base + node);
+        to[tid] = place(base + d);
+        if ((from[tid] < 0 || to[tid] < 0) && blockIdx.y == 0) set_error(a.err, MOE_ERANGE);
+      }
+    }
+    __syncthreads();
+    const int steps = min(kept - d0, kSteps);
+    for (int c = tid; c < kv.Hkv * a.vecs; c += kThreads) {
+      const int head = c / a.vecs;
+      uint8_t* col = pool + head * kv.head_stride + (c - head * a.vecs) * 16;
+      for (int e0 = 0; e0 < steps; e0 += kAhead) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (e0 + e < steps && from[e0 + e] >= 0 && to[e0 + e] >= 0) x[e] = *reinterpret_cast<const uint4*>(col + from[e0 + e]);
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+          if (e0 + e < steps && from[e0 + e] >= 0 && to[e0 + e] >= 0) *reinterpret_cast<uint4*>(col + to[e0 + e]) = x[e];
+      }
+    }
+    __syncthreads();
+  }
+  if (speaks) {
+    if (kept < want || kv.q_start[b + 1] < kv.q_start[b]) set_error(a.err, MOE_ERANGE);
+    if (a.len) a.len[b] = int(min(max(base + kept, (long long)INT32_MIN), (long long)INT32_MAX));
+  }
+}
+
+// ------------------------------------------------------------------ pages
+// A CTA takes kPiece 16-byte pieces of a page in one pool, all of a thread's loads before its stores.
+constexpr int kCopyThreads = 256, kEach = 8, kPiece = kCopyThreads * kEach;
+
+__global__ void __launch_bounds__(kCopyThreads) k_copy(const __grid_constant__ Args a) {
+  pdl_trigger();
+  pdl_wait();
+  const KvView& kv = a.kv;
+  const int i = blockIdx.x / a.blocks, part = blockIdx.x - i * a.blocks;
+  const int src = a.src[i], dst = a.dst[i];
+  int most = 1 << kv.page_shift;
+  if (a.tokens) most = min(a.tokens[i], most);
+  if (src < 0 || src >= kv.npages || dst < 0 || dst >= kv.npages) {
+    if (part == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_error(a.err, MOE_ERANGE);
+    return;
+  }
+  const int total = (kv.Hkv << kv.page_shift) * a.vecs;
+  const uint8_t* in = a.pool[blockIdx.y] + src * kv.page_stride;
+  uint8_t* out = a.pool[blockIdx.y] + dst * kv.page_stride;
+  uint4 x[kEach];
+  long long at[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int v = part * kPiece + e * kCopyThreads + threadIdx.x, row = v / a.vecs, tok = row & ((1 << kv.page_shift) - 1);
+    at[e] = -1;
+    if (v >= total || tok >= most) continue;
+    at[e] = (row >> kv.page_shift) * kv.head_stride + tok * kv.tok_stride + (v - row * a.vecs) * 16;
+    x[e] = *reinterpret_cast<const uint4*>(in + at[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e)
+    if (at[e] >= 0) *reinterpret_cast<uint4*>(out + at[e]) = x[e];
+}
+
+// Whether the layers' pools are of one geometry.
+bool alike(const moe_kv_pages* kv, int L) {
+  for (int l = 1; l < L; ++l) {
+    const moe_kv_pages &p = kv[0], &x = kv[l];
+    if (x.e4m3 != p.e4m3 || x.Hkv != p.Hkv || x.D != p.D || x.page != p.page || x.npages != p.npages ||
+        x.page_stride != p.page_stride || x.head_stride != p.head_stride || x.tok_stride != p.tok_stride || !x.k || !x.v ||
+        (reinterpret_cast<uintptr_t>(x.k) & 15) || (reinterpret_cast<uintptr_t>(x.v) & 15))
+      return false;
+  }
+  return true;
+}
+
+template <typename Kernel>
+int over_layers(Kernel kernel, Args& a, const moe_kv_pages* kv, int L, unsigned x, int threads, cudaStream_t s) {
+  for (int l0 = 0; l0 < L; l0 += kPools / 2) {
+    const int m = L - l0 < kPools / 2 ? L - l0 : kPools / 2;
+    for (int l = 0; l < m; ++l) {
+      a.pool[2 * l] = static_cast<uint8_t*>(kv[l0 + l].k);
+      a.pool[2 * l + 1] = static_cast<uint8_t*>(kv[l0 + l].v);
+    }
+    if (launch_pdl(kernel, dim3(x, 2 * m), dim3(threads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace move
+}  // namespace moe
+
+extern "C" int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch* b, const int32_t* path, int path_stride,
+                              const int32_t* count, int32_t* kv_len_out, int32_t* err_dev, moe_stream_t stream) {
+  using namespace moe;
+  move::Args a = {};
+  if (!kv || L < 1 || L > move::kMaxLayers) return MOE_EINVAL;
+  const int rc = kv_view(kv, b, &a.kv);
+  if (rc) return rc;
+  if (!move::alike(kv, L) || path_stride < 1 || (kv_len_out && kv_len_out == b->kv_len)) return MOE_EINVAL;
+  if (b->B == 0) return MOE_OK;
+  if (!path || !count || !b->q_start || !b->kv_len || (!b->page_table && b->table_stride > 0)) return MOE_EINVAL;
+  a.vecs = kv->D * (kv->e4m3 ? 1 : 2) / 16;
+  a.path = path;
+  a.count = count;
+  a.path_stride = path_stride;
+  a.len = kv_len_out;
+  a.err = err_dev;
+  return move::over_layers(move::k_compact, a, kv, L, unsigned(b->B), move::kThreads, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_kv_copy_pages(const moe_kv_pages* kv, int L, const int32_t* src, const int32_t* dst,
+                                 const int32_t* tokens, int n, int32_t* err_dev, moe_stream_t stream) {
+  using namespace moe;
+  move::Args a = {};
+  if (!kv || L < 1 || L > move::kMaxLayers || n < 0 || n > 1 << 20) return MOE_EINVAL;
+  const moe_kv_batch none = {};
+  const int rc = kv_view(kv, &none, &a.kv);
+  if (rc) return rc;
+  if (!move::alike(kv, L)) return MOE_EINVAL;
+  if (n == 0) return MOE_OK;
+  if (!src || !dst) return MOE_EINVAL;
+  a.vecs = kv->D * (kv->e4m3 ? 1 : 2) / 16;
+  const long long pieces = (long long)kv->Hkv * kv->page * a.vecs;
+  if (pieces > INT32_MAX - move::kPiece) return MOE_EINVAL;
+  a.blocks = int((pieces + move::kPiece - 1) / move::kPiece);
+  if ((long long)n * a.blocks > INT32_MAX) return MOE_EINVAL;
+  a.src = src;
+  a.dst = dst;
+  a.tokens = tokens;
+  a.err = err_dev;
+  return move::over_layers(move::k_copy, a, kv, L, unsigned(n * a.blocks), move::kCopyThreads,
+                           reinterpret_cast<cudaStream_t>(stream));
+}

@@ -32,7 +32,8 @@ EXPORTED = (
     "moe_ws_set_fused_heat", "cache_lru_plan", "moe_cache_apply_lru", "moe_ws_set_decode_path",
     "moe_ws_set_wait_test", "moe_nvfp4_split", "moe_layers_forward_streamed", "moe_rope_create", "moe_rope_destroy",
     "moe_kv_append", "moe_attn_ws_create", "moe_attn_ws_destroy", "moe_attn_ws_get_view", "moe_attn_sync_status",
-    "moe_paged_attention", "moe_block_norm", "moe_attn_ws_set_wait_test",
+    "moe_paged_attention", "moe_block_norm", "moe_attn_ws_set_wait_test", "moe_tree_prepare", "moe_kv_append_norm",
+    "moe_tree_attention", "moe_verify_drafts", "moe_kv_compact", "moe_kv_copy_pages",
 )
 
 
@@ -85,6 +86,21 @@ class moe_kv_batch(C.Structure):
 
 class moe_attn_ws_view(C.Structure):
     _fields_ = [("error", C.c_void_p)]
+
+
+class moe_tree(C.Structure):
+    _fields_ = [("parent", C.c_void_p), ("depth", C.c_void_p), ("above", C.c_void_p), ("below", C.c_void_p),
+                ("words", C.c_int)]
+
+
+class moe_head_norm(C.Structure):
+    _fields_ = [("w_q", C.c_void_p), ("w_k", C.c_void_p), ("eps", C.c_float)]
+
+
+class moe_verify_desc(C.Structure):
+    _fields_ = [("target", C.c_void_p), ("target_stride", C.c_longlong), ("draft", C.c_void_p),
+                ("draft_stride", C.c_longlong), ("token", C.c_void_p), ("parent", C.c_void_p), ("u", C.c_void_p),
+                ("u_last", C.c_void_p), ("V", C.c_int)]
 
 
 class moe_block_norm_desc(C.Structure):
@@ -151,6 +167,12 @@ def load() -> C.CDLL:
         "moe_attn_ws_set_wait_test": (I, [P, I]),
         "moe_paged_attention": (I, [P, P, P, Q, I, P, Q, F, I, P, P]),
         "moe_block_norm": (I, [P, P, Q, P, Q, P, Q, I, I, P]),
+        "moe_tree_prepare": (I, [P, P, P, P]),
+        "moe_kv_append_norm": (I, [P, P, P, P, P, P, Q, P, Q, I, P, Q, P, Q, P, P]),
+        "moe_tree_attention": (I, [P, P, P, P, Q, I, P, Q, F, I, P, P]),
+        "moe_verify_drafts": (I, [P, P, P, I, P, P, P, P]),
+        "moe_kv_compact": (I, [P, I, P, P, I, P, P, P, P]),
+        "moe_kv_copy_pages": (I, [P, I, P, P, P, I, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -683,3 +705,191 @@ def moe_block_norm(desc: BlockNormDesc, x, x_out, xn, T: int, H: int, stream=Non
     if not (desc.on_gpu and x.is_cuda and (x_out is None or x_out.is_cuda) and (xn is None or xn.is_cuda)):
         raise ValueError(_ELSEWHERE)
     _check(load().moe_block_norm(desc.ref, xp, xs, op, os_, np_, ns, T, H, _stream(stream)), "moe_block_norm")
+
+
+# --------------------------------------------- a step of drafted token trees
+
+def _ints(t, shape, what: str):
+    """Address of a contiguous int32 tensor."""
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {list(shape)}, got {list(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+def _error_word(err):
+    """Address of an error word, and whether it is where the kernels can write it."""
+    if err is None or isinstance(err, int):
+        return err, True
+    return _ints(err, (1,), "err"), err.is_cuda
+
+
+class Tree:
+    """The trees of a batch's new tokens: parent int32 [T], an index among the request's own rows or -1;
+    depth int32 [T] and the masks above and below int32 [T, words], which moe_tree_prepare fills."""
+
+    def __init__(self, batch: KvBatch, parent):
+        import torch
+        T, words = batch.c.T, max(1, -(-batch.c.max_n // 32))
+        if words > 8:
+            raise ValueError(f"Tree: at most 256 nodes a request, max_n is {batch.c.max_n}")
+        p = _ints(parent, (T,), "parent")
+        self.parent, self.words = parent, words
+        self.depth = torch.zeros(T, dtype=torch.int32, device=parent.device)
+        self.above, self.below = (torch.zeros(T, words, dtype=torch.int32, device=parent.device) for _ in range(2))
+        self.c = moe_tree(p, self.depth.data_ptr(), self.above.data_ptr(), self.below.data_ptr(), words)
+        self.T, self.on_gpu = T, parent.is_cuda
+        self.ref = C.addressof(self.c)
+
+
+def _same_rows(batch: KvBatch, tree: "Tree") -> None:
+    if tree.T != batch.c.T:
+        raise ValueError(f"the tree has {tree.T} rows, the batch {batch.c.T}")
+
+
+def moe_tree_prepare(batch: KvBatch, tree: Tree, err=None, stream=None) -> None:
+    """Depths and masks of the trees from their parents, once for all layers of a step."""
+    _same_rows(batch, tree)
+    ep, there = _error_word(err)
+    if not (batch.on_gpu and tree.on_gpu and there):
+        raise ValueError(_ELSEWHERE)
+    _check(load().moe_tree_prepare(batch.ref, tree.ref, ep, _stream(stream)), "moe_tree_prepare")
+
+
+class HeadNorm:
+    """Norms of each head's queries and keys: weights bf16 [D] (or their bits) or None, for ones."""
+
+    def __init__(self, w_q=None, w_k=None, eps: float = 1e-6):
+        bf16 = _row_types()[1]
+        for w in (w_q, w_k):
+            if w is not None and (w.dim() != 1 or w.dtype not in bf16 or not w.is_contiguous()):
+                raise ValueError("HeadNorm: the weights are contiguous bf16 [D]")
+        widths = {w.numel() for w in (w_q, w_k) if w is not None}
+        if len(widths) > 1:
+            raise ValueError("HeadNorm: the weights differ in size")
+        self.w_q, self.w_k, self.D = w_q, w_k, widths.pop() if widths else None
+        self.c = moe_head_norm(_ptr(w_q), _ptr(w_k), eps)
+        self.on_gpu = _on_gpu(w_q, w_k)
+        self.ref = C.addressof(self.c)
+
+
+def moe_kv_append_norm(pages: KvPages, batch: KvBatch, rope: Optional[Rope], norm: Optional[HeadNorm], q, q_out, k, v,
+                       tree: Optional[Tree] = None, err=None, stream=None) -> None:
+    """moe_kv_append behind norms of the queries' and keys' heads, at the positions of a tree's nodes."""
+    T, D, bf16 = batch.c.T, pages.D, _row_types()[1]
+    kv = (T, pages.Hkv, D)
+    kp, ks = _heads(k, kv, bf16, "k")
+    vp, vs = _heads(v, kv, bf16, "v")
+    on_gpu = pages.on_gpu and batch.on_gpu and k.is_cuda and v.is_cuda
+    Hq, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        Hq = q.shape[1]
+        rows = (T, Hq, D)
+        qp, qs = _heads(q, rows, bf16, "q")
+        op, os_ = (qp, qs) if q_out is q else _heads(q_out, rows, bf16, "q_out")
+        on_gpu = on_gpu and q.is_cuda and q_out.is_cuda
+    if norm is not None:
+        if norm.D not in (None, D):
+            raise ValueError(f"moe_kv_append_norm: the norms' weights are [{D}]")
+        on_gpu = on_gpu and norm.on_gpu
+    if tree is not None:
+        _same_rows(batch, tree)
+        on_gpu = on_gpu and tree.on_gpu
+    ep, there = _error_word(err)
+    if not (on_gpu and there):
+        raise ValueError(_ELSEWHERE)
+    _check(load().moe_kv_append_norm(pages.ref, batch.ref, None if tree is None else tree.ref,
+                                     None if rope is None else rope.handle, None if norm is None else norm.ref, qp, qs, op,
+                                     os_, Hq, kp, ks, vp, vs, ep, _stream(stream)), "moe_kv_append_norm")
+
+
+def moe_tree_attention(pages: KvPages, batch: KvBatch, tree: Tree, q, o, ws: AttnWorkspace, scale: float, window: int = 0,
+                       stream=None) -> None:
+    """o (bf16 [T, Hq, D]) = attention of every tree node over its request's pages and the nodes above it."""
+    rows, bf16 = (batch.c.T, ws.Hq, pages.D), _row_types()[1]
+    qp, qs = _heads(q, rows, bf16, "q")
+    op, os_ = _heads(o, rows, bf16, "o")
+    _same_rows(batch, tree)
+    if not (pages.on_gpu and batch.on_gpu and tree.on_gpu and q.is_cuda and o.is_cuda):
+        raise ValueError(_ELSEWHERE)
+    _check(load().moe_tree_attention(pages.ref, batch.ref, tree.ref, qp, qs, ws.Hq, op, os_, scale, window, ws.handle,
+                                     _stream(stream)), "moe_tree_attention")
+
+
+class VerifyDesc:
+    """Owner of a moe_verify_desc and references to its tensors."""
+
+    def __init__(self, target, token, parent, u, u_last, draft=None):
+        import torch
+        if target.dim() != 2:
+            raise ValueError("verify_desc: target is float32 [T, V]")
+        T, V = target.shape
+        fp32 = _row_types()[0]
+        tp, ts = _columns(target, (T, V), fp32, "target")
+        dp, ds = (None, 0) if draft is None else _columns(draft, (T, V), fp32, "draft")
+        for t, n in ((u, (T,)), (u_last, (u_last.numel(),))):
+            if t.dtype != torch.float32 or tuple(t.shape) != n or not t.is_contiguous():
+                raise ValueError("verify_desc: u and u_last are contiguous float32 [T] and [B]")
+        self.tensors = (target, token, parent, u, u_last, draft)
+        self.T, self.B = T, u_last.numel()
+        self.c = moe_verify_desc(tp, ts, dp, ds, _ints(token, (T,), "token"), _ints(parent, (T,), "parent"), u.data_ptr(),
+                                 u_last.data_ptr(), V)
+        self.on_gpu = _on_gpu(*self.tensors)
+        self.ref = C.addressof(self.c)
+
+
+def verify_desc(target, token, parent, u, u_last, draft=None) -> VerifyDesc:
+    return VerifyDesc(target, token, parent, u, u_last, draft)
+
+
+def moe_verify_drafts(batch: KvBatch, desc: VerifyDesc, path, count, token, err=None, stream=None) -> None:
+    """path int32 [B, most], count and token int32 [B]: the nodes the target keeps and the next token."""
+    B = batch.c.B
+    if desc.T != batch.c.T or desc.B != B:
+        raise ValueError(f"moe_verify_drafts: {desc.T} rows and {desc.B} requests, the batch has {batch.c.T} and {B}")
+    if path.dim() != 2:
+        raise ValueError("path: int32 [B, most nodes kept]")
+    pp, cp, tp = _ints(path, (B, path.shape[1]), "path"), _ints(count, (B,), "count"), _ints(token, (B,), "token")
+    ep, there = _error_word(err)
+    if not (batch.on_gpu and desc.on_gpu and path.is_cuda and count.is_cuda and token.is_cuda and there):
+        raise ValueError(_ELSEWHERE)
+    _check(load().moe_verify_drafts(batch.ref, desc.ref, pp, path.shape[1], cp, tp, ep, _stream(stream)),
+           "moe_verify_drafts")
+
+
+class KvLayers:
+    """The pools of a model's layers, of one geometry, for the calls that move keys and values in all of them."""
+
+    def __init__(self, layers):
+        self.layers = list(layers)
+        if not self.layers or any(not isinstance(p, KvPages) for p in self.layers):
+            raise ValueError("KvLayers: a list of KvPages, one a layer")
+        self.c = (moe_kv_pages * len(self.layers))(*[p.c for p in self.layers])
+        self.on_gpu = all(p.on_gpu for p in self.layers)
+        self.ref = C.addressof(self.c)
+
+
+def moe_kv_compact(layers: KvLayers, batch: KvBatch, path, count, kv_len_out=None, err=None, stream=None) -> None:
+    """Keys and values of the kept nodes to the front of their trees in every layer; kv_len_out int32 [B]: the new lengths."""
+    B = batch.c.B
+    if path.dim() != 2:
+        raise ValueError("path: int32 [B, most nodes kept]")
+    pp, cp = _ints(path, (B, path.shape[1]), "path"), _ints(count, (B,), "count")
+    lp = None if kv_len_out is None else _ints(kv_len_out, (B,), "kv_len_out")
+    ep, there = _error_word(err)
+    if not (layers.on_gpu and batch.on_gpu and path.is_cuda and count.is_cuda and (kv_len_out is None or kv_len_out.is_cuda)
+            and there):
+        raise ValueError(_ELSEWHERE)
+    _check(load().moe_kv_compact(layers.ref, len(layers.layers), batch.ref, pp, path.shape[1], cp, lp, ep, _stream(stream)),
+           "moe_kv_compact")
+
+
+def moe_kv_copy_pages(layers: KvLayers, src, dst, tokens=None, err=None, stream=None) -> None:
+    """Page src[i] to page dst[i] in every layer, or its first tokens[i] places."""
+    n = src.numel()
+    sp, dp = _ints(src, (n,), "src"), _ints(dst, (n,), "dst")
+    tp = None if tokens is None else _ints(tokens, (n,), "tokens")
+    ep, there = _error_word(err)
+    if not (layers.on_gpu and src.is_cuda and dst.is_cuda and (tokens is None or tokens.is_cuda) and there):
+        raise ValueError(_ELSEWHERE)
+    _check(load().moe_kv_copy_pages(layers.ref, len(layers.layers), sp, dp, tp, n, ep, _stream(stream)), "moe_kv_copy_pages")
