@@ -512,7 +512,7 @@ __device__ __forceinline__ int4 join_record(const Args& a, const Plan& p, const 
   return make_int4(w.r.s0 + w.s.i0, w.h, (w.s.i1 - w.s.i0 + 1) * a.G, run_of(p.total, p.runs, at + w.s.nt - 1) - run + 2);
 }
 
-template <int NR>
+template <int NR, bool TREE>
 struct Misc {
   uint64_t full[16], empty[16], kfull[8], kempty[8], rfull[8], rempty[8], factors[2], qfull[2], qfree[2], sfull[2], pfull[2], pvdone[2], ofree[2], drain;
   uint32_t taddr;
@@ -526,6 +526,7 @@ struct Misc {
   int page[2][kKeys];        // pages of a tile's boxes, for keys and for values
   int nbad;
   uint8_t bad[kKeys];  // keys of a tile with values that are not finite
+  uint8_t deep[TREE ? NR : 1];  // a tree under a window: its rows' depths
 };
 
 // Whether a key's row of N columns in a slot has a value that is not finite: 0 times it is NaN.
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
   uint8_t* raw = kring + C::NK * C::RAW;        // E4M3: values as they come
   uint8_t* sq = raw + C::NRAW * C::RAW;
   uint8_t* sp = sq + C::QB * C::QBYTES;
-  using Ms = Misc<NR>;
+  using Ms = Misc<NR, TREE>;
   static_assert(sizeof(Ms) <= misc_bytes(NR), "misc");
   Ms& ms = *reinterpret_cast<Ms*>(sp + 2 * C::PBYTES);
   volatile int* fail = &ms.fail;
@@ -1035,6 +1036,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
             newest = w.r.pos0 + w.s.i1, oldest = w.r.pos0 + w.s.i0;
             whole1 = max(min(TREE ? w.r.pos0 : oldest + 1, cap), 0) / kKeys - w.s.tile0;
             whole0 = a.window > 0 ? max(newest - a.window + kKeys, 0) / kKeys - w.s.tile0 : 0;
+            if (TREE && a.window > 0) {  // the piece before was read by all before its sums were added up
+              if (tid < NR) ms.deep[tid] = uint8_t(a.depth[w.r.s0 + min(w.s.i0 + tid / a.G, w.s.i1)]);
+              softmax_sync<kSoft>();
+            }
           }
           const uint32_t to = tl + uint32_t(2 * C::SN + (piece & 1) * C::H * NR);  // O of this piece
           const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
@@ -1066,7 +1071,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
 #pragma unroll
               for (int x = 0; x < CK; ++x) {
                 bool sees = nodes >> i & 1;
-                if (a.window > 0) sees = sees && at_depth > a.depth[w.r.s0 + min(w.s.i0 + i, w.s.i1)] - a.window;
+                if (a.window > 0) sees = sees && at_depth > ms.deep[c0 + x0 + x] - a.window;
                 if (!sees) s[x] = -INFINITY;
                 if (++g == a.G) g = 0, ++i;
               }

@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   // apart, those met in four banks, and the prompt chunk took 32.2 us)
   __shared__ float2 cs[8][kMaxPairs / 8];
   __shared__ int owner, position, begins;
+  __shared__ uint4 weights[NORM ? D / 4 : 1];
   pdl_trigger();
   pdl_wait();
   const int t = blockIdx.x, step = blockDim.x, pairs = a.rot / 2;
@@ -141,21 +142,14 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   Item x[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) fetch(threadIdx.x + i * step, x[i]);
-  uint4 w[2][2];  // weights of this thread's columns: of the queries, of the keys
   int deep = 0;
   if constexpr (NORM) {
-    const int j = threadIdx.x % kItems;
-    const bool halves = 16 * j < a.rot && !a.interleaved;
-    const int c0 = halves ? 8 * j : 16 * j, c1 = halves ? pairs + 8 * j : 16 * j + 8;
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const uint16_t* src = z ? a.wk : a.wq;
-      w[z][0] = w[z][1] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-      if (src) {
-        w[z][0] = *reinterpret_cast<const uint4*>(src + c0);
-        w[z][1] = *reinterpret_cast<const uint4*>(src + c1);
+    if (a.norm)
+      for (int i = threadIdx.x; i < D / 4; i += step) {  // eight columns of the queries' weights, then of the keys'
+        const uint16_t* src = i < D / 8 ? a.wq : a.wk;
+        weights[i] = src ? reinterpret_cast<const uint4*>(src)[i % (D / 8)]
+                         : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
       }
-    }
     if (a.depth) deep = a.depth[t];
   }
 
@@ -208,10 +202,10 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
 #pragma unroll
         for (int o = 1; o < kItems; o <<= 1) sum += __shfl_xor_sync(mates, sum, o);
         const float inv = rsqrtf(sum * (1.f / D) + a.eps);
-        const int z = x.head >= a.Hq;
+        const int z = x.head >= a.Hq ? D / 8 : 0;
         float w0[8], w1[8];
-        unpack8(z ? w[1][0] : w[0][0], w0);
-        unpack8(z ? w[1][1] : w[0][1], w1);
+        unpack8(weights[z + x.c0 / 8], w0);
+        unpack8(weights[z + x.c1 / 8], w1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f0[i] *= inv * w0[i], f1[i] *= inv * w1[i];
       }

@@ -19,6 +19,7 @@ struct Args {
   int32_t *len, *err;
   const int32_t *src, *dst, *tokens;
   int blocks;  // of a page
+  int pools, first;  // of the launch; the call's first launch
   uint8_t* pool[kPools];
 };
 
@@ -26,7 +27,7 @@ struct Args {
 // A CTA per request and pool.  A thread moves one 16-byte column of a head through all kept nodes in their order,
 // kAhead loads before their stores: as kept indices rise, path[d] >= d, and no place is written before the thread has
 // read it.
-constexpr int kThreads = 256, kSteps = 256, kAhead = 8;
+constexpr int kThreads = 256, kSteps = 256, kAhead = 8, kCompactPerSm = 4;
 
 __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Args a) {
   __shared__ long long from[kSteps], to[kSteps];
@@ -40,8 +41,10 @@ __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Ar
   int want = a.count[b];
   want = min(max(want, 0), min(n, a.path_stride));
   const int32_t* path = a.path + (long long)b * a.path_stride;
-  const bool speaks = blockIdx.y == 0 && tid == 0;
-  uint8_t* pool = a.pool[blockIdx.y];
+  const bool speaks = a.first && blockIdx.y == 0 && tid == 0;
+  // this CTA's pools, and their columns of all heads
+  const int each = (a.pools + gridDim.y - 1) / gridDim.y, pool0 = blockIdx.y * each, pools = min(each, a.pools - pool0);
+  const int cols = kv.Hkv * a.vecs;
   auto place = [&](long long p) -> long long {  // byte offset of a position in the pool, < 0: there is none
     if (p < 0 || (p >> kv.page_shift) >= kv.table_stride) return -1;
     const int id = kv.page_table[(long long)b * kv.table_stride + (p >> kv.page_shift)];
@@ -64,14 +67,14 @@ __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Ar
       if (node != d) {
         from[tid] = place(base + node);
         to[tid] = place(base + d);
-        if ((from[tid] < 0 || to[tid] < 0) && blockIdx.y == 0) set_error(a.err, MOE_ERANGE);
+        if (from[tid] < 0 || to[tid] < 0) set_error(a.err, MOE_ERANGE);
       }
     }
     __syncthreads();
     const int steps = min(kept - d0, kSteps);
-    for (int c = tid; c < kv.Hkv * a.vecs; c += kThreads) {
-      const int head = c / a.vecs;
-      uint8_t* col = pool + head * kv.head_stride + (c - head * a.vecs) * 16;
+    for (int c = tid; c < pools * cols; c += kThreads) {
+      const int pool = c / cols, head = (c - pool * cols) / a.vecs;
+      uint8_t* col = a.pool[pool0 + pool] + head * kv.head_stride + (c - pool * cols - head * a.vecs) * 16;
       for (int e0 = 0; e0 < steps; e0 += kAhead) {
         uint4 x[kAhead];
 #pragma unroll
@@ -136,15 +139,18 @@ bool alike(const moe_kv_pages* kv, int L) {
   return true;
 }
 
+// y: CTAs over the pools of a launch, 0: one each.
 template <typename Kernel>
-int over_layers(Kernel kernel, Args& a, const moe_kv_pages* kv, int L, unsigned x, int threads, cudaStream_t s) {
+int over_layers(Kernel kernel, Args& a, const moe_kv_pages* kv, int L, unsigned x, int y, int threads, cudaStream_t s) {
   for (int l0 = 0; l0 < L; l0 += kPools / 2) {
     const int m = L - l0 < kPools / 2 ? L - l0 : kPools / 2;
+    a.pools = 2 * m;
+    a.first = l0 == 0;
     for (int l = 0; l < m; ++l) {
       a.pool[2 * l] = static_cast<uint8_t*>(kv[l0 + l].k);
       a.pool[2 * l + 1] = static_cast<uint8_t*>(kv[l0 + l].v);
     }
-    if (launch_pdl(kernel, dim3(x, 2 * m), dim3(threads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+    if (launch_pdl(kernel, dim3(x, y > 0 && y < 2 * m ? y : 2 * m), dim3(threads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
   }
   return MOE_OK;
 }
@@ -168,7 +174,9 @@ extern "C" int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch*
   a.path_stride = path_stride;
   a.len = kv_len_out;
   a.err = err_dev;
-  return move::over_layers(move::k_compact, a, kv, L, unsigned(b->B), move::kThreads, reinterpret_cast<cudaStream_t>(stream));
+  // CTAs for one turn of the GPU's 152 SMs, each over several pools: the chain before the first row is paid once
+  const int y = (152 * move::kCompactPerSm + b->B - 1) / b->B;
+  return move::over_layers(move::k_compact, a, kv, L, unsigned(b->B), y, move::kThreads, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_kv_copy_pages(const moe_kv_pages* kv, int L, const int32_t* src, const int32_t* dst,
@@ -191,6 +199,6 @@ extern "C" int moe_kv_copy_pages(const moe_kv_pages* kv, int L, const int32_t* s
   a.dst = dst;
   a.tokens = tokens;
   a.err = err_dev;
-  return move::over_layers(move::k_copy, a, kv, L, unsigned(n * a.blocks), move::kCopyThreads,
+  return move::over_layers(move::k_copy, a, kv, L, unsigned(n * a.blocks), 0, move::kCopyThreads,
                            reinterpret_cast<cudaStream_t>(stream));
 }

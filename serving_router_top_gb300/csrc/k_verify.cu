@@ -23,7 +23,7 @@ namespace verify {
 
 using u64 = unsigned long long;
 
-constexpr int kNodes = 256, kThreads = 256, kWarps = kThreads / 32, kMaxCtas = 8;
+constexpr int kNodes = 256, kThreads = 512, kWarps = kThreads / 32, kMaxCtas = 16, kGroups = 4;
 constexpr u64 kOne = 1ull << 60, kMost = 1ull << 62;
 
 struct Args {
@@ -118,12 +118,13 @@ __device__ __forceinline__ u64 rest(float p, float q, int refused, const u64* si
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ Args a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = int(my_rank()), C = int(ranks()), b = blockIdx.x / C;
   pdl_trigger();
   pdl_wait();
+  const float u_last = a.u_last[b];
   // ------------------------------------------------------------ the first CTA's view of the tree
   int s0 = 0, n = 0;
   if (rank == 0) {
@@ -178,6 +179,11 @@ __global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ Arg
   };
   if (rank == 0 && warp == 0 && n > 0) arrive_at(0);
 
+  // A warp's lines of 128 places are in four groups, a line of each read at once.  With one line to a group the values
+  // stay in registers: further sums over the same row, and the draw, read nothing.
+  float4 x[kGroups], y[kGroups];
+  int held = -1;         // the row that they are of
+  bool held_q = false;   // and of the draft's
   bool own_row = false;  // nothing was left of R: the target's own row is drawn from
   for (;;) {
     if (!own_row) {
@@ -252,40 +258,52 @@ __global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ Arg
     }
     const int lines = (rows.end + 127) / 128, each = (lines + C * kWarps - 1) / (C * kWarps);  // of 128 places; of a warp
     const int line0 = min((rank * kWarps + warp) * each, lines), line1 = min(line0 + each, lines);
-    u64 mine = 0;
-    constexpr int kAhead = 4;
-    for (int l = line0; l < line1; l += kAhead) {
-      float4 x[kAhead], y[kAhead];
+    const int deep = (each + kGroups - 1) / kGroups;  // lines of a group
+    u64 sum[kGroups] = {};
+    for (int l = 0; l < deep; ++l) {
+      const bool p_here = deep == 1 && held == o.row, q_here = p_here && held_q;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (l + i < line1) {
-          load4(rows.p, rows, 128 * (l + i) + 4 * lane, true, &x[i]);
-          if (o.refused > 0) load4(rows.q, rows, 128 * (l + i) + 4 * lane, rows.together, &y[i]);
+      for (int g = 0; g < kGroups; ++g) {
+        const int line = line0 + g * deep + l;
+        if (!p_here) x[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!q_here) y[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (line < line1) {
+          if (!p_here) load4(rows.p, rows, 128 * line + 4 * lane, true, &x[g]);
+          if (!q_here && o.refused > 0) load4(rows.q, rows, 128 * line + 4 * lane, rows.together, &y[g]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int g = 0; g < kGroups; ++g) {
         // four of at most 2^60 beside at most 2^62: no carry is lost
-        mine += rest(x[i].x, y[i].x, o.refused, sh.sigma) + rest(x[i].y, y[i].y, o.refused, sh.sigma) +
-                rest(x[i].z, y[i].z, o.refused, sh.sigma) + rest(x[i].w, y[i].w, o.refused, sh.sigma);
-        mine = min(mine, kMost);
+        sum[g] += rest(x[g].x, y[g].x, o.refused, sh.sigma) + rest(x[g].y, y[g].y, o.refused, sh.sigma) +
+                  rest(x[g].z, y[g].z, o.refused, sh.sigma) + rest(x[g].w, y[g].w, o.refused, sh.sigma);
+        sum[g] = min(sum[g], kMost);
       }
     }
+    held = o.row;
+    held_q = o.refused > 0;
+    // Without the picked ones that are gone, from line `from` to before line `to`.
+    auto without = [&](u64 v, int from, int to) {
+      for (int k = 0; k < o.gone; k += 32) {
+        const int t = k + lane < o.gone ? sh.gone[k + lane] : -1, line = (t + rows.lead) / 128;
+        for (unsigned here = __ballot_sync(0xffffffffu, t >= 0 && line >= from && line < to); here; here &= here - 1)
+          v = less(v, fixed(__ldg(p + __shfl_sync(0xffffffffu, t, __ffs(here) - 1))));
+      }
+      return v;
+    };
+    auto over_lanes = [](u64 v) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mine = plus(mine, __shfl_xor_sync(0xffffffffu, mine, d));
-    for (int k = 0; k < o.gone; k += 32) {
-      const int x = k + lane < o.gone ? sh.gone[k + lane] : -1;
-      unsigned here = __ballot_sync(0xffffffffu, x >= 0 && (x + rows.lead) / 128 >= line0 && (x + rows.lead) / 128 < line1);
-      for (; here; here &= here - 1) mine = less(mine, fixed(__ldg(p + __shfl_sync(0xffffffffu, x, __ffs(here) - 1))));
-    }
+      for (int d = 16; d > 0; d >>= 1) v = plus(v, __shfl_xor_sync(0xffffffffu, v, d));
+      return v;
+    };
+    const u64 mine = without(over_lanes(plus(plus(sum[0], sum[1]), plus(sum[2], sum[3]))), line0, line1);
     if (lane == 0) sh.warp[warp] = mine;
     __syncthreads();
     if (tid < C) {
-      u64 sum = 0;
+      u64 all = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum = plus(sum, sh.warp[w]);
-      put(at_rank(&sh.part[rank], tid), sum);
+      for (int w = 0; w < kWarps; ++w) all = plus(all, sh.warp[w]);
+      put(at_rank(&sh.part[rank], tid), all);
     }
     meet();
     u64 total = 0, before = 0;
@@ -305,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ Arg
       continue;
     }
     // ---------------------------------------------------------- the draw
-    u64 t = __umul64hi(chance(a.u_last[b]), total);
+    u64 t = __umul64hi(chance(u_last), total);
     if (t < before) return;
     t -= before;
     for (int w = 0; w < warp; ++w) {
@@ -313,13 +331,26 @@ __global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ Arg
       t -= sh.warp[w];
     }
     if (t >= sh.warp[warp]) return;
-    for (int l = line0; l < line1; ++l) {
+    int l = line0, end = line1;
+    float4 px, qx;  // of line l, where a group is one line
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const u64 here = without(over_lanes(sum[g]), line0 + g * deep, min(line0 + (g + 1) * deep, line1));
+      l = line0 + g * deep;
+      end = min(l + deep, line1);
+      px = x[g];
+      qx = y[g];
+      if (t < here) break;
+      t -= here;
+    }
+    for (; l < end; ++l) {
       const int x0 = 128 * l + 4 * lane;
-      float4 x, y = make_float4(0.f, 0.f, 0.f, 0.f);
-      load4(rows.p, rows, x0, true, &x);
-      if (o.refused > 0) load4(rows.q, rows, x0, rows.together, &y);
-      u64 r[4] = {rest(x.x, y.x, o.refused, sh.sigma), rest(x.y, y.y, o.refused, sh.sigma),
-                  rest(x.z, y.z, o.refused, sh.sigma), rest(x.w, y.w, o.refused, sh.sigma)};
+      if (deep > 1) {
+        load4(rows.p, rows, x0, true, &px);
+        if (o.refused > 0) load4(rows.q, rows, x0, rows.together, &qx);
+      }
+      u64 r[4] = {rest(px.x, qx.x, o.refused, sh.sigma), rest(px.y, qx.y, o.refused, sh.sigma),
+                  rest(px.z, qx.z, o.refused, sh.sigma), rest(px.w, qx.w, o.refused, sh.sigma)};
       for (int k = 0; k < o.gone; ++k) {
         const int g = sh.gone[k] + rows.lead - x0;
 #pragma unroll
@@ -365,8 +396,14 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
   if ((reinterpret_cast<uintptr_t>(d->target) | reinterpret_cast<uintptr_t>(d->draft)) & 3) return MOE_EINVAL;
   verify::Args a = {b->q_start, d->target, d->draft, b->T > 1 ? d->target_stride : d->V, b->T > 1 ? d->draft_stride : d->V,
                     d->token, d->parent, d->u, d->u_last, d->V, b->T, path, count, token, path_stride, err_dev};
-  const int ctas = verify::kMaxCtas;
+  // CTAs of a request: up to two an SM in all, and no more than have four lines of 128 values a warp to read
+  const int sms = 152, most = d->V / (128 * verify::kGroups * verify::kWarps) + 1;
+  int ctas = verify::kMaxCtas;
+  while (ctas > 1 && ((long long)b->B * ctas > 2 * sms || ctas >= 2 * most)) ctas /= 2;
   if ((long long)b->B * ctas > INT32_MAX) return MOE_EINVAL;
+  // clusters of sixteen are to be asked for
+  if (ctas > 8 && cudaFuncSetAttribute(verify::k_verify, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(b->B) * ctas);
   cfg.blockDim = dim3(verify::kThreads);
