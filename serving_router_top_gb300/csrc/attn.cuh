@@ -125,6 +125,11 @@ struct Cfg {
   // and 39.2 us, 128 columns 45.6, 41.4 and 40.8, 256 columns 36.9, 35.3 and 37.6; 16 windows of four over up
   // to 32768 keys 26.5, 24.6 and 24.0, 29.4, 27.0 and 26.2, 42.7, 39.8 and 39.0.  3 is within 3% of the best.
   static constexpr int V = !E4M3 && SLOT * H * 2 >= 65536 ? 2 : 3;
+  // Trees, whose units end in tiles that hide keys by their masks.  32 trees of up to 16 nodes over 60 to 8192 tokens, 128
+  // columns, with 2, 3, 4, 5, 6 and 8: 55.0, 48.6, 47.6, 48.6, 49.9 and 52.4 us; 64 columns 53.1, 46.7, 41.9, 40.1, 37.9 and
+  // 37.4; 16 of up to 32 over 512 to 32768, 256 columns, bf16 108.8, 112.3, 112.5, 104.8, 96.2 and 88.6, E4M3 150.0, 129.2,
+  // 122.7, 115.7, 111.1 and 111.8; up to 4 nodes, E4M3, 128 columns 38.8, 34.7, 32.8, 32.3, 32.1 and 33.9.
+  static constexpr int VT = !E4M3 && D == 128 ? 4 : 6;
   static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
 };
 
@@ -653,7 +658,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
   }
   pdl_wait();
 
-  constexpr int V = C::V;
+  constexpr int V = TREE ? C::VT : C::V;
   const int cap = cap_of(a.kv);
   const Plan plan = plan_run<V, C::THREADS, TREE>(a, cap, ms.plan);
   const uint32_t taddr = ms.taddr;
@@ -1044,37 +1049,39 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           const uint32_t to = tl + uint32_t(2 * C::SN + (piece & 1) * C::H * NR);  // O of this piece
           const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
           const bool whole = w.j >= whole0 && w.j < whole1;
-          // A tree's tile: bit i is set where the key is the unit's node i or above it, and the key's position less
-          // that of the tree's first, which a node's depth must be below by less than the window.
-          uint64_t nodes = 0;
-          int at_depth = 0;
+          // A tree's tile: bit x is set where this warp's row c0 + x sees the key.
+          uint32_t rows_see = 0;
           if constexpr (TREE) {
-            const int node = key - w.r.pos0;
             if (!whole && key < cap) {
-              if (node < 0) {
-                nodes = ~0ull;
-                at_depth = node;
-              } else if (node < w.r.n) {
-                const uint32_t* row = a.below + (long long)(w.r.s0 + node) * a.words;
-                const int from = w.s.i0 >> 5, sh = w.s.i0 & 31;
-                const uint32_t w0 = mask_word(row, a.words, from), w1 = mask_word(row, a.words, from + 1),
-                               w2 = mask_word(row, a.words, from + 2);
-                nodes = __funnelshift_r(w0, w1, sh) | uint64_t(__funnelshift_r(w1, w2, sh)) << 32;
-                if (a.window > 0) at_depth = a.depth[w.r.s0 + node];
+              const int node = key - w.r.pos0;
+              uint64_t nodes = ~0ull;  // of the unit's nodes: those that see the key, as far as the tree goes
+              int at_depth = node;     // the key's position less that of the tree's first
+              if (node >= 0) {
+                nodes = 0;
+                if (node < w.r.n) {
+                  const uint32_t* row = a.below + (long long)(w.r.s0 + node) * a.words;
+                  const int from = w.s.i0 >> 5, sh = w.s.i0 & 31;
+                  const uint32_t w0 = mask_word(row, a.words, from), w1 = mask_word(row, a.words, from + 1),
+                                 w2 = mask_word(row, a.words, from + 2);
+                  nodes = __funnelshift_r(w0, w1, sh) | uint64_t(__funnelshift_r(w1, w2, sh)) << 32;
+                  if (a.window > 0) at_depth = a.depth[w.r.s0 + node];
+                }
+              }
+#pragma unroll 1
+              for (int i = c0 / a.G, x = i * a.G - c0; x < CW; ++i, x += a.G) {
+                bool sees = nodes >> i & 1;
+                if (a.window > 0) sees = sees && at_depth > ms.deep[i * a.G] - a.window;
+                const int at = max(x, 0), n = min(x + a.G, 32) - at;  // its rows here
+                if (sees) rows_see |= (0xffffffffu >> (32 - n)) << at;
               }
             }
           }
           auto hide = [&](int x0, float* s) {
             if (whole) return;
             if constexpr (TREE) {
-              int i = (c0 + x0) / a.G, g = c0 + x0 - i * a.G;
 #pragma unroll
-              for (int x = 0; x < CK; ++x) {
-                bool sees = nodes >> i & 1;
-                if (a.window > 0) sees = sees && at_depth > ms.deep[c0 + x0 + x] - a.window;
-                if (!sees) s[x] = -INFINITY;
-                if (++g == a.G) g = 0, ++i;
-              }
+              for (int x = 0; x < CK; ++x)
+                if (!(rows_see >> (x0 + x) & 1)) s[x] = -INFINITY;
               return;
             }
             // rows are in the order of their tokens: rows from .. to - 1 see this key

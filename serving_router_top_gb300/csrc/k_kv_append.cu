@@ -8,87 +8,10 @@
 // fixed-point fraction of a turn: p times it, modulo 2^64, is the angle's
 // fraction of a turn with an error of at most p * 2^-65, and only its top bits
 // become a float, for sincospif.
-#include <limits.h>
-#include <math.h>
-
-#include "paged.cuh"
-
-struct moe_rope {
-  int rot, interleaved;
-  uint64_t* turns;  // device [rot/2]
-};
+#include "append.cuh"
 
 namespace moe {
 namespace append {
-
-constexpr int kMaxThreads = 256;
-constexpr int kMaxPairs = 128;  // rot <= 256
-
-struct Args {
-  KvView kv;
-  const uint64_t* turns;
-  int rot, interleaved;
-  const uint16_t *q, *k, *v;
-  uint16_t* qo;
-  long long qs, qos, ks, vs;
-  int Hq;
-  int32_t* err;
-  // moe_kv_append_norm alone
-  const int32_t* depth;  // of the rows in their trees, or null: they follow one another
-  int norm;
-  const uint16_t *wq, *wk;
-  float eps;
-};
-
-__device__ __forceinline__ void unpack8(uint4 u, float f[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float f[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Two values -> two E4M3 bytes (low byte first), to nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Eight columns of one head to where they belong: head < Hq is a query, then keys, then values.
-template <bool E4M3>
-__device__ __forceinline__ void store8(const Args& a, int t, int head, int col, const float f[8], int D, long long at,
-                                       float scale) {
-  if (head < a.Hq) {
-    *reinterpret_cast<uint4*>(a.qo + (long long)t * a.qos + head * D + col) = pack8(f);
-    return;
-  }
-  if (at < 0) return;
-  const bool is_v = head >= a.Hq + a.kv.Hkv;
-  const int h = head - a.Hq - (is_v ? a.kv.Hkv : 0);
-  uint8_t* dst = (is_v ? a.kv.v : a.kv.k) + at + h * a.kv.head_stride;
-  if (!E4M3) {
-    *reinterpret_cast<uint4*>(dst + 2 * col) = pack8(f);
-  } else {
-    // A division for each column, as the code is that of x / scale: times the scale's reciprocal, ties and the
-    // smallest scales go elsewhere.  4096 tokens of 32 + 2 x 4 heads of 128 take 17.9 us, with the reciprocal 16.6.
-    uint2 u;
-    u.x = e4m3x2(f[0] / scale, f[1] / scale) | (e4m3x2(f[2] / scale, f[3] / scale) << 16);
-    u.y = e4m3x2(f[4] / scale, f[5] / scale) | (e4m3x2(f[6] / scale, f[7] / scale) << 16);
-    *reinterpret_cast<uint2*>(dst + col) = u;
-  }
-}
 
 // One CTA per token; a thread takes kMine items of 16 columns of a head at a time (the two halves'
 // vectors of eight pairs, or two neighbours).  The first items' loads are on their way while the
@@ -98,18 +21,13 @@ __device__ __forceinline__ void store8(const Args& a, int t, int head, int col, 
 // one or three items a thread 32.0 and 28.4 us.
 constexpr int kMine = 2;
 
-// NORM: moe_kv_append_norm.  The lanes that hold a head's columns are neighbours (4, 8 or 16 of them, and a thread's
-// items all have the same columns), so its sum of squares is two to four exchanges between lanes, and the weights
-// are in registers before the request is found.  rsqrtf is within 2 units of fp32, as are the sum's roundings: far
-// below the one rounding that follows.
-template <bool E4M3, int D, bool NORM>
+template <bool E4M3, int D>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant__ Args a) {
   constexpr int kItems = D / 16;
   // cos, sin of each pair's angle: pair 8 j + i at [i][j], as the lanes of a head read them (64 bytes
   // apart, those met in four banks, and the prompt chunk took 32.2 us)
   __shared__ float2 cs[8][kMaxPairs / 8];
-  __shared__ int owner, position, begins;
-  __shared__ uint4 weights[NORM ? D / 4 : 1];
+  __shared__ int owner, position;
   pdl_trigger();
   pdl_wait();
   const int t = blockIdx.x, step = blockDim.x, pairs = a.rot / 2;
@@ -142,16 +60,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   Item x[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) fetch(threadIdx.x + i * step, x[i]);
-  int deep = 0;
-  if constexpr (NORM) {
-    if (a.norm)
-      for (int i = threadIdx.x; i < D / 4; i += step) {  // eight columns of the queries' weights, then of the keys'
-        const uint16_t* src = i < D / 8 ? a.wq : a.wk;
-        weights[i] = src ? reinterpret_cast<const uint4*>(src)[i % (D / 8)]
-                         : make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-      }
-    if (a.depth) deep = a.depth[t];
-  }
 
   // the request whose rows t is one of
   bool found = false;
@@ -159,7 +67,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
     const int s0 = a.kv.q_start[b], s1 = a.kv.q_start[b + 1], len = a.kv.kv_len[b];
     if (s0 <= t && t < s1) {
       owner = b;
-      if (NORM) begins = s0;
       position = int(min(max((long long)len - (s1 - t), (long long)INT_MIN), (long long)INT_MAX));
       found = true;
     }
@@ -170,14 +77,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   int id = -1;
   if (pos >= 0 && (pos >> a.kv.page_shift) < a.kv.table_stride)
     id = a.kv.page_table[(long long)b * a.kv.table_stride + (pos >> a.kv.page_shift)];
-  // the angles' position: a node's place is not it
-  int turned = pos;
-  if constexpr (NORM) {
-    if (a.depth) turned = int(min(max((long long)pos - (t - begins) + deep, (long long)INT_MIN), (long long)INT_MAX));
-  }
   for (int i = threadIdx.x; i < pairs; i += step) {
     // a signed fraction of a turn in [-1/2, 1/2); sincospif takes half turns
-    const long long frac = (long long)(uint64_t(int64_t(turned)) * a.turns[i]);
+    const long long frac = (long long)(uint64_t(int64_t(pos)) * a.turns[i]);
     float c, s;
     sincospif(float(frac) * 0x1p-63f, &s, &c);
     cs[i & 7][i >> 3] = make_float2(c, s);
@@ -193,23 +95,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
     float f0[8], f1[8];
     unpack8(x.v0, f0);
     unpack8(x.v1, f1);
-    if constexpr (NORM) {
-      if (a.norm && x.head < a.Hq + a.kv.Hkv) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], sum));
-        const unsigned mates = ((1u << kItems) - 1) << ((threadIdx.x & 31) / kItems * kItems);
-#pragma unroll
-        for (int o = 1; o < kItems; o <<= 1) sum += __shfl_xor_sync(mates, sum, o);
-        const float inv = rsqrtf(sum * (1.f / D) + a.eps);
-        const int z = x.head >= a.Hq ? D / 8 : 0;
-        float w0[8], w1[8];
-        unpack8(weights[z + x.c0 / 8], w0);
-        unpack8(weights[z + x.c1 / 8], w1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f0[i] *= inv * w0[i], f1[i] *= inv * w1[i];
-      }
-    }
     if (x.pair >= 0) {
       if (!a.interleaved) {
 #pragma unroll
@@ -243,14 +128,14 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_append(const __grid_constant
   }
 }
 
-template <bool E4M3, bool NORM>
+template <bool E4M3>
 cudaError_t launch(int D, int T, cudaStream_t s, const Args& a) {
   const int n = (a.Hq + 2 * a.kv.Hkv) * (D / 16), each = (n + kMine - 1) / kMine;
   const dim3 block(each >= kMaxThreads ? kMaxThreads : (each + 31) / 32 * 32);
   switch (D) {
-    case 64: return launch_pdl(k_kv_append<E4M3, 64, NORM>, dim3(T), block, 0, s, a);
-    case 128: return launch_pdl(k_kv_append<E4M3, 128, NORM>, dim3(T), block, 0, s, a);
-    default: return launch_pdl(k_kv_append<E4M3, 256, NORM>, dim3(T), block, 0, s, a);
+    case 64: return launch_pdl(k_kv_append<E4M3, 64>, dim3(T), block, 0, s, a);
+    case 128: return launch_pdl(k_kv_append<E4M3, 128>, dim3(T), block, 0, s, a);
+    default: return launch_pdl(k_kv_append<E4M3, 256>, dim3(T), block, 0, s, a);
   }
 }
 
@@ -317,44 +202,6 @@ extern "C" int moe_rope_destroy(moe_rope* r) {
   return MOE_OK;
 }
 
-namespace moe {
-namespace append {
-
-// The checks of both calls; `a` is filled and `work` tells whether there is anything to launch.
-int checked(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q, long long q_stride,
-            uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k, long long k_stride, const uint16_t* v,
-            long long v_stride, int32_t* err_dev, Args* out, bool* work) {
-  Args& a = *out;
-  *work = false;
-  const int rc = kv_view(kv, b, &a.kv);
-  if (rc) return rc;
-  const int T = b->T, D = kv->D;
-  if (Hq < 0 || Hq > 1024 * kMaxGroup || (Hq > 0) != (q != nullptr) || (rope && rope->rot > D)) return MOE_EINVAL;
-  if (T == 0 || b->B == 0) return MOE_OK;
-  if (q && (!rows_ok(q, q_stride, T, (long long)Hq * D) || !rows_ok(q_out, q_out_stride, T, (long long)Hq * D)))
-    return MOE_EINVAL;
-  if (!rows_ok(k, k_stride, T, (long long)kv->Hkv * D) || !rows_ok(v, v_stride, T, (long long)kv->Hkv * D))
-    return MOE_EINVAL;
-  a.turns = rope ? rope->turns : nullptr;
-  a.rot = rope ? rope->rot : 0;
-  a.interleaved = rope ? rope->interleaved : 0;
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.qo = q_out;
-  a.qs = q_stride;
-  a.qos = q_out_stride;
-  a.ks = k_stride;
-  a.vs = v_stride;
-  a.Hq = Hq;
-  a.err = err_dev;
-  *work = true;
-  return MOE_OK;
-}
-
-}  // namespace append
-}  // namespace moe
-
 extern "C" int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_rope* rope, const uint16_t* q,
                              long long q_stride, uint16_t* q_out, long long q_out_stride, int Hq, const uint16_t* k,
                              long long k_stride, const uint16_t* v, long long v_stride, int32_t* err_dev,
@@ -365,33 +212,7 @@ extern "C" int moe_kv_append(const moe_kv_pages* kv, const moe_kv_batch* b, cons
   const int rc = append::checked(kv, b, rope, q, q_stride, q_out, q_out_stride, Hq, k, k_stride, v, v_stride, err_dev, &a, &work);
   if (rc || !work) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return (kv->e4m3 ? append::launch<true, false>(kv->D, b->T, s, a) : append::launch<false, false>(kv->D, b->T, s, a)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ECUDA;
-}
-
-extern "C" int moe_kv_append_norm(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const moe_rope* rope,
-                                  const moe_head_norm* norm, const uint16_t* q, long long q_stride, uint16_t* q_out,
-                                  long long q_out_stride, int Hq, const uint16_t* k, long long k_stride, const uint16_t* v,
-                                  long long v_stride, int32_t* err_dev, moe_stream_t stream) {
-  using namespace moe;
-  append::Args a = {};
-  if (norm && (!(norm->eps > 0.f) || !isfinite(norm->eps) || (reinterpret_cast<uintptr_t>(norm->w_q) & 15) ||
-               (reinterpret_cast<uintptr_t>(norm->w_k) & 15)))
-    return MOE_EINVAL;
-  bool work;
-  const int rc = append::checked(kv, b, rope, q, q_stride, q_out, q_out_stride, Hq, k, k_stride, v, v_stride, err_dev, &a, &work);
-  if (rc || !work) return rc;
-  if (tree && !tree->depth) return MOE_EINVAL;
-  a.depth = tree ? tree->depth : nullptr;
-  a.norm = norm != nullptr;
-  if (norm) {
-    a.wq = norm->w_q;
-    a.wk = norm->w_k;
-    a.eps = norm->eps;
-  }
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return (kv->e4m3 ? append::launch<true, true>(kv->D, b->T, s, a) : append::launch<false, true>(kv->D, b->T, s, a)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ECUDA;
+  if ((kv->e4m3 ? append::launch<true>(kv->D, b->T, s, a) : append::launch<false>(kv->D, b->T, s, a)) != cudaSuccess)
+    return MOE_ECUDA;
+  return MOE_OK;
 }

@@ -24,14 +24,14 @@ struct Args {
 };
 
 // ------------------------------------------------------------------ kept nodes
-// A CTA per request and pool.  A thread moves one 16-byte column of a head through all kept nodes in their order,
-// kAhead loads before their stores: as kept indices rise, path[d] >= d, and no place is written before the thread has
-// read it.
-constexpr int kThreads = 256, kSteps = 256, kAhead = 8, kCompactPerSm = 4;
+// A CTA takes a request in several pools.  A thread moves 16-byte columns of a head through all kept nodes in their order,
+// kAhead loads of kCols columns before their stores: as kept indices rise, path[d] >= d, and no place is written before
+// the thread has read it.  Nodes that are kept in their places are the path's first.
+constexpr int kThreads = 256, kSteps = 256, kAhead = 4, kCols = 3, kCompactPerSm = 4;
 
 __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Args a) {
   __shared__ long long from[kSteps], to[kSteps];
-  __shared__ int bad;
+  __shared__ int bad, moved;  // the first index that does not rise; the first that moves
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Ar
   };
   int kept = want;
   for (int d0 = 0; d0 < kept; d0 += kSteps) {
-    if (tid == 0) bad = want;
+    if (tid == 0) bad = moved = want;
     __syncthreads();
     const int d = d0 + tid;
     int node = 0;
@@ -62,27 +62,38 @@ __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Ar
     }
     __syncthreads();
     kept = min(kept, bad);
-    if (d < kept) {
-      from[tid] = to[tid] = -1;
-      if (node != d) {
-        from[tid] = place(base + node);
-        to[tid] = place(base + d);
-        if (from[tid] < 0 || to[tid] < 0) set_error(a.err, MOE_ERANGE);
-      }
+    if (d < kept && node != d) {
+      atomicMin(&moved, d);
+      const long long at = place(base + node), into = place(base + d);
+      if (at < 0 || into < 0) set_error(a.err, MOE_ERANGE);
+      from[tid] = at < 0 || into < 0 ? -1 : at;
+      to[tid] = into;
     }
     __syncthreads();
-    const int steps = min(kept - d0, kSteps);
-    for (int c = tid; c < pools * cols; c += kThreads) {
-      const int pool = c / cols, head = (c - pool * cols) / a.vecs;
-      uint8_t* col = a.pool[pool0 + pool] + head * kv.head_stride + (c - pool * cols - head * a.vecs) * 16;
-      for (int e0 = 0; e0 < steps; e0 += kAhead) {
-        uint4 x[kAhead];
+    const int step0 = max(moved - d0, 0), steps = min(kept - d0, kSteps);
+    for (int c0 = tid; c0 < pools * cols; c0 += kCols * kThreads) {
+      uint8_t* col[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int c = c0 + i * kThreads, pool = c / cols, head = (c - pool * cols) / a.vecs;
+        col[i] = c < pools * cols ? a.pool[pool0 + pool] + head * kv.head_stride + (c - pool * cols - head * a.vecs) * 16 : nullptr;
+      }
+      for (int e0 = step0; e0 < steps; e0 += kAhead) {
+        uint4 x[kCols][kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e)
-          if (e0 + e < steps && from[e0 + e] >= 0 && to[e0 + e] >= 0) x[e] = *reinterpret_cast<const uint4*>(col + from[e0 + e]);
+          if (e0 + e < steps && from[e0 + e] >= 0) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if (col[i]) x[i][e] = *reinterpret_cast<const uint4*>(col[i] + from[e0 + e]);
+          }
 #pragma unroll
         for (int e = 0; e < kAhead; ++e)
-          if (e0 + e < steps && from[e0 + e] >= 0 && to[e0 + e] >= 0) *reinterpret_cast<uint4*>(col + to[e0 + e]) = x[e];
+          if (e0 + e < steps && from[e0 + e] >= 0) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if (col[i]) *reinterpret_cast<uint4*>(col[i] + to[e0 + e]) = x[i][e];
+          }
       }
     }
     __syncthreads();

@@ -118,7 +118,8 @@ __device__ __forceinline__ u64 rest(float p, float q, int refused, const u64* si
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ Args a) {
+template <bool DRAWN, int PER_SM>
+__global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_constant__ Args a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = int(my_rank()), C = int(ranks()), b = blockIdx.x / C;
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ 
         if (x < 0 || x >= a.V) x = -1;
         if (up >= 0 && x >= 0) {
           p = fixed(a.target[(s0 + up) * a.ts + x]);
-          if (a.draft) q = fixed(a.draft[(s0 + up) * a.ds + x]);
+          if (DRAWN) q = fixed(a.draft[(s0 + up) * a.ds + x]);
         }
       }
       sh.parent[i] = short(up);
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ 
             seen = c;
             u64 r = sh.p[c];
             bool keep;
-            if (a.draft) {
+            if constexpr (DRAWN) {
               const u64 f = sh.q[c];
               if (refused > 0) r = less(r, f);
               for (int k = 1; k < refused; ++k) r = less(r, times(sh.sigma[k], f));
@@ -217,12 +218,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ 
             }
             if (keep) {
               arrive_at(c);
-            } else if (a.draft) {
+            } else if (DRAWN) {
               ++refused;
               break;
             }
           }
-          o = {s0 + node, refused, gone, a.draft ? next_child() < 0 : 1};
+          o = {s0 + node, refused, gone, DRAWN ? next_child() < 0 : 1};
           if (lane == 0) a.count[b] = kept;
         } else if (lane == 0) {
           a.count[b] = 0;
@@ -240,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ 
       meet();
     }
     Order o = sh.order;
+    if (!DRAWN) o.refused = 0;
+    else o.gone = 0;
     if (o.row < 0) return;
     if (own_row) o.refused = o.gone = 0;
 
@@ -331,26 +334,32 @@ __global__ void __launch_bounds__(kThreads, 2) k_verify(const __grid_constant__ 
       t -= sh.warp[w];
     }
     if (t >= sh.warp[warp]) return;
-    int l = line0, end = line1;
-    float4 px, qx;  // of line l, where a group is one line
+    int l0 = line0, end = line1;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const u64 here = without(over_lanes(sum[g]), line0 + g * deep, min(line0 + (g + 1) * deep, line1));
-      l = line0 + g * deep;
-      end = min(l + deep, line1);
-      px = x[g];
-      qx = y[g];
+      l0 = line0 + g * deep;
+      end = min(l0 + deep, line1);
+      if (deep == 1) x[0] = x[g], y[0] = y[g];
       if (t < here) break;
       t -= here;
     }
-    for (; l < end; ++l) {
-      const int x0 = 128 * l + 4 * lane;
-      if (deep > 1) {
-        load4(rows.p, rows, x0, true, &px);
-        if (o.refused > 0) load4(rows.q, rows, x0, rows.together, &qx);
+    for (int l = l0; l < end; ++l) {
+      const int at = (l - l0) % kGroups;
+      if (deep > 1 && at == 0) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (l + g >= end) break;
+          load4(rows.p, rows, 128 * (l + g) + 4 * lane, true, &x[g]);
+          if (o.refused > 0) load4(rows.q, rows, 128 * (l + g) + 4 * lane, rows.together, &y[g]);
+        }
+      } else if (at > 0) {  // the next one read
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) x[g - 1] = x[g], y[g - 1] = y[g];
       }
-      u64 r[4] = {rest(px.x, qx.x, o.refused, sh.sigma), rest(px.y, qx.y, o.refused, sh.sigma),
-                  rest(px.z, qx.z, o.refused, sh.sigma), rest(px.w, qx.w, o.refused, sh.sigma)};
+      const int x0 = 128 * l + 4 * lane;
+      u64 r[4] = {rest(x[0].x, y[0].x, o.refused, sh.sigma), rest(x[0].y, y[0].y, o.refused, sh.sigma),
+                  rest(x[0].z, y[0].z, o.refused, sh.sigma), rest(x[0].w, y[0].w, o.refused, sh.sigma)};
       for (int k = 0; k < o.gone; ++k) {
         const int g = sh.gone[k] + rows.lead - x0;
 #pragma unroll
@@ -401,8 +410,11 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
   int ctas = verify::kMaxCtas;
   while (ctas > 1 && ((long long)b->B * ctas > 2 * sms || ctas >= 2 * most)) ctas /= 2;
   if ((long long)b->B * ctas > INT32_MAX) return MOE_EINVAL;
+  const bool alone = (long long)b->B * ctas <= sms;
+  auto* kernel = d->draft ? alone ? verify::k_verify<true, 1> : verify::k_verify<true, 2>
+                          : alone ? verify::k_verify<false, 1> : verify::k_verify<false, 2>;
   // clusters of sixteen are to be asked for
-  if (ctas > 8 && cudaFuncSetAttribute(verify::k_verify, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (ctas > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return MOE_ECUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(b->B) * ctas);
@@ -415,5 +427,5 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
   attr[1].val.clusterDim = {unsigned(ctas), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify::k_verify, a) == cudaSuccess ? MOE_OK : MOE_ECUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
