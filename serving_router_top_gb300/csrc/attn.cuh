@@ -1476,6 +1476,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_many(const __grid_constan
 // applies, from the first size on: 8 requests of 9 tokens of 8 heads (72 rows) over 4000 E4M3 keys, 128
 // columns 28.6 us (33.8 in 64-row tiles), 64 columns 21.3 (25.8).  A tile holds the heads of whole tokens.
 constexpr int kChunkRows = 256;
+constexpr int kWideRows = 128;  // of attn_wide.cuh
 inline int row_tile(int D, int G, int n) {
   return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || D > 128 ? 64 : kChunkRows;
 }

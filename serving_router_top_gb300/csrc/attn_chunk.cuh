@@ -95,14 +95,15 @@ __device__ __forceinline__ void turn4(float (&v)[16], int lane) {
       }
 }
 
-// Bit j of seen: node i sees key key0 + j.
+// Bit j of seen: node i sees key key0 + j, of 32 WORDS keys.
+template <int WORDS>
 __device__ __forceinline__ void tree_keys(const Args& a, const Req& r, int i, int key0, int cap, uint32_t* seen) {
   const uint32_t* row = a.above + (long long)(r.s0 + i) * a.words;
   const int node0 = key0 - r.pos0, deep = a.window > 0 ? a.depth[r.s0 + i] : 0;
   const int from = a.window > 0 ? r.pos0 + deep - a.window + 1 - key0 : INT_MIN;  // of the keys before the tree
   uint32_t low = mask_word(row, a.words, node0 >> 5);
 #pragma unroll
-  for (int k = 0; k < kKeys / 32; ++k) {
+  for (int k = 0; k < WORDS; ++k) {
     const uint32_t high = mask_word(row, a.words, (node0 >> 5) + k + 1);
     uint32_t m = __funnelshift_r(low, high, node0 & 31);
     low = high;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1) k_chunk(const __grid
             f = factor > 0.f ? factor : 1.f;
             if constexpr (TREE) {
               uint32_t seen[kKeys / 32];  // of the tile's keys, by this row
-              tree_keys(a, w.r, pos - w.r.pos0, key0, cap, seen);
+              tree_keys<kKeys / 32>(a, w.r, pos - w.r.pos0, key0, cap, seen);
 #pragma unroll
               for (int i = 0; i < kKeys; ++i) s[i] = seen[i / 32] >> (i % 32) & 1 ? s[i] * once : -INFINITY;
             } else {

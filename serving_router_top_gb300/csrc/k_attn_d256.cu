@@ -34,6 +34,7 @@ int opt_in_d256() {
                  as_before(k_join<256, 16>) ||
                  as_before(k_join<256, 32>) ||
                  as_before(k_join<256, 64>) ||
+                 as_before(k_join<256, 128>) ||
                  as_before(k_join_many<256>)
              ? MOE_ECUDA
              : MOE_OK;
@@ -46,7 +47,8 @@ int launch_join<256>(const Args& a, int nr, bool many, int ctas, cudaStream_t s)
   if (many) e = launch_pdl(k_join_many<256>, dim3(ctas, a.G < 16 ? a.G : 16), threads, 0, s, a);
   else if (nr == 16) e = launch_pdl(k_join<256, 16>, dim3(ctas, join_y(16)), threads, 0, s, a);
   else if (nr == 32) e = launch_pdl(k_join<256, 32>, dim3(ctas, join_y(32)), threads, 0, s, a);
-  else e = launch_pdl(k_join<256, 64>, dim3(ctas, join_y(64)), threads, 0, s, a);
+  else if (nr == 64) e = launch_pdl(k_join<256, 64>, dim3(ctas, join_y(64)), threads, 0, s, a);
+  else e = launch_pdl(k_join<256, 128>, dim3(ctas, join_y(128)), threads, 0, s, a);
   return e == cudaSuccess ? MOE_OK : MOE_ECUDA;
 }
 

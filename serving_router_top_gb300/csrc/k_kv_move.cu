@@ -25,11 +25,14 @@ struct Args {
 
 // ------------------------------------------------------------------ kept nodes
 // A CTA takes a request in several pools.  A thread moves 16-byte columns of a head through all kept nodes in their order,
-// kAhead loads of kCols columns before their stores: as kept indices rise, path[d] >= d, and no place is written before
-// the thread has read it.  Nodes that are kept in their places are the path's first.
-constexpr int kThreads = 256, kSteps = 256, kAhead = 4, kCols = 3, kCompactPerSm = 4;
+// kAhead loads before their stores: as kept indices rise, path[d] >= d, and no place is written before the thread has read
+// it.  Nodes that are kept in their places are the path's first.
+//
+// 64 trees' up to six nodes in 24 layers, 28 MB in rows of 256 bytes: 8.8 us; up to twelve, 66 MB, 15.9 us, 4.2 TB/s: rows
+// that lie far apart.  With two, three and four columns a thread at a time 9.0 to 10.4 us, and a CTA for each pool 14.0.
+constexpr int kThreads = 256, kSteps = 256, kAhead = 8, kCompactPerSm = 4;
 
-__global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, kCompactPerSm) k_compact(const __grid_constant__ Args a) {
   __shared__ long long from[kSteps], to[kSteps];
   __shared__ int bad, moved;  // the first index that does not rise; the first that moves
   pdl_trigger();
@@ -71,29 +74,17 @@ __global__ void __launch_bounds__(kThreads) k_compact(const __grid_constant__ Ar
     }
     __syncthreads();
     const int step0 = max(moved - d0, 0), steps = min(kept - d0, kSteps);
-    for (int c0 = tid; c0 < pools * cols; c0 += kCols * kThreads) {
-      uint8_t* col[kCols];
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        const int c = c0 + i * kThreads, pool = c / cols, head = (c - pool * cols) / a.vecs;
-        col[i] = c < pools * cols ? a.pool[pool0 + pool] + head * kv.head_stride + (c - pool * cols - head * a.vecs) * 16 : nullptr;
-      }
+    for (int c = tid; c < pools * cols; c += kThreads) {
+      const int pool = c / cols, head = (c - pool * cols) / a.vecs;
+      uint8_t* col = a.pool[pool0 + pool] + head * kv.head_stride + (c - pool * cols - head * a.vecs) * 16;
       for (int e0 = step0; e0 < steps; e0 += kAhead) {
-        uint4 x[kCols][kAhead];
+        uint4 x[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e)
-          if (e0 + e < steps && from[e0 + e] >= 0) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i)
-              if (col[i]) x[i][e] = *reinterpret_cast<const uint4*>(col[i] + from[e0 + e]);
-          }
+          if (e0 + e < steps && from[e0 + e] >= 0) x[e] = *reinterpret_cast<const uint4*>(col + from[e0 + e]);
 #pragma unroll
         for (int e = 0; e < kAhead; ++e)
-          if (e0 + e < steps && from[e0 + e] >= 0) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i)
-              if (col[i]) *reinterpret_cast<uint4*>(col[i] + to[e0 + e]) = x[i][e];
-          }
+          if (e0 + e < steps && from[e0 + e] >= 0) *reinterpret_cast<uint4*>(col + to[e0 + e]) = x[e];
       }
     }
     __syncthreads();
@@ -186,7 +177,7 @@ extern "C" int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch*
   a.len = kv_len_out;
   a.err = err_dev;
   // CTAs for one turn of the GPU's 152 SMs, each over several pools: the chain before the first row is paid once
-  const int y = (152 * move::kCompactPerSm + b->B - 1) / b->B;
+  const int y = 152 * move::kCompactPerSm > b->B ? 152 * move::kCompactPerSm / b->B : 1;
   return move::over_layers(move::k_compact, a, kv, L, unsigned(b->B), y, move::kThreads, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -65,6 +65,11 @@ CASES = [
     (128, 2, 2, 16, [300, 20], [10, 10], 3, 1),            # each node itself alone
     (128, 1, 4, 1, [70], [9], 3, 0),                       # pages of one token
     (64, 1, 8, 2, [150], [30], 4, 0),
+    (256, 1, 3, 16, [500, 200], [100, 40], 9, 0),          # one 128-row tile of 42 tokens
+    (256, 2, 64, 32, [300, 7], [3, 7], 2, 0),              # two tokens a tile
+    (256, 1, 8, 64, [1000, 256, 129], [256, 256, 9], 20, 0),
+    (256, 2, 8, 16, [900, 300, 40], [40, 33, 20], 5, 100),
+    (256, 1, 8, 1, [140], [20], 1, 0),                     # pages of one token
 ]
 
 
@@ -89,7 +94,7 @@ def test_layouts_strides_and_rows_of_nobody(layout):
     check(o, ref, tol)
 
 
-@pytest.mark.parametrize("D,G,n", [(128, 2, 6), (128, 8, 40), (64, 8, 30), (256, 4, 10)])
+@pytest.mark.parametrize("D,G,n", [(128, 2, 6), (128, 8, 40), (64, 8, 30), (256, 4, 10), (256, 8, 40)])
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_what_a_node_does_not_see_may_be_anything(D, G, n, e4m3):
     """Siblings' keys and values that are NaN or infinite reach only their own descendants."""
@@ -111,7 +116,7 @@ def test_what_a_node_does_not_see_may_be_anything(D, G, n, e4m3):
     assert torch.isnan(o[~keep]).all()
 
 
-@pytest.mark.parametrize("D,G,n", [(128, 2, 6), (128, 8, 40), (64, 2, 7)])
+@pytest.mark.parametrize("D,G,n", [(128, 2, 6), (128, 8, 40), (64, 2, 7), (256, 8, 40)])
 def test_infinite_values_reach_the_nodes_that_see_them(D, G, n):
     P = Paged([150 + n], [n], 1, D, 16, seed=3)
     parents = random_parents(n, 2, 1)
@@ -142,9 +147,9 @@ def test_forests_see_the_prefix():
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
-@pytest.mark.parametrize("n,G", [(6, 4), (40, 8)])
-def test_scales(scale, n, G):
-    P = Paged([200], [n], 1, 128, 16, seed=6)
+@pytest.mark.parametrize("n,G,D", [(6, 4, 128), (40, 8, 128), (40, 8, 256)])
+def test_scales(scale, n, G, D):
+    P = Paged([200], [n], 1, D, 16, seed=6)
     o, ref, tol, err = attend(P, [random_parents(n, 4, 2)], G, scale=scale)
     assert err == 0
     check(o, ref, tol)
@@ -170,8 +175,13 @@ def test_long_contexts_and_many_requests():
     o, ref, tol, err = attend(P, [random_parents(n, 4, n) for n in ns], 4)
     assert err == 0
     check(o, ref, tol)
-    P = Paged([9000], [12], 1, 64, 64, seed=5)
-    o, ref, tol, err = attend(P, [random_parents(12, 4, 0)], 8)
+    for D in (64, 256):
+        P = Paged([9000], [12], 1, D, 64, seed=5)
+        o, ref, tol, err = attend(P, [random_parents(12, 4, 0)], 8)
+        assert err == 0
+        check(o, ref, tol)
+    P = Paged([70000, 30000], [30, 9], 1, 256, 64, seed=5)  # rings and schedules that go round
+    o, ref, tol, err = attend(P, [random_parents(30, 4, 0), random_parents(9, 2, 0)], 8)
     assert err == 0
     check(o, ref, tol)
 
@@ -233,7 +243,8 @@ def test_a_captured_call_follows_its_tensors(n, G):
 
 
 @pytest.mark.parametrize("stage", [1, 2, 3])
-@pytest.mark.parametrize("D,G,n,e4m3", [(128, 4, 4, False), (256, 4, 16, True), (128, 8, 40, False), (64, 8, 40, True)])
+@pytest.mark.parametrize("D,G,n,e4m3", [(128, 4, 4, False), (256, 4, 16, True), (128, 8, 40, False), (64, 8, 40, True),
+                                        (256, 8, 40, False), (256, 8, 40, True)])
 def test_waits_that_run_out_are_reported(stage, D, G, n, e4m3):
     # a slot is waited for from a run's fourth to eighth tile on: 1172 tiles are in at most 304 runs
     P = Paged([60000, 50001, 40100], [n] * 3, 1, D, 64, e4m3=e4m3, seed=1)
