@@ -1,4 +1,4 @@
-// Attention of drafted trees of more than 64 rows a key head with 256 columns: rows on the lanes, as in attn_chunk.cuh.
+// Attention of drafted trees of more than 32 rows a key head with 256 columns: rows on the lanes, as in attn_chunk.cuh.
 //
 //   S = Q K^T      [128 rows x 128 keys]   (M = rows)
 //   O += P V       [128 rows x 256]        P from tensor memory
@@ -12,7 +12,12 @@
 // E4M3 tiles come as they are into a ring of their own, and eight warps turn them into bf16, exactly.
 //
 // attn.cuh's form takes these rows 64 at a time, reads keys and values as often, and has no slot to spare beside a key
-// and a value tile.
+// and a value tile.  16 trees of up to 32 nodes of 8 heads over 512 to 32768 tokens (22 rows' worth of nodes on average):
+// bf16 63.7 us, E4M3 69.4 with the join; in 64-row tiles 96 and 111.
+//
+// What bounds it: memory's way.  Without the conversions E4M3 takes 61 us, without exponentials or maxima, or with half the
+// products, what it takes with them; bf16 over pages that the L2 holds 50.4 (of 63.7).  The join is 8 to 12 us of either:
+// each of 152 runs leaves one or two pieces of 128 x 256 sums.
 #pragma once
 
 #include "attn_chunk.cuh"
@@ -52,7 +57,9 @@ struct Cfg {
   static_assert(NS * SLOT + NRAW * RAW + QBYTES + kMisc <= kSmem, "shared memory of an SM");
 };
 constexpr int kSoftThreads = 256;
-constexpr int V = 3;  // what a unit costs beside its tiles, in tiles
+// What a unit costs beside its tiles, in tiles: 2, 3, 5 and 8 give 71.4, 69.3, 70.5 and 72.9 us (E4M3), 68.9, 63.8, 69.1 and
+// 65.7 (bf16).  Four converting warps 88.8 us, eight 69.3.
+constexpr int V = 3;
 
 template <bool E4M3>
 __global__ void __launch_bounds__(Cfg<E4M3>::THREADS, 1) k_wide(const __grid_constant__ Args a) {
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(Cfg<E4M3>::THREADS, 1) k_wide(const __grid_con
     Walk<V, true> w;
     w.start(a, cap, ms.plan.first, plan.x1 - plan.x0);
     if (warp >= C::MMA) {
-      if (E4M3) leave_registers<72>();
+      if (E4M3) leave_registers<80>();
       if (warp == C::MMA) {
         // -------------------------------------------------------- tensor cores
         // D f32, A and B bf16, M = N = 128; S: both K-major; O: B (V) MN-major
@@ -262,8 +269,8 @@ __global__ void __launch_bounds__(Cfg<E4M3>::THREADS, 1) k_wide(const __grid_con
         }
       }
     } else {
-      static_assert(!E4M3 || kSoftThreads * 128 + (C::THREADS - kSoftThreads) * 72 <= C::THREADS * 96, "registers of the launch");
-      if (E4M3) take_registers<128>();
+      static_assert(!E4M3 || kSoftThreads * 120 + (C::THREADS - kSoftThreads) * 80 <= C::THREADS * 96, "registers of the launch");
+      if (E4M3) take_registers<120>();
       // -------------------------------------------------------- softmax, two threads a row
       constexpr int HK = kKeys / 2;
       const int half = warp >> 2, quad = warp & 3, krow = quad * 32 + lane;  // half of the keys, and of O's columns; row

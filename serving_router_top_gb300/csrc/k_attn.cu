@@ -139,7 +139,10 @@ int attend(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, 
   const long long width = (long long)Hq * kv->D;
   if (!rows_ok(q, q_stride, T, width) || !rows_ok(o, o_stride, T, width)) return MOE_EINVAL;
   int nr = attn::row_tile(kv->D, Hq / kv->Hkv, b->max_n > 1 ? b->max_n : 1);
-  if (tree && kv->D == 256 && b->max_n > 64 / (Hq / kv->Hkv)) nr = attn::kWideRows;
+  // Trees with more than 32 rows a key head of 256 columns go to attn_wide.cuh: 16 trees of 8 nodes of 8 heads (64 rows) over
+  // 512 to 32768 tokens 54.5 us in bf16 and 49.7 in E4M3, in 64-row tiles of attn.cuh 58.5 and 61.0; one of them over 717
+  // tokens 14.2 and 13.7.
+  if (tree && kv->D == 256 && b->max_n > 32 / (Hq / kv->Hkv)) nr = attn::kWideRows;
   a.o = o;
   a.os = T > 1 ? o_stride : width;
   a.q = q;

@@ -9,14 +9,12 @@ int launch_tree_d256(const Args& a, int e4m3, int nr, int sms, cudaStream_t s) {
     switch (nr) {
       case 16: return launch_one<256, 16, true, true>(a, sms, s);
       case 32: return launch_one<256, 32, true, true>(a, sms, s);
-      case 64: return launch_one<256, 64, true, true>(a, sms, s);
       default: return wide::launch<true>(a, sms, s);
     }
   } else {
     switch (nr) {
       case 16: return launch_one<256, 16, false, true>(a, sms, s);
       case 32: return launch_one<256, 32, false, true>(a, sms, s);
-      case 64: return launch_one<256, 64, false, true>(a, sms, s);
       default: return wide::launch<false>(a, sms, s);
     }
   }
@@ -25,10 +23,8 @@ int launch_tree_d256(const Args& a, int e4m3, int nr, int sms, cudaStream_t s) {
 int opt_in_tree_d256() {
   return opt_in<256, 16, false, true>() ||
                  opt_in<256, 32, false, true>() ||
-                 opt_in<256, 64, false, true>() ||
                  opt_in<256, 16, true, true>() ||
                  opt_in<256, 32, true, true>() ||
-                 opt_in<256, 64, true, true>() ||
                  wide::opt_in<false>() ||
                  wide::opt_in<true>()
              ? MOE_ECUDA
