@@ -1049,36 +1049,50 @@ __global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::O
           const uint32_t to = tl + uint32_t(2 * C::SN + (piece & 1) * C::H * NR);  // O of this piece
           const int key0 = (w.s.tile0 + w.j) * kKeys, key = key0 + krow;
           const bool whole = w.j >= whole0 && w.j < whole1;
-          // A tree's tile: bit x is set where this warp's row c0 + x sees the key.
-          uint32_t rows_see = 0;
+          // A tree's tile: bit x is set where this warp's row c0 + x sees the key.  Most of a tile's warps have keys that every
+          // row sees or none does, and a walk over the rows' nodes is left to the others.
+          uint32_t rows_see = 0xffffffffu;
+          bool mixed_warp = false;
           if constexpr (TREE) {
-            if (!whole && key < cap) {
+            if (!whole) {
               const int node = key - w.r.pos0;
-              uint64_t nodes = ~0ull;  // of the unit's nodes: those that see the key, as far as the tree goes
-              int at_depth = node;     // the key's position less that of the tree's first
-              if (node >= 0) {
-                nodes = 0;
-                if (node < w.r.n) {
+              // the key is seen by rows less deep than this, as far as the window goes
+              const int below = a.window <= 0 ? INT_MAX : a.window + (node < 0 ? node : node < w.r.n ? a.depth[w.r.s0 + node] : 0);
+              const bool none = key >= min(cap, w.s.hi) || below <= 0, all = !none && node < 0 && below > w.s.i1;
+              if (none) rows_see = 0;
+              mixed_warp = !__all_sync(0xffffffffu, all);
+              if (!__all_sync(0xffffffffu, none || all)) {
+                uint64_t nodes = none ? 0 : ~0ull;  // of the unit's nodes: those that the key is or is above of
+                if (!none && node >= 0) {
                   const uint32_t* row = a.below + (long long)(w.r.s0 + node) * a.words;
                   const int from = w.s.i0 >> 5, sh = w.s.i0 & 31;
                   const uint32_t w0 = mask_word(row, a.words, from), w1 = mask_word(row, a.words, from + 1),
                                  w2 = mask_word(row, a.words, from + 2);
                   nodes = __funnelshift_r(w0, w1, sh) | uint64_t(__funnelshift_r(w1, w2, sh)) << 32;
-                  if (a.window > 0) at_depth = a.depth[w.r.s0 + node];
                 }
-              }
+                int i = c0 / a.G, x = i * a.G - c0;  // the warp's first node, and its first row here
+                nodes >>= i;
+                uint64_t heads = a.G < 64 ? (1ull << a.G) - 1 : ~0ull;
+                uint32_t rows = uint32_t(heads >> -x);
+                rows_see = 0;
 #pragma unroll 1
-              for (int i = c0 / a.G, x = i * a.G - c0; x < CW; ++i, x += a.G) {
-                bool sees = nodes >> i & 1;
-                if (a.window > 0) sees = sees && at_depth > ms.deep[i * a.G] - a.window;
-                const int at = max(x, 0), n = min(x + a.G, 32) - at;  // its rows here
-                if (sees) rows_see |= (0xffffffffu >> (32 - n)) << at;
+                for (;;) {
+                  bool sees = nodes & 1;
+                  if (a.window > 0) sees = sees && below > ms.deep[i * a.G];
+                  if (sees) rows_see |= rows;
+                  nodes >>= 1;
+                  ++i;
+                  x += a.G;
+                  if (x >= CW) break;
+                  rows = uint32_t(heads) << x;
+                }
               }
             }
           }
           auto hide = [&](int x0, float* s) {
             if (whole) return;
             if constexpr (TREE) {
+              if (!mixed_warp) return;
 #pragma unroll
               for (int x = 0; x < CK; ++x)
                 if (!(rows_see >> (x0 + x) & 1)) s[x] = -INFINITY;
