@@ -123,6 +123,8 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = int(my_rank()), C = int(ranks()), b = blockIdx.x / C;
+  // no CTA writes to another before all have begun: they meet once the first has its view of the tree
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_trigger();
   pdl_wait();
   const float u_last = a.u_last[b];
@@ -158,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
     if (tid == 0) a.next[b] = -1;
     __syncthreads();
   }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   // the walk's state, in the first CTA's first warp
   int node = 0, seen = 0, kept = 0, refused = 0, gone = 0;
   u64 sigma = kOne;

@@ -197,3 +197,37 @@ def test_many_pages():
     want[:, :, order[1500:]] = raw[:, :, order[:1500]]
     moe.moe_kv_copy_pages(layers, i32(order[:1500]), i32(order[1500:]))
     assert torch.equal(raw, want)
+
+
+def test_pools_past_four_gigabytes():
+    """Pages whose bytes lie past 2^32, copied and moved in."""
+    page, D, npages = 64, 256, 140000  # 32 KB a page
+    k, v = (torch.empty(npages, 1, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    layers = moe.KvLayers([moe.KvPages(k, v)])
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(2, 1, page, D, generator=g).to(torch.bfloat16).cuda()
+    for pool in (k, v):
+        pool[5], pool[npages - 2] = x[0], x[1]
+    moe.moe_kv_copy_pages(layers, i32([5, npages - 2]), i32([npages - 1, 7]))
+    for pool in (k, v):
+        assert torch.equal(pool[npages - 1], x[0]) and torch.equal(pool[7], x[1])
+    batch = moe.KvBatch(i32([0, 10]), i32([70]), i32([[npages - 1, npages - 2]]), 10, 10)
+    lens = i32([0])
+    moe.moe_kv_compact(layers, batch, i32([[0, 5, 8, -1]]), i32([3]), lens)
+    for pool in (k, v):  # places 60, 65 and 68 to 60, 61 and 62
+        want = x[0].clone()
+        want[0, 61], want[0, 62] = x[1, 0, 1], x[1, 0, 4]
+        assert torch.equal(pool[npages - 1], want)
+    assert lens.tolist() == [63]
+
+
+def test_lengths_in_32_bits():
+    """A request whose length is past the table: nothing is read or written astray, and the length is told."""
+    s = Step([40], [10], 16, [[0, 4, 5]])
+    raw, layers = pools(1, s.npages, 2, 16, 64)
+    want = raw.clone()
+    for length in (2 ** 31 - 1, 49 + 16 * 1000, 5, 0, -2 ** 31):
+        s.batch.kv_len.fill_(length)
+        got, err = s.run(layers)
+        assert err == moe.MOE_ERANGE and got == [max(length - 10 + 3, -2 ** 31)]
+        assert torch.equal(raw, want)

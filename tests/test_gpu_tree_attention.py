@@ -262,3 +262,50 @@ def test_waits_that_run_out_are_reported(stage, D, G, n, e4m3):
     assert moe.moe_attn_sync_status(ws) == 0
     ref, tol = tree_attention_ref(P, q, G, 0.1, 0, parents)
     check(o.cpu().double(), ref, tol)
+
+
+@pytest.mark.parametrize("D,G,n", [(128, 4, 6), (128, 8, 40), (256, 8, 20), (64, 8, 40)])
+def test_lengths_past_the_table(D, G, n):
+    """Keys end where the table does; the nodes past it see those, and the call says so."""
+    P = Paged([100], [n], 1, D, 16, seed=2, table_extra=0)
+    parents = random_parents(n, 3, 0)
+    q = strided_rows(P.T, G, D, 0, torch.Generator().manual_seed(3))
+    pages, batch = P.device()
+    ws = moe.AttnWorkspace(G, 1, D)
+    t = tree_of(P, batch, [parents])
+    o = torch.empty(P.T, G, D, dtype=torch.bfloat16, device="cuda")
+    cap = P.width * 16
+    for pool in (P.dk, P.dv):
+        pool.nan_to_num_(0.25)
+    batch.kv_len.fill_(cap + n + 3)
+    moe.moe_tree_attention(pages, batch, t, q.cuda(), o, ws, scale=0.1)
+    assert moe.moe_attn_sync_status(ws) == moe.MOE_ERANGE
+    k, v = (torch.cat([x[int(i), 0].float() for i in P.table[0]]).double().cpu() for x in (P.dk, P.dv))
+    w = torch.softmax(torch.einsum("tgd,jd->tgj", q.double(), k) * 0.1, -1)
+    ref = torch.einsum("tgj,jd->tgd", w, v)
+    mag = torch.einsum("tgj,jd->tgd", w, v.abs())
+    ds = 2 * D * 2.0 ** -24 * (torch.einsum("tgd,jd->tgj", q.double().abs(), k.abs()) * 0.1).amax(-1, keepdim=True)
+    tol = mag * (2.0 ** -8 + 2 * ds + 2.0 ** -21 + 2 * cap * 2.0 ** -24) + ref.abs() * 2.0 ** -8 * (1 + 2.0 ** -8)
+    assert ((o.cpu().double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n,G,D", [(6, 4, 128), (40, 8, 128), (30, 8, 256)])
+def test_the_same_call_gives_the_same_bits(n, G, D):
+    """On any stream, beside another batch, in any run."""
+    lens, ns = [700 + n, 300 + n, 2000 + n], [n] * 3
+    P = Paged(lens, ns, 2, D, 16, seed=3)
+    parents = [random_parents(n, 3, b) for b in range(3)]
+    q = strided_rows(P.T, 2 * G, D, 0, torch.Generator().manual_seed(3)).cuda()
+    pages, batch = P.device()
+    t = tree_of(P, batch, parents)
+    torch.cuda.synchronize()
+    outs = []
+    for s in [torch.cuda.Stream() for _ in range(3)]:
+        ws = moe.AttnWorkspace(2 * G, 2, D)
+        for _ in range(3):
+            o = torch.empty(P.T, 2 * G, D, dtype=torch.bfloat16, device="cuda")
+            moe.moe_tree_attention(pages, batch, t, q, o, ws, scale=0.1, stream=s)
+            outs.append((o, ws))
+    torch.cuda.synchronize()
+    for o, _ in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0][0].view(torch.int16))

@@ -253,3 +253,47 @@ def test_two_streams_and_a_captured_call():
     torch.cuda.synchronize()
     want = a.expect(9)
     assert (outs[0][0].cpu().numpy() == want[0]).all() and outs[0][1].tolist() == want[1] and outs[0][2].tolist() == want[2]
+
+
+@pytest.mark.parametrize("B,V", [(1, 131072), (1, 7), (9, 20000), (19, 5000), (40, 3000)])
+def test_every_size_of_a_cluster(B, V):
+    """One request to so many that each has a CTA or two; called, captured and replayed."""
+    for drawn in (True, False):
+        c = Case([5] * B, V, drawn, spread=2, seed=B, near=0.3)
+        want = c.check()
+        batch, desc = c.device()
+        out = [torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((B, 5), (B,), (B,))]
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=st):
+                moe.moe_verify_drafts(batch, desc, *out)
+            for _ in range(3):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert (out[0].cpu().numpy() == want[0]).all() and out[1].tolist() == want[1] and out[2].tolist() == want[2]
+
+
+def test_many_clusters_of_one():
+    c = Case([3] * 700, 200, True, spread=2, seed=2, near=0.3)
+    c.check()
+
+
+def test_rows_past_four_gigabytes():
+    """The last request's rows lie past 2^32 bytes, and past 2^31 elements."""
+    c = Case([4], 65536, True, spread=2, seed=5, near=0.2)
+    lead = (1 << 31) // 65536 + 8
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    T = lead + 4
+    rows = [torch.empty(T, 65536, device="cuda") for _ in range(2)]
+    for big, small in zip(rows, (c.target, c.draft)):
+        big[lead:].copy_(torch.from_numpy(small))
+    wide = lambda x, fill: np.concatenate([np.full(lead, fill, dtype=x.dtype), x])  # noqa: E731
+    desc = moe.verify_desc(rows[0], i32(wide(c.token, 0)), i32(wide(c.parent, 0)), torch.from_numpy(wide(c.u, 0)).cuda(),
+                           torch.from_numpy(c.u_last).cuda(), draft=rows[1])
+    batch = moe.KvBatch(i32([lead, T]), i32([0]), i32([[0]]), T, 4)
+    out = [torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((1, 4), (1,), (1,))]
+    moe.moe_verify_drafts(batch, desc, *out)
+    want = c.expect(4)
+    assert (out[0].cpu().numpy() == want[0]).all() and out[1].tolist() == want[1] and out[2].tolist() == want[2]
