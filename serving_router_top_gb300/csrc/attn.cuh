@@ -88,7 +88,7 @@ struct Args {
   int words;
 };
 
-template <int D, int NR, bool E4M3>
+template <int D, int NR, bool E4M3, bool TREE>
 struct Cfg {
   static constexpr int DS = D < 128 ? D : 128;       // columns in a slot
   static constexpr int H = D / DS;                   // slots of a key or value tile
@@ -110,7 +110,10 @@ struct Cfg {
   static constexpr int NS0 = E4M3 ? NV : (FREE - QB * QBYTES) / SLOT, NS = NS0 > 16 ? 16 : NS0;
   static constexpr int NK0 = (codes(QB) + 1) / 2, NK = NK0 > 8 ? 8 : NK0, NR0 = codes(QB) / 2, NRAW = NR0 > 8 ? 8 : NR0;
   static constexpr int SN = E4M3 ? 2 * NR : NR;      // columns of S
-  static constexpr int CW = NR < 32 ? NR : 32;                 // rows a softmax warp holds
+  // Trees of 64 columns: twice the warps with half the rows each, as a tile's masks are a chain in every warp.  32 of up to
+  // 16 nodes of four heads over 60 to 8192 tokens 35.3 us, with 32 rows a warp 36.9; of eight under a window 25.4 and 26.5.
+  // With 128 and 256 columns it is the same within 1%; with 64 rows a warp and two CTAs an SM 46.5.
+  static constexpr int CW = TREE && !E4M3 && D == 64 ? 16 : NR < 32 ? NR : 32;                 // rows a softmax warp holds
   static constexpr int SW = 4 * (NR / CW);                      // softmax warps
   // Converting warps: four take 65 us where eight take 53 (128 columns, 16 rows); beside 16 softmax warps
   // eight leave no registers.
@@ -126,9 +129,8 @@ struct Cfg {
   // to 32768 keys 26.5, 24.6 and 24.0, 29.4, 27.0 and 26.2, 42.7, 39.8 and 39.0.  3 is within 3% of the best.
   static constexpr int V = !E4M3 && SLOT * H * 2 >= 65536 ? 2 : 3;
   // Trees, whose units end in tiles that hide keys by their masks.  32 trees of up to 16 nodes over 60 to 8192 tokens, 128
-  // columns, with 2, 3, 4, 5, 6 and 8: 55.0, 48.6, 47.6, 48.6, 49.9 and 52.4 us; 64 columns 53.1, 46.7, 41.9, 40.1, 37.9 and
-  // 37.4; 16 of up to 32 over 512 to 32768, 256 columns, bf16 108.8, 112.3, 112.5, 104.8, 96.2 and 88.6, E4M3 150.0, 129.2,
-  // 122.7, 115.7, 111.1 and 111.8; up to 4 nodes, E4M3, 128 columns 38.8, 34.7, 32.8, 32.3, 32.1 and 33.9.
+  // columns, with 2, 3, 4, 5, 6 and 8: 55.0, 48.6, 47.6, 48.6, 49.9 and 52.4 us; 64 columns with 3, 4, 5, 6 and 8: 41.7, 37.0,
+  // 36.0, 35.0 and 36.6; E4M3, 128 columns, up to 4 nodes, with 2, 3, 4, 5, 6 and 8: 38.8, 34.7, 32.8, 32.3, 32.1 and 33.9.
   static constexpr int VT = !E4M3 && D == 128 ? 4 : 6;
   static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
 };
@@ -606,8 +608,8 @@ __device__ __forceinline__ float transpose_sum(float (&v)[W], int lane) {
 }
 
 template <int D, int NR, bool E4M3, bool TREE>
-__global__ void __launch_bounds__(Cfg<D, NR, E4M3>::THREADS, Cfg<D, NR, E4M3>::OCC) k_attn(const __grid_constant__ Args a) {
-  using C = Cfg<D, NR, E4M3>;
+__global__ void __launch_bounds__(Cfg<D, NR, E4M3, TREE>::THREADS, Cfg<D, NR, E4M3, TREE>::OCC) k_attn(const __grid_constant__ Args a) {
+  using C = Cfg<D, NR, E4M3, TREE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;                         // keys and values, or values alone
   uint8_t* kring = ring + C::NS * C::SLOT;      // E4M3: keys
@@ -1494,6 +1496,16 @@ constexpr int kWideRows = 128;  // of attn_wide.cuh
 inline int row_tile(int D, int G, int n) {
   return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || D > 128 ? 64 : kChunkRows;
 }
+// The same for trees.  Those with more than 32 rows a key head of 256 columns go to attn_wide.cuh: 16 trees of 8 nodes of 8
+// heads (64 rows) over 512 to 32768 tokens 54.5 us in bf16 and 49.7 in E4M3, in 64-row tiles of attn.cuh 58.5 and 61.0;
+// one of them over 717 tokens 14.4 and 13.7.  With 64 columns there is a tile of 48 rows: 48 trees of up to 12 nodes of three
+// heads (36 rows) under a window of 1000 33.0 us, in 64 rows 36.2; with 128 columns memory is the bound and it
+// makes no difference (52.9 and 52.9).
+inline int tree_row_tile(int D, int G, int n, bool e4m3) {
+  const int nr = row_tile(D, G, n);
+  if (D == 256 && nr == 64) return kWideRows;
+  return D == 64 && !e4m3 && nr == 64 && 48 / G >= n ? 48 : nr;
+}
 
 // The join of NR-row tiles, which is the same for every kernel: one of a file for each D.
 template <int D>
@@ -1504,7 +1516,7 @@ template <> int launch_join<256>(const Args&, int, bool, int, cudaStream_t);
 
 template <int D, int NR, bool E4M3, bool TREE>
 int launch_one(const Args& a, int sms, cudaStream_t s) {
-  using C = Cfg<D, NR, E4M3>;
+  using C = Cfg<D, NR, E4M3, TREE>;
   // So few units that each is cut into more than sixteen pieces even at one run an SM: one run then, as
   // every further piece is another to join, and the join for many.  One token over 131071 keys: 52.4 us
   // at two runs an SM, 49.6 at one, 46.9 with this join.
@@ -1516,7 +1528,7 @@ int launch_one(const Args& a, int sms, cudaStream_t s) {
 template <int D, int NR, bool E4M3, bool TREE>
 int opt_in() {
   return cudaFuncSetAttribute(k_attn<D, NR, E4M3, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D, NR, E4M3>::SMEM) == cudaSuccess
+                              Cfg<D, NR, E4M3, TREE>::SMEM) == cudaSuccess
              ? MOE_OK
              : MOE_ECUDA;
 }

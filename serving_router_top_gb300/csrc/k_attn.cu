@@ -138,16 +138,13 @@ int attend(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, 
   if (T == 0 || b->B == 0) return MOE_OK;
   const long long width = (long long)Hq * kv->D;
   if (!rows_ok(q, q_stride, T, width) || !rows_ok(o, o_stride, T, width)) return MOE_EINVAL;
-  int nr = attn::row_tile(kv->D, Hq / kv->Hkv, b->max_n > 1 ? b->max_n : 1);
-  // Trees with more than 32 rows a key head of 256 columns go to attn_wide.cuh: 16 trees of 8 nodes of 8 heads (64 rows) over
-  // 512 to 32768 tokens 54.5 us in bf16 and 49.7 in E4M3, in 64-row tiles of attn.cuh 58.5 and 61.0; one of them over 717
-  // tokens 14.2 and 13.7.
-  if (tree && kv->D == 256 && b->max_n > 32 / (Hq / kv->Hkv)) nr = attn::kWideRows;
+  const int G = Hq / kv->Hkv, n = b->max_n > 1 ? b->max_n : 1;
+  const int nr = tree ? attn::tree_row_tile(kv->D, G, n, kv->e4m3) : attn::row_tile(kv->D, G, n);
   a.o = o;
   a.os = T > 1 ? o_stride : width;
   a.q = q;
   a.qs = T > 1 ? q_stride : width;
-  a.G = Hq / kv->Hkv;
+  a.G = G;
   a.window = window < attn::cap_of(a.kv) ? window : 0;  // one that holds every key is none
   const int tile = nr == attn::kChunkRows ? nr / 2 / a.G : nr / a.G;  // tokens of a row tile
   a.tokens = nr == attn::kChunkRows ? 2 * tile : tile;

@@ -38,6 +38,7 @@ int opt_in_d64() {
                  chunk::opt_in<64, true, false>() ||
                  as_before(k_join<64, 16>) ||
                  as_before(k_join<64, 32>) ||
+                 as_before(k_join<64, 48>) ||
                  as_before(k_join<64, 64>) ||
                  as_before(k_join<64, 256>) ||
                  as_before(k_join_many<64>)
@@ -52,6 +53,7 @@ int launch_join<64>(const Args& a, int nr, bool many, int ctas, cudaStream_t s) 
   if (many) e = launch_pdl(k_join_many<64>, dim3(ctas, a.G < 16 ? a.G : 16), threads, 0, s, a);
   else if (nr == 16) e = launch_pdl(k_join<64, 16>, dim3(ctas, join_y(16)), threads, 0, s, a);
   else if (nr == 32) e = launch_pdl(k_join<64, 32>, dim3(ctas, join_y(32)), threads, 0, s, a);
+  else if (nr == 48) e = launch_pdl(k_join<64, 48>, dim3(ctas, join_y(48)), threads, 0, s, a);
   else if (nr == 64) e = launch_pdl(k_join<64, 64>, dim3(ctas, join_y(64)), threads, 0, s, a);
   else e = launch_pdl(k_join<64, kChunkRows>, dim3(ctas, join_y(kChunkRows)), threads, 0, s, a);
   return e == cudaSuccess ? MOE_OK : MOE_ECUDA;

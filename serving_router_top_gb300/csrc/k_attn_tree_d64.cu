@@ -17,6 +17,7 @@ int launch_tree_d64(const Args& a, int e4m3, int nr, int sms, cudaStream_t s) {
     switch (nr) {
       case 16: return launch_one<64, 16, false, true>(a, sms, s);
       case 32: return launch_one<64, 32, false, true>(a, sms, s);
+      case 48: return launch_one<64, 48, false, true>(a, sms, s);
       case 64: return launch_one<64, 64, false, true>(a, sms, s);
       default: return chunk::launch<64, false, true>(a, sms, s);
     }
@@ -27,6 +28,7 @@ int opt_in_tree_d64() {
   return opt_in<64, 16, false, true>() ||
                  opt_in<64, 32, false, true>() ||
                  opt_in<64, 64, false, true>() ||
+                 opt_in<64, 48, false, true>() ||
                  opt_in<64, 16, true, true>() ||
                  opt_in<64, 32, true, true>() ||
                  opt_in<64, 64, true, true>() ||
