@@ -20,16 +20,18 @@ struct NormArgs {
   float eps;
 };
 
-// 8192 tokens of 32 + 2 x 4 heads of 128 columns, 168 MB: 33.1 us with two items a thread and 64 registers (four CTAs of
-// 256 threads); with registers for five 34.3, six 38.9, without a limit 34.2; one item 39.6 at its best, three 33.2, four
-// 34.1.  It issues on 69% of the cycles; a third of its instructions find request, page and angles.
+// 8192 tokens of 32 + 2 x 4 heads of 128 columns, 168 MB: 32.3 us, 5.2 TB/s, with two items a thread and 64 registers (four
+// CTAs of 256 threads); with one fp32 at a time 33.3, of which with registers for five CTAs 34.3, for six 38.9, without a
+// limit 34.2; with one item a thread 39.6 at its best, three 33.2, four 34.1.  It issues on two cycles of three; a third of
+// its instructions find request, page and angles.
 constexpr int kMine = 2, kPerSm = 4;
 
 template <bool E4M3, int D>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm) k_kv_append_norm(const __grid_constant__ NormArgs na) {
   const Args& a = na.a;
   constexpr int kItems = D / 16;
-  __shared__ float2 cs[8][kMaxPairs / 8];  // cos, sin of each pair's angle: pair 8 j + i at [i][j]
+  // cos of pairs 8 j + 4 z .. at [0][z][j], sin at [1][z][j]: a lane takes four of each at a time
+  __shared__ float4 turn[2][2][kMaxPairs / 8];
   __shared__ uint4 weights[D / 4];         // eight columns each: the queries', then the keys'
   __shared__ int owner, position, begins;
   pdl_trigger();
@@ -103,7 +105,8 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) k_kv_append_norm(const __
     const long long frac = (long long)(uint64_t(int64_t(turned)) * a.turns[i]);
     float c, s;
     sincospif(float(frac) * 0x1p-63f, &s, &c);
-    cs[i & 7][i >> 3] = make_float2(c, s);
+    reinterpret_cast<float*>(&turn[0][i >> 2 & 1][i >> 3])[i & 3] = c;
+    reinterpret_cast<float*>(&turn[1][i >> 2 & 1][i >> 3])[i & 3] = s;
   }
   if (id >= 0 && id < a.kv.npages)
     at = id * a.kv.page_stride + (long long)(pos & ((1 << a.kv.page_shift) - 1)) * a.kv.tok_stride;
@@ -118,41 +121,55 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) k_kv_append_norm(const __
     unpack8(x.v0, f0);
     unpack8(x.v1, f1);
     if (na.norm && x.head < a.Hq + a.kv.Hkv) {
-      float sum = 0.f;
+      float2 both = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], sum));
+      for (int i = 0; i < 8; i += 2) {
+        const float2 u = make_float2(f0[i], f0[i + 1]), v = make_float2(f1[i], f1[i + 1]);
+        both = __ffma2_rn(u, u, __ffma2_rn(v, v, both));
+      }
+      float sum = both.x + both.y;
       const unsigned mates = ((1u << kItems) - 1) << ((threadIdx.x & 31) / kItems * kItems);
 #pragma unroll
       for (int o = 1; o < kItems; o <<= 1) sum += __shfl_xor_sync(mates, sum, o);
       const float inv = rsqrtf(sum * (1.f / D) + na.eps);
       const int z = x.head >= a.Hq ? D / 8 : 0;
+      const float2 inv2 = make_float2(inv, inv);
       float w[8];
       unpack8(weights[z + x.c0 / 8], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f0[i] *= inv * w[i];
+      for (int i = 0; i < 8; i += 2) {
+        const float2 r = __fmul2_rn(make_float2(f0[i], f0[i + 1]), __fmul2_rn(make_float2(w[i], w[i + 1]), inv2));
+        f0[i] = r.x, f0[i + 1] = r.y;
+      }
       unpack8(weights[z + x.c1 / 8], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f1[i] *= inv * w[i];
+      for (int i = 0; i < 8; i += 2) {
+        const float2 r = __fmul2_rn(make_float2(f1[i], f1[i + 1]), __fmul2_rn(make_float2(w[i], w[i + 1]), inv2));
+        f1[i] = r.x, f1[i + 1] = r.y;
+      }
     }
     if (x.pair >= 0) {
-      if (!a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 r = cs[i][x.pair];
-          const float u = f0[i], w = f1[i];
-          f0[i] = u * r.x - w * r.y;
-          f1[i] = w * r.x + u * r.y;
-        }
-      } else {
+      for (int h = 0; h < 2; ++h) {
+        const float4 c4 = turn[0][h][x.pair], s4 = turn[1][h][x.pair];
+        if (!a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 r = cs[i][x.pair], r2 = cs[4 + i][x.pair];
-          float u = f0[2 * i], w = f0[2 * i + 1];
-          f0[2 * i] = u * r.x - w * r.y;
-          f0[2 * i + 1] = w * r.x + u * r.y;
-          u = f1[2 * i], w = f1[2 * i + 1];
-          f1[2 * i] = u * r2.x - w * r2.y;
-          f1[2 * i + 1] = w * r2.x + u * r2.y;
+          for (int i = 0; i < 4; i += 2) {
+            float *u = f0 + 4 * h + i, *w = f1 + 4 * h + i;
+            const float2 c = i ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y), s = i ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+            const float2 uu = make_float2(u[0], u[1]), ww = make_float2(w[0], w[1]), ws = __fmul2_rn(ww, s);
+            const float2 r = __ffma2_rn(uu, c, make_float2(-ws.x, -ws.y)), q = __ffma2_rn(uu, s, __fmul2_rn(ww, c));
+            u[0] = r.x, u[1] = r.y, w[0] = q.x, w[1] = q.y;
+          }
+        } else {
+          float* f = h ? f1 : f0;
+          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float u = f[2 * i], w = f[2 * i + 1];
+            f[2 * i] = fmaf(u, c[i], -(w * s[i]));
+            f[2 * i + 1] = fmaf(u, s[i], w * c[i]);
+          }
         }
       }
     }
