@@ -652,7 +652,7 @@ int moe_kv_append_norm(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_
  * own less the window.  What other nodes' places hold takes no part.  The masks
  * are moe_tree_prepare's for the same batch, each the other's transpose; with
  * others a row may see what either of them says.  Everything else as in
- * moe_paged_attention. */
+ * moe_paged_attention, with seven in the place of four in the size of a call. */
 int moe_tree_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, const uint16_t* q,
                        long long q_stride, int Hq, uint16_t* o, long long o_stride, float scale, int window,
                        moe_attn_ws* ws, moe_stream_t stream);
@@ -688,7 +688,7 @@ typedef struct {
 /* path int32 [B][path_stride]: the kept nodes in their order, node 0 first, then -1; at
  * most path_stride of them (the walk ends there as at a node without children).
  * count int32 [B]: how many; 0 for a request without nodes.  token int32 [B]: the
- * next token, -1 for a request without nodes.  Of b, q_start, B, T and max_n are used.
+ * next token, -1 for a request without nodes.  Of b, q_start, B and T are used.
  * Nodes past 256 of a request are never reached and record MOE_ERANGE in err_dev
  * (int32[1], may be NULL), as does q_start that decreases.  path_stride >= 1, fp32
  * arrays 4-byte aligned.  Asynchronous on `stream`. */

@@ -113,7 +113,7 @@ struct Cfg {
   // Trees of 64 columns: twice the warps with half the rows each, as a tile's masks are a chain in every warp.  32 of up to
   // 16 nodes of four heads over 60 to 8192 tokens 35.3 us, with 32 rows a warp 36.9; of eight under a window 25.4 and 26.5.
   // With 128 and 256 columns it is the same within 1%; with 64 rows a warp and two CTAs an SM 46.5.
-  static constexpr int CW = TREE && !E4M3 && D == 64 ? 16 : NR < 32 ? NR : 32;                 // rows a softmax warp holds
+  static constexpr int CW = TREE && !E4M3 && D == 64 ? 16 : NR < 32 ? NR : 32;  // rows a softmax warp holds
   static constexpr int SW = 4 * (NR / CW);                      // softmax warps
   // Converting warps: four take 65 us where eight take 53 (128 columns, 16 rows); beside 16 softmax warps
   // eight leave no registers.
@@ -132,6 +132,7 @@ struct Cfg {
   // columns, with 2, 3, 4, 5, 6 and 8: 55.0, 48.6, 47.6, 48.6, 49.9 and 52.4 us; 64 columns with 3, 4, 5, 6 and 8: 41.7, 37.0,
   // 36.0, 35.0 and 36.6; E4M3, 128 columns, up to 4 nodes, with 2, 3, 4, 5, 6 and 8: 38.8, 34.7, 32.8, 32.3, 32.1 and 33.9.
   static constexpr int VT = !E4M3 && D == 128 ? 4 : 6;
+  static_assert(V <= 3 && VT <= 6, "places of a unit, as the call's checks count them");
   static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
 };
 

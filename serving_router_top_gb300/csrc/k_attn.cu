@@ -148,8 +148,9 @@ int attend(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_tree* tree, 
   a.window = window < attn::cap_of(a.kv) ? window : 0;  // one that holds every key is none
   const int tile = nr == attn::kChunkRows ? nr / 2 / a.G : nr / a.G;  // tokens of a row tile
   a.tokens = nr == attn::kChunkRows ? 2 * tile : tile;
-  // the schedule counts in 31 bits: a unit has at most its request's tiles, and three more places
-  if ((double(T) / a.tokens + b->B) * kv->Hkv * (double(a.kv.table_stride) * kv->page / attn::kKeys + 4) > 2147483000.0)
+  // the schedule counts in 31 bits: a unit has at most its request's tiles, and three more places, of a tree six
+  const int more = tree ? 7 : 4;
+  if ((double(T) / a.tokens + b->B) * kv->Hkv * (double(a.kv.table_stride) * kv->page / attn::kKeys + more) > 2147483000.0)
     return MOE_EINVAL;
   const int size = kv->e4m3 ? 1 : 2, box = kv->page < attn::kKeys ? kv->page : attn::kKeys;
   // sizes and byte strides of the pools, innermost first; a size of one takes any stride

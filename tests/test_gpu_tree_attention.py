@@ -309,3 +309,20 @@ def test_the_same_call_gives_the_same_bits(n, G, D):
     torch.cuda.synchronize()
     for o, _ in outs[1:]:
         assert torch.equal(o.view(torch.int16), outs[0][0].view(torch.int16))
+
+
+def test_calls_that_the_schedule_cannot_count_are_refused():
+    """Nothing is launched: the addresses are never followed."""
+    import ctypes as C
+    from tests.test_attn_refusals import P16, batch, pages
+    ws = moe.AttnWorkspace(2, 2, 128)
+    t = moe.moe_tree(P16, P16, P16, P16, 1)
+    p = pages()
+    for b, ok in ((batch(T=1 << 22, B=1 << 12, table_stride=1 << 17), False), (batch(T=0, B=1 << 12, table_stride=1 << 17), True)):
+        rc = moe.load().moe_tree_attention(C.byref(p), C.byref(b), C.byref(t), P16, 256, 2, P16, 256, 1.0, 0, ws.handle, None)
+        assert rc == (moe.MOE_OK if ok else moe.MOE_EINVAL)
+    for bad in (dict(words=0), dict(words=9), dict(above=None), dict(below=None), dict(depth=None)):
+        t = moe.moe_tree(*[{**dict(parent=P16, depth=P16, above=P16, below=P16, words=1), **bad}[n] for n, _ in moe.moe_tree._fields_])
+        b = batch()
+        assert moe.load().moe_tree_attention(C.byref(p), C.byref(b), C.byref(t), P16, 256, 2, P16, 256, 1.0, 0, ws.handle,
+                                             None) == moe.MOE_EINVAL
