@@ -721,7 +721,7 @@ def _error_word(err):
     """Address of an error word, and whether it is where the kernels can write it."""
     if err is None or isinstance(err, int):
         return err, True
-    return _ints(err, (1,), "err"), err.is_cuda
+    return err.data_ptr(), err.is_cuda
 
 
 class Tree:
