@@ -26,6 +26,7 @@ runs a prompt, decode windows and trees of a small model and prints the times.
 from __future__ import annotations
 
 import dataclasses
+import weakref
 from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
@@ -132,6 +133,9 @@ class Pages:
 
 
 class Decoder:
+    # trees that accept() has not seen: their batch, and the nodes of each request, 0 once it was released
+    trees: Tuple[Tuple["weakref.ref[moe.KvBatch]", List[int]], ...] = ()
+
     def __init__(self, w: I.Workload, s: AttentionShape, requests: int, max_len: int, maxT: int, eps: float = 1e-6):
         self.st = ModelState(w, maxT=maxT)
         self.s, self.H, self.eps, self.maxT = s, w.shape.H, eps, maxT
@@ -153,11 +157,18 @@ class Decoder:
         self.o = torch.empty(maxT, s.Hq, s.D, dtype=bf, device="cuda")
         self.lens = [0] * requests
 
+    def open_tree(self, request: int) -> bool:
+        """Whether the request's last tokens are a tree's nodes, of which accept() has yet to tell what stays."""
+        return any(nodes[request] for _, nodes in self.trees)
+
     def batch(self, new: Sequence[int]) -> moe.KvBatch:
-        """The next call's requests: new[r] tokens of request r (pages are reserved for them).  A call
-        that raises leaves lengths and pages as they were."""
+        """The next call's requests: new[r] tokens of request r (pages are reserved for them), none for one whose
+        tree waits for accept().  A call that raises leaves lengths and pages as they were."""
         if len(new) != len(self.lens) or min(new) < 0 or sum(new) > self.maxT:
             raise ValueError(f"new tokens of {len(self.lens)} requests, at most {self.maxT} in all, got {list(new)}")
+        for r, n in enumerate(new):
+            if n and self.open_tree(r):
+                raise ValueError(f"the tree of request {r} has not been verified")
         lens = [have + n for have, n in zip(self.lens, new)]
         self.pages.reserve_all(dict(enumerate(lens)))
         self.lens = lens
@@ -168,31 +179,49 @@ class Decoder:
 
     def tree_batch(self, parents: Sequence[Sequence[int]]) -> Tuple[moe.KvBatch, moe.Tree]:
         """The next call's trees: parents[r] for each node of request r, -1 for its root.  The nodes count among the
-        request's tokens until accept() tells which of them stay."""
+        request's tokens until accept() tells which of them stay; until then it takes no other tokens and is not
+        forked.  What other requests do in between is theirs."""
         new = [len(p) for p in parents]
         if max(new) > 256 or any(not -1 <= up < i for p in parents for i, up in enumerate(p)):
             raise ValueError("a tree has at most 256 nodes, each behind its parent")
         bt = self.batch(new)
         tree = moe.Tree(bt, torch.tensor([up for p in parents for up in p], dtype=torch.int32).cuda())
         moe.moe_tree_prepare(bt, tree, err=self.ws.error_ptr)
+        # those that nobody can accept any more and that hold up no request go
+        self.trees = tuple(t for t in self.trees if any(t[1]) or t[0]() is not None) + ((weakref.ref(bt), new),)
         return bt, tree
 
     def accept(self, bt: moe.KvBatch, desc: moe.VerifyDesc, most: Optional[int] = None) -> Tuple[List[List[int]], List[int]]:
-        """After forward() of tree_batch()'s trees: the nodes of each request that the target keeps (at most `most`), and its
-        next token.  Keys and values of the others are gone, and lengths are those of what was kept."""
-        B = len(self.lens)
-        most = bt.c.max_n if most is None else most
-        path = torch.empty(B, max(most, 1), dtype=torch.int32, device="cuda")
-        count, token, lens = (torch.empty(B, dtype=torch.int32, device="cuda") for _ in range(3))
+        """After forward() of tree_batch()'s trees, once: the nodes of each request that the target keeps (at most `most`),
+        and its next token.  Keys and values of the others are gone, and the lengths of the trees' requests are those of
+        what was kept.  A request that was released meanwhile keeps nothing."""
+        mine = [nodes for batch, nodes in self.trees if batch() is bt]
+        if not mine:
+            raise ValueError("a batch of trees that has not been verified is wanted")
+        most = max(bt.c.max_n, 1) if most is None else most
+        if most < 1:
+            raise ValueError("at least a tree's first node is kept")
+        B, nodes = len(self.lens), mine[0]
+        path = torch.empty(B, most, dtype=torch.int32, device="cuda")
+        count, token = (torch.empty(B, dtype=torch.int32, device="cuda") for _ in range(2))
         moe.moe_verify_drafts(bt, desc, path, count, token, err=self.ws.error_ptr)
-        moe.moe_kv_compact(self.kv_layers, bt, path, count, lens, err=self.ws.error_ptr)
-        self.lens = lens.tolist()
-        return [p[:n] for p, n in zip(path.tolist(), count.tolist())], token.tolist()
+        if sum(nodes) < bt.c.T:  # the places of a released request may be another's by now
+            here = torch.tensor([n > 0 for n in nodes]).cuda()
+            count.masked_fill_(~here, 0)
+            token.masked_fill_(~here, -1)
+        moe.moe_kv_compact(self.kv_layers, bt, path, count, err=self.ws.error_ptr)
+        kept = count.tolist()
+        for r, n in enumerate(nodes):
+            self.lens[r] -= n - kept[r]
+        self.trees = tuple(t for t in self.trees if t[0]() is not bt)
+        return [p[:n] for p, n in zip(path.tolist(), kept)], token.tolist()
 
     def fork(self, source: int, request: int) -> None:
-        """Request `request`, which has no tokens, goes on from the tokens of `source`."""
+        """Request `request`, which has no tokens, goes on from the tokens of `source`, whose tree if any is verified."""
         if self.lens[request]:
             raise ValueError(f"request {request} has tokens of its own")
+        if self.open_tree(source):
+            raise ValueError(f"the tree of request {source} has not been verified")
         self.pages.release(request)
         for a, z, n in self.pages.fork(source, request, self.lens[source]):
             i32 = lambda x: torch.tensor([x], dtype=torch.int32).cuda()  # noqa: E731
@@ -200,9 +229,12 @@ class Decoder:
         self.lens[request] = self.lens[source]
 
     def release(self, request: int) -> None:
-        """The request has no tokens any more."""
+        """The request has no tokens any more, nor a tree.  What forward() is still to run finds no pages of it."""
         self.pages.release(request)
+        self.pages.upload()
         self.lens[request] = 0
+        for _, nodes in self.trees:
+            nodes[request] = 0
 
     def attention(self, l: int, xn: torch.Tensor, bt: moe.KvBatch, y: torch.Tensor, tree: Optional[moe.Tree] = None) -> None:
         """y = attention of layer l on the normalised rows xn, whose keys and values join the cache."""
