@@ -57,6 +57,7 @@
 #include <limits.h>
 
 #include "paged.cuh"
+#include "tree_mask.h"
 
 namespace moe {
 namespace attn {
@@ -563,10 +564,6 @@ __device__ __forceinline__ void drop_not_finite(uint8_t* slot, int key) {
 }
 
 // ------------------------------------------------------------------ trees
-// Of the 32 nodes from 32 w on: bits of a node's row of a mask.  Before the first are keys that every node sees.
-__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int words, int w) {
-  return w < 0 ? 0xffffffffu : w < words ? row[w] : 0u;
-}
 // Whether node i of a request sees a key.
 __device__ __forceinline__ bool tree_sees(const Args& a, const Req& r, int i, int key) {
   const int node = key - r.pos0;

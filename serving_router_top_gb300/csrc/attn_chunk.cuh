@@ -98,27 +98,9 @@ __device__ __forceinline__ void turn4(float (&v)[16], int lane) {
 // Bit j of seen: node i sees key key0 + j, of 32 WORDS keys.
 template <int WORDS>
 __device__ __forceinline__ void tree_keys(const Args& a, const Req& r, int i, int key0, int cap, uint32_t* seen) {
-  const uint32_t* row = a.above + (long long)(r.s0 + i) * a.words;
-  const int node0 = key0 - r.pos0, deep = a.window > 0 ? a.depth[r.s0 + i] : 0;
-  const int from = a.window > 0 ? r.pos0 + deep - a.window + 1 - key0 : INT_MIN;  // of the keys before the tree
-  uint32_t low = mask_word(row, a.words, node0 >> 5);
-#pragma unroll
-  for (int k = 0; k < WORDS; ++k) {
-    const uint32_t high = mask_word(row, a.words, (node0 >> 5) + k + 1);
-    uint32_t m = __funnelshift_r(low, high, node0 & 31);
-    low = high;
-    // keys past the request's or the table's end, and keys before the tree and the window
-    const int end = min(cap, r.kv) - key0 - 32 * k, begin = min(from, -node0) - 32 * k;
-    m = end >= 32 ? m : end <= 0 ? 0u : m & ((1u << end) - 1);
-    m = begin <= 0 ? m : begin >= 32 ? 0u : m & (0xffffffffu << begin);
-    if (a.window > 0 && deep >= a.window) {  // a window smaller than the tree is deep: nodes, one by one
-      for (uint32_t rest = m; rest; rest &= rest - 1) {
-        const int node = node0 + 32 * k + __ffs(rest) - 1;
-        if (node >= 0 && a.depth[r.s0 + node] <= deep - a.window) m &= ~(rest & -rest);
-      }
-    }
-    seen[k] = m;
-  }
+  const int deep = a.window > 0 ? a.depth[r.s0 + i] : 0;
+  seen_keys<WORDS>(a.above + (long long)(r.s0 + i) * a.words, a.words, a.depth + r.s0, deep, a.window, key0 - r.pos0,
+                   min(cap, r.kv) - key0, seen);
 }
 
 // Registers a thread from here on, of a warpgroup.
