@@ -144,10 +144,10 @@ struct Req {
 };
 __device__ __forceinline__ Req load_req(const KvView& kv, int b) {
   Req r;
-  const int s0 = kv.q_start[b], s1 = kv.q_start[b + 1];
+  const RowSpan rows = row_span(kv.q_start, b, kv.T);
   r.kv = max(kv.kv_len[b], 0);
-  r.s0 = min(max(s0, 0), kv.T);
-  r.n = min(s1, kv.T) - r.s0;  // below zero where the starts decrease
+  r.s0 = rows.s0;
+  r.n = rows.n;
   r.pos0 = r.kv - r.n;
   return r;
 }

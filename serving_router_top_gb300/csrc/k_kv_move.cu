@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThreads, kCompactPerSm) k_compact(const __gri
   pdl_wait();
   const int b = blockIdx.x, tid = threadIdx.x;
   const KvView& kv = a.kv;
-  const int s0 = min(max(kv.q_start[b], 0), kv.T), n = max(min(kv.q_start[b + 1], kv.T) - s0, 0);
+  const int rows = row_span(kv.q_start, b, kv.T).n, n = max(rows, 0);
   const long long base = (long long)kv.kv_len[b] - n;
   int want = a.count[b];
   want = min(max(want, 0), min(n, a.path_stride));
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, kCompactPerSm) k_compact(const __gri
     __syncthreads();
   }
   if (speaks) {
-    if (kept < want || kv.q_start[b + 1] < kv.q_start[b]) set_error(a.err, MOE_ERANGE);
+    if (kept < want || rows < 0) set_error(a.err, MOE_ERANGE);
     if (a.len) a.len[b] = int(min(max(base + kept, (long long)INT32_MIN), (long long)INT32_MAX));
   }
 }

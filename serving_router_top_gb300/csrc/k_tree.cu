@@ -27,7 +27,8 @@ __global__ void __launch_bounds__(kNodes) k_tree(const __grid_constant__ Args a)
   pdl_trigger();
   pdl_wait();
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5, W = a.words;
-  const int s0 = min(max(a.q_start[blockIdx.x], 0), a.T), n = min(a.q_start[blockIdx.x + 1], a.T) - s0;
+  const RowSpan rows = row_span(a.q_start, blockIdx.x, a.T);
+  const int s0 = rows.s0, n = rows.n;
   if (n < 0 && i == 0) set_error(a.err, MOE_ERANGE);
   if (n <= 0) return;
   const int m = min(n, 32 * W);

@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
   // ------------------------------------------------------------ the first CTA's view of the tree
   int s0 = 0, n = 0;
   if (rank == 0) {
-    const int first = a.q_start[b], last = a.q_start[b + 1];
-    s0 = min(max(first, 0), a.T);
-    n = min(last, a.T) - s0;
+    const RowSpan rows = row_span(a.q_start, b, a.T);
+    s0 = rows.s0;
+    n = rows.n;
     if (tid == 0 && (n < 0 || n > kNodes)) set_error(a.err, MOE_ERANGE);
     n = min(max(n, 0), kNodes);
     for (int i = tid; i < kNodes; i += kThreads) {

@@ -18,6 +18,16 @@ struct KvView {
   int B, T, table_stride;
 };
 
+// A request's first row and how many there are, among T: below zero where its starts decrease.  A start below the call's
+// rows counts as -1, as the difference to one far below would leave 32 bits and be a number of rows.
+struct RowSpan {
+  int s0, n;
+};
+__device__ __forceinline__ RowSpan row_span(const int32_t* q_start, int b, int T) {
+  const int s0 = min(max(q_start[b], 0), T);
+  return {s0, min(max(q_start[b + 1], -1), T) - s0};
+}
+
 // MOE_OK and the view when the pools and the requests pass their checks.
 inline int kv_view(const moe_kv_pages* p, const moe_kv_batch* b, KvView* out) {
   if (!p || !b || !p->k || !p->v || (p->e4m3 != 0 && p->e4m3 != 1) || p->Hkv < 1 || p->Hkv > 1024 ||
