@@ -387,8 +387,9 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
         continue;
       }
       const unsigned past = __ballot_sync(0xffffffffu, t < upto);
+      const u64 earlier = __shfl_up_sync(0xffffffffu, upto, 1);  // at most t where upto is above it, so it was not cut
       if (lane == __ffs(past) - 1) {
-        u64 left = t - (upto - four);
+        u64 left = lane > 0 ? t - earlier : t;
         int i = 0;
         while (i < 3 && left >= r[i]) left -= r[i++];
         a.next[b] = x0 + i - rows.lead;
