@@ -669,7 +669,7 @@ int moe_tree_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_
  * q independently of one another (or picked before u is known), kept tokens and next
  * token are distributed as the target's.
  * Rows are probabilities: an entry below 0 or NaN counts as 0, one above 1 as 1; sums
- * above 4 count as 4.  Sums are kept in fixed point, 2^-60 a unit: no order of sums
+ * above 4 count as 4, s below 0 as 0.  Sums are kept in fixed point, 2^-60 a unit: no order of sums
  * changes a result.  A u below 0 or NaN counts as 0, from 1 on as the largest below 1. */
 typedef struct {
   const float* target;    /* fp32 [T][V] device, one row a node                           */

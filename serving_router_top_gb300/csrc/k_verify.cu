@@ -270,6 +270,26 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
     const int lines = (rows.end + 127) / 128, each = (lines + C * kWarps - 1) / (C * kWarps);  // of 128 places; of a warp
     const int line0 = min((rank * kWarps + warp) * each, lines), line1 = min(line0 + each, lines);
     const int deep = (each + kGroups - 1) / kGroups;  // lines of a group
+    // Picked tokens that are gone are zeros before anything is added up: taken off a sum that was cut they would leave
+    // another one, by what else the sum was of.  A few of a request's warps have any.
+    bool lost = false;
+    if constexpr (!DRAWN)
+      for (int k = 0; k < o.gone; k += 32) {
+        const int line = k + lane < o.gone ? (sh.gone[k + lane] + rows.lead) / 128 : -1;
+        lost |= __any_sync(0xffffffffu, line >= line0 && line < line1);
+      }
+    auto drop = [&](int line, float4& v) {
+      for (int k = 0; k < o.gone; k += 32) {
+        const int t = k + lane < o.gone ? sh.gone[k + lane] + rows.lead : -1;
+        for (unsigned here = __ballot_sync(0xffffffffu, t >= 0 && t / 128 == line); here; here &= here - 1) {
+          const int at = __shfl_sync(0xffffffffu, t, __ffs(here) - 1) - 128 * line - 4 * lane;
+          if (at == 0) v.x = 0.f;
+          if (at == 1) v.y = 0.f;
+          if (at == 2) v.z = 0.f;
+          if (at == 3) v.w = 0.f;
+        }
+      }
+    };
     u64 sum[kGroups] = {};
     for (int l = 0; l < deep; ++l) {
       const bool p_here = deep == 1 && held == o.row, q_here = p_here && held_q;
@@ -283,6 +303,9 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
           if (!q_here && o.refused > 0) load4(rows.q, rows, 128 * line + 4 * lane, rows.together, &y[g]);
         }
       }
+      if (!DRAWN && lost)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) drop(line0 + g * deep + l, x[g]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         // four of at most 2^60 beside at most 2^62: no carry is lost
@@ -291,23 +314,14 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
         sum[g] = min(sum[g], kMost);
       }
     }
-    held = o.row;
+    held = lost ? -1 : o.row;
     held_q = o.refused > 0;
-    // Without the picked ones that are gone, from line `from` to before line `to`.
-    auto without = [&](u64 v, int from, int to) {
-      for (int k = 0; k < o.gone; k += 32) {
-        const int t = k + lane < o.gone ? sh.gone[k + lane] : -1, line = (t + rows.lead) / 128;
-        for (unsigned here = __ballot_sync(0xffffffffu, t >= 0 && line >= from && line < to); here; here &= here - 1)
-          v = less(v, fixed(__ldg(p + __shfl_sync(0xffffffffu, t, __ffs(here) - 1))));
-      }
-      return v;
-    };
     auto over_lanes = [](u64 v) {
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) v = plus(v, __shfl_xor_sync(0xffffffffu, v, d));
       return v;
     };
-    const u64 mine = without(over_lanes(plus(plus(sum[0], sum[1]), plus(sum[2], sum[3]))), line0, line1);
+    const u64 mine = over_lanes(plus(plus(sum[0], sum[1]), plus(sum[2], sum[3])));
     if (lane == 0) sh.warp[warp] = mine;
     __syncthreads();
     if (tid < C) {
@@ -345,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_verify(const __grid_consta
     int l0 = line0, end = line1;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const u64 here = without(over_lanes(sum[g]), line0 + g * deep, min(line0 + (g + 1) * deep, line1));
+      const u64 here = over_lanes(sum[g]);
       l0 = line0 + g * deep;
       end = min(l0 + deep, line1);
       if (deep == 1) x[0] = x[g], y[0] = y[g];

@@ -70,7 +70,16 @@ def check(c, most):
         assert path[b].tolist() == want + [-1] * (most - len(want)) and count[b] == len(want) and token[b] == nxt, b
 
 
-@pytest.mark.parametrize("drawn", [True])
+def test_a_refused_pick_is_not_taken_off_a_cut_sum():
+    """Halves: R's running sum passes 0.95 x 4 at the eighth index that is left."""
+    for B in (1, 40):
+        c = Case([2] * B, 5000, False, spread=1, seed=1)
+        c.target[:], c.token[:], c.u[:], c.u_last[:] = 0.5, 3, 0.9, 0.95
+        _, count, token, _ = c.run(2)
+        assert count == [1] * B and token == [8] * B
+
+
+@pytest.mark.parametrize("drawn", [True, False])
 @pytest.mark.parametrize("B,V,n", [(1, 5000, 6), (1, 140001, 4), (9, 20000, 6), (70, 30011, 5), (320, 600, 6), (700, 90, 12)])
 def test_rows_of_any_size(B, V, n, drawn):
     """Rows of eighths that sum from a fraction to thousands, at every size of a cluster."""
