@@ -177,8 +177,10 @@ extern "C" int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch*
   a.path_stride = path_stride;
   a.len = kv_len_out;
   a.err = err_dev;
-  // CTAs for one turn of the GPU's 152 SMs, each over several pools: the chain before the first row is paid once
-  const int y = 152 * move::kCompactPerSm > b->B ? 152 * move::kCompactPerSm / b->B : 1;
+  const int places = sm_count() * move::kCompactPerSm;
+  if (places < 1) return MOE_ECUDA;
+  // CTAs for one turn of the GPU, each over several pools: the chain before the first row is paid once
+  const int y = places > b->B ? places / b->B : 1;
   return move::over_layers(move::k_compact, a, kv, L, unsigned(b->B), y, move::kThreads, reinterpret_cast<cudaStream_t>(stream));
 }
 

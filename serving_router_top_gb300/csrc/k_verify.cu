@@ -430,7 +430,9 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
                     d->token, d->parent, d->u, d->u_last, d->V, b->T, path, count, token, path_stride, err_dev};
   // CTAs of a request: up to two an SM in all, and no more than have four lines of 128 values a warp to read.  Up to four
   // an SM took 64 picked trees from 21.9 to 29.2 us (64 registers), as half of the requests then wait for the others.
-  const int sms = 152, most = d->V / (128 * verify::kGroups * verify::kWarps) + 1;
+  const int sms = sm_count();
+  if (sms < 1) return MOE_ECUDA;
+  const int most = d->V / (128 * verify::kGroups * verify::kWarps) + 1;
   int ctas = verify::kMaxCtas;
   while (ctas > 1 && ((long long)b->B * ctas > 2 * sms || ctas >= 2 * most)) ctas /= 2;
   if ((long long)b->B * ctas > INT32_MAX) return MOE_EINVAL;

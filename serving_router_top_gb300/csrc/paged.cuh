@@ -2,11 +2,24 @@
 // request lookup on the device (not part of the ABI).
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace moe {
 
 constexpr int kMaxGroup = 64;  // query heads per key head
+
+// SMs of the current device, asked for once each; 0 where they cannot be told.
+inline int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 // Pools and requests as the kernels take them; strides in bytes.
 struct KvView {
