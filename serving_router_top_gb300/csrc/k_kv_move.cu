@@ -3,6 +3,8 @@
 //
 // What bounds them: memory for copies, and for kept nodes, whose few rows are a megabyte a layer at most, the
 // chain count, path, table, row, store.  One launch holds the pools of 128 layers, so a step pays for that chain once.
+#include <stdlib.h>
+
 #include "paged.cuh"
 
 namespace moe {
@@ -142,18 +144,38 @@ bool alike(const moe_kv_pages* kv, int L) {
   return true;
 }
 
-// y: CTAs over the pools of a launch, 0: one each.
+// Addresses that have been met, in an open table of at least twice as many places.
+struct Met {
+  uint8_t** at;
+  int bits = 2;
+  explicit Met(int n) {
+    while (1 << bits < 2 * n) ++bits;
+    at = static_cast<uint8_t**>(calloc(size_t(1) << bits, sizeof(uint8_t*)));
+  }
+  ~Met() { free(at); }
+  bool first(uint8_t* p) {
+    uint64_t h = (reinterpret_cast<uintptr_t>(p) >> 4) * 0x9e3779b97f4a7c15ull >> (64 - bits);
+    for (; at[h]; h = (h + 1) & ((1ull << bits) - 1))
+      if (at[h] == p) return false;
+    at[h] = p;
+    return true;
+  }
+};
+
+// Every pool once, also where layers, or a layer's keys and values, share it: a second move would find places that the
+// first has written.  y: CTAs over the pools of a launch, 0: one each.
 template <typename Kernel>
 int over_layers(Kernel kernel, Args& a, const moe_kv_pages* kv, int L, unsigned x, int y, int threads, cudaStream_t s) {
-  for (int l0 = 0; l0 < L; l0 += kPools / 2) {
-    const int m = L - l0 < kPools / 2 ? L - l0 : kPools / 2;
-    a.pools = 2 * m;
-    a.first = l0 == 0;
-    for (int l = 0; l < m; ++l) {
-      a.pool[2 * l] = static_cast<uint8_t*>(kv[l0 + l].k);
-      a.pool[2 * l + 1] = static_cast<uint8_t*>(kv[l0 + l].v);
-    }
-    if (launch_pdl(kernel, dim3(x, y > 0 && y < 2 * m ? y : 2 * m), dim3(threads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+  Met met(2 * L);
+  if (!met.at) return MOE_ENOMEM;
+  a.first = 1;
+  a.pools = 0;
+  for (int i = 0; i < 2 * L; ++i) {
+    uint8_t* p = static_cast<uint8_t*>(i & 1 ? kv[i / 2].v : kv[i / 2].k);
+    if (met.first(p)) a.pool[a.pools++] = p;
+    if (a.pools < kPools && (i + 1 < 2 * L || a.pools == 0)) continue;
+    if (launch_pdl(kernel, dim3(x, y > 0 && y < a.pools ? y : a.pools), dim3(threads), 0, s, a) != cudaSuccess) return MOE_ECUDA;
+    a.first = a.pools = 0;
   }
   return MOE_OK;
 }

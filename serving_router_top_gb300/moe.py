@@ -859,7 +859,8 @@ def moe_verify_drafts(batch: KvBatch, desc: VerifyDesc, path, count, token, err=
 
 
 class KvLayers:
-    """The pools of a model's layers, of one geometry, for the calls that move keys and values in all of them."""
+    """The pools of a model's layers, of one geometry, for the calls that move keys and values in all of them; one that
+    layers share counts once."""
 
     def __init__(self, layers):
         self.layers = list(layers)
