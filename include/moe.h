@@ -704,7 +704,7 @@ int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d, int32_t* 
  * not; count is cut to path_stride.  A place past the table or in a page outside
  * [0, npages) also records MOE_ERANGE and is neither read nor written.
  * kv_len_out int32 [B] device or NULL: base + the kept nodes, the request's
- * tokens from here on; not b->kv_len itself.  A pool that several layers share, or a
+ * tokens from here on; apart from path, count and the batch's arrays.  A pool that several layers share, or a
  * layer's keys and values, is moved once; others do not overlap.  Two requests must
  * not share a page of their trees.  L <= 4096.  Asynchronous on `stream`. */
 int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch* b, const int32_t* path, int path_stride,
