@@ -688,7 +688,8 @@ typedef struct {
 /* path int32 [B][path_stride]: the kept nodes in their order, node 0 first, then -1; at
  * most path_stride of them (the walk ends there as at a node without children).
  * count int32 [B]: how many; 0 for a request without nodes.  token int32 [B]: the
- * next token, -1 for a request without nodes.  Of b, q_start, B and T are used.
+ * next token, -1 for a request without nodes.  The three lie apart, and from the
+ * inputs.  Of b, q_start, B and T are used.
  * Nodes past 256 of a request are never reached and record MOE_ERANGE in err_dev
  * (int32[1], may be NULL), as does q_start that decreases.  path_stride >= 1, fp32
  * arrays 4-byte aligned.  Asynchronous on `stream`. */

@@ -144,12 +144,6 @@ bool alike(const moe_kv_pages* kv, int L) {
   return true;
 }
 
-// Whether n and m 32-bit words lie apart.
-bool apart(const void* p, long long n, const void* q, long long m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a + 4 * n <= b || b + 4 * m <= a;
-}
-
 // Addresses that have been met, in an open table of at least twice as many places.
 struct Met {
   uint8_t** at;
@@ -201,9 +195,9 @@ extern "C" int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch*
   if (!path || !count || !b->q_start || !b->kv_len || (!b->page_table && b->table_stride > 0)) return MOE_EINVAL;
   // the lengths are written while other CTAs, and the launches of later layers, still read what they go by
   const long long B = b->B;
-  if (kv_len_out && !(move::apart(kv_len_out, B, b->kv_len, B) && move::apart(kv_len_out, B, count, B) &&
-                      move::apart(kv_len_out, B, path, B * path_stride) && move::apart(kv_len_out, B, b->q_start, B + 1) &&
-                      move::apart(kv_len_out, B, b->page_table, B * b->table_stride)))
+  if (kv_len_out && !(apart(kv_len_out, B, b->kv_len, B) && apart(kv_len_out, B, count, B) &&
+                      apart(kv_len_out, B, path, B * path_stride) && apart(kv_len_out, B, b->q_start, B + 1) &&
+                      apart(kv_len_out, B, b->page_table, B * b->table_stride)))
     return MOE_EINVAL;
   a.vecs = kv->D * (kv->e4m3 ? 1 : 2) / 16;
   a.path = path;

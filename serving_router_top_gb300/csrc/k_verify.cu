@@ -426,6 +426,18 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
   if (b->T > 0 && (!d->target || !d->token || !d->parent || !d->u)) return MOE_EINVAL;
   if (b->T > 1 && (d->target_stride < d->V || (d->draft && d->draft_stride < d->V))) return MOE_EINVAL;
   if ((reinterpret_cast<uintptr_t>(d->target) | reinterpret_cast<uintptr_t>(d->draft)) & 3) return MOE_EINVAL;
+  // a request's outputs are written while others still read their tokens and random numbers
+  const long long B = b->B, T = b->T;
+  const struct {
+    const void* p;
+    long long n;
+  } out[3] = {{path, B * path_stride}, {count, B}, {token, B}}, in[5] = {{b->q_start, B + 1}, {d->token, T}, {d->parent, T}, {d->u, T}, {d->u_last, B}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& x : in)
+      if (!apart(out[i].p, out[i].n, x.p, x.n)) return MOE_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (!apart(out[i].p, out[i].n, out[j].p, out[j].n)) return MOE_EINVAL;
+  }
   verify::Args a = {b->q_start, d->target, d->draft, b->T > 1 ? d->target_stride : d->V, b->T > 1 ? d->draft_stride : d->V,
                     d->token, d->parent, d->u, d->u_last, d->V, b->T, path, count, token, path_stride, err_dev};
   // CTAs of a request: up to two an SM in all, and no more than have four lines of 128 values a warp to read.  Up to four

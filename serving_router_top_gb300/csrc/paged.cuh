@@ -76,6 +76,12 @@ inline int kv_view(const moe_kv_pages* p, const moe_kv_batch* b, KvView* out) {
   return MOE_OK;
 }
 
+// Whether n and m 32-bit words lie apart.
+inline bool apart(const void* p, long long n, const void* q, long long m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a + 4 * n <= b || b + 4 * m <= a;
+}
+
 // Token rows [T][heads][D] of bf16: 16-byte aligned, token stride whole 16-byte pieces.
 inline bool rows_ok(const void* p, long long stride, int T, long long width) {
   return p && !(reinterpret_cast<uintptr_t>(p) & 15) && (T <= 1 || (stride >= width && stride % 8 == 0));
