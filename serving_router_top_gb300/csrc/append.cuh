@@ -1,6 +1,7 @@
 // What the two append kernels share: arguments, their checks, and the stores (not part of the ABI).
 #pragma once
 
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 

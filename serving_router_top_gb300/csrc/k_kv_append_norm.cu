@@ -20,8 +20,8 @@ struct NormArgs {
   float eps;
 };
 
-// 8192 tokens of 32 + 2 x 4 heads of 128 columns, 168 MB: 32.3 us, 5.2 TB/s, with two items a thread and 64 registers (four
-// CTAs of 256 threads); with one fp32 at a time 33.3, of which with registers for five CTAs 34.3, for six 38.9, without a
+// 8192 tokens of 32 + 2 x 4 heads of 128 columns, 168 MB: 32.8 us, 5.1 TB/s, with two items a thread and 64 registers (four
+// CTAs of 256 threads).  Without the look at sums past fp32 32.3 us; of that, with one fp32 at a time 33.3, of which with registers for five CTAs 34.3, for six 38.9, without a
 // limit 34.2; with one item a thread 39.6 at its best, three 33.2, four 34.1.  It issues on two cycles of three; a third of
 // its instructions find request, page and angles.
 constexpr int kMine = 2, kPerSm = 4;
@@ -121,17 +121,27 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) k_kv_append_norm(const __
     unpack8(x.v0, f0);
     unpack8(x.v1, f1);
     if (na.norm && x.head < a.Hq + a.kv.Hkv) {
-      float2 both = make_float2(0.f, 0.f);
+      auto squares = [&]() {  // of the head's columns, the same in all its lanes
+        float2 both = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 u = make_float2(f0[i], f0[i + 1]), v = make_float2(f1[i], f1[i + 1]);
-        both = __ffma2_rn(u, u, __ffma2_rn(v, v, both));
+        for (int i = 0; i < 8; i += 2) {
+          const float2 u = make_float2(f0[i], f0[i + 1]), v = make_float2(f1[i], f1[i + 1]);
+          both = __ffma2_rn(u, u, __ffma2_rn(v, v, both));
+        }
+        float sum = both.x + both.y;
+        const unsigned mates = ((1u << kItems) - 1) << ((threadIdx.x & 31) / kItems * kItems);
+#pragma unroll
+        for (int o = 1; o < kItems; o <<= 1) sum += __shfl_xor_sync(mates, sum, o);
+        return sum;
+      };
+      float sum = squares(), eps = na.eps;
+      if (sum > FLT_MAX) {  // columns from 2^60 on: 2^-96 of them has the same norm, with eps taken along
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f0[i] *= 0x1p-96f, f1[i] *= 0x1p-96f;
+        sum = squares();
+        eps = eps * 0x1p-96f * 0x1p-96f;
       }
-      float sum = both.x + both.y;
-      const unsigned mates = ((1u << kItems) - 1) << ((threadIdx.x & 31) / kItems * kItems);
-#pragma unroll
-      for (int o = 1; o < kItems; o <<= 1) sum += __shfl_xor_sync(mates, sum, o);
-      const float inv = rsqrtf(sum * (1.f / D) + na.eps);
+      const float inv = rsqrtf(sum * (1.f / D) + eps);
       const int z = x.head >= a.Hq ? D / 8 : 0;
       const float2 inv2 = make_float2(inv, inv);
       float w[8];
