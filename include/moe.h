@@ -626,7 +626,7 @@ typedef struct {
 /* Fills depth, above and below from parent, once for all layers of a step.  A parent
  * that is not below its node's index is taken as -1; so are all nodes of a request
  * past 32 * words, whose masks are empty; both record MOE_ERANGE in err_dev
- * (int32[1], may be NULL).  Rows outside [q_start[0], q_start[B]) are left as they
+ * (int32[1], may be NULL), as does q_start that decreases.  Rows outside [q_start[0], q_start[B]) are left as they
  * are.  Asynchronous on `stream`. */
 int moe_tree_prepare(const moe_kv_batch* b, const moe_tree* tree, int32_t* err_dev, moe_stream_t stream);
 
@@ -669,8 +669,9 @@ int moe_tree_attention(const moe_kv_pages* kv, const moe_kv_batch* b, const moe_
  * q independently of one another (or picked before u is known), kept tokens and next
  * token are distributed as the target's.
  * Rows are probabilities: an entry below 0 or NaN counts as 0, one above 1 as 1; sums
- * above 4 count as 4, s below 0 as 0.  Sums are kept in fixed point, 2^-60 a unit: no order of sums
- * changes a result.  A u below 0 or NaN counts as 0, from 1 on as the largest below 1. */
+ * above 4 count as 4, s below 0 as 0.  Sums are kept in fixed point, 2^-60 a unit: no
+ * order of sums changes a result.  A u below 0 or NaN counts as 0, from 1 on as the
+ * largest below 1. */
 typedef struct {
   const float* target;    /* fp32 [T][V] device, one row a node                           */
   long long target_stride; /* elements between rows, at least V (not checked for T <= 1)  */
@@ -701,8 +702,8 @@ int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d, int32_t* 
  * same): place base + path[b][d] goes to place base + d for d < count[b].  path
  * int32 [B][path_stride] and count int32 [B] device, as moe_verify_drafts writes
  * them: indices rise and are below n_b, else MOE_ERANGE is recorded in err_dev
- * (int32[1], may be NULL) and the request's path ends before the first that does
- * not; count is cut to path_stride.  A place past the table or in a page outside
+ * (int32[1], may be NULL), as does q_start that decreases, and the request's path ends
+ * before the first that does not; count is cut to path_stride.  A place past the table or in a page outside
  * [0, npages) also records MOE_ERANGE and is neither read nor written.
  * kv_len_out int32 [B] device or NULL: base + the kept nodes, the request's
  * tokens from here on; apart from path, count and the batch's arrays.  A pool that several layers share, or a

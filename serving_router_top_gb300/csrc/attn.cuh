@@ -131,7 +131,11 @@ struct Cfg {
   static constexpr int V = !E4M3 && SLOT * H * 2 >= 65536 ? 2 : 3;
   // Trees, whose units end in tiles that hide keys by their masks.  32 trees of up to 16 nodes over 60 to 8192 tokens, 128
   // columns, with 2, 3, 4, 5, 6 and 8: 55.0, 48.6, 47.6, 48.6, 49.9 and 52.4 us; 64 columns with 3, 4, 5, 6 and 8: 41.7, 37.0,
-  // 36.0, 35.0 and 36.6; E4M3, 128 columns, up to 4 nodes, with 2, 3, 4, 5, 6 and 8: 38.8, 34.7, 32.8, 32.3, 32.1 and 33.9.
+  // 36.0, 35.0 and 36.6; E4M3, 128 columns, up to 4 nodes, with 2, 3, 4, 5, 6 and 8: 38.8, 34.7, 32.8, 32.3, 32.1 and 33.9;
+  // E4M3, 64 columns, 32 of up to 4, 8 and 16 nodes of four heads with 3, 4, 5, 6 and 8: 32.3, 30.6, 30.3, 29.7, 31.2; 58.1,
+  // 56.9, 52.1, 49.2, 48.7; 61.0, 55.6, 53.8, 51.8, 50.0.  With 256 columns nothing hangs on it: 16 of up to 4 nodes of
+  // eight heads over 60 to 32768 tokens with 2, 3, 4, 5, 6 and 8 56.7, 56.4, 56.6, 56.4, 56.2 and 56.9, E4M3 46.3, 44.2, 41.6,
+  // 42.4, 41.3 and 42.1; 64 over 60 to 2000 tokens 26.7, 25.9, 26.6, 28.1, 26.6 and 29.1, E4M3 29.8, 28.2, 26.9, 28.8, 28.1, 31.3.
   static constexpr int VT = !E4M3 && D == 128 ? 4 : 6;
   static_assert(V <= 3 && VT <= 6, "places of a unit, as the call's checks count them");
   static_assert(COLS0 <= 512 && (E4M3 ? NK >= 2 && NRAW >= 2 : NS >= 3), "resources of an SM");
@@ -1494,11 +1498,17 @@ constexpr int kWideRows = 128;  // of attn_wide.cuh
 inline int row_tile(int D, int G, int n) {
   return 16 / G >= n ? 16 : 32 / G >= n ? 32 : 64 / G >= n || D > 128 ? 64 : kChunkRows;
 }
-// The same for trees.  Those with more than 32 rows a key head of 256 columns go to attn_wide.cuh: 16 trees of 8 nodes of 8
-// heads (64 rows) over 512 to 32768 tokens 54.5 us in bf16 and 49.7 in E4M3, in 64-row tiles of attn.cuh 58.5 and 61.0;
-// one of them over 717 tokens 14.4 and 13.7.  With 64 columns there is a tile of 48 rows: 48 trees of up to 12 nodes of three
-// heads (36 rows) under a window of 1000 33.0 us, in 64 rows 36.2; with 128 columns memory is the bound and it
-// makes no difference (52.9 and 52.9).
+// The same for trees.  Those with more than 32 rows a key head of 256 columns go to attn_wide.cuh.  Trees of 8 nodes of 8
+// heads (64 rows) there, and in 64-row tiles of attn.cuh: 16 over 512 to 32768 tokens 54.6 and 58.2 us, E4M3 50.1 and 62.3; 64
+// over 100 to 2000 33.9 and 36.1, E4M3 35.5 and 47.6; one over 8000 26.6 and 35.6, E4M3 27.2 and 42.0; over 717 tokens one
+// 14.3 and 13.6, four 16.1 and 15.7, eight 17.2 and 18.2, E4M3 one 16.1 and 19.3.  So the other way round is better by half a
+// microsecond for a few short bf16 requests alone, which the host cannot tell from long ones.
+//
+// With 64 columns there is a tile of 48 rows.  There, and in 64 rows: 48 trees of up to 12 nodes of three heads (36 rows) over
+// 60 to 8192 tokens 40.0 and 42.7 us, under a window of 1000 30.7 and 33.4; 32 of up to 12 of four (48 rows) 36.2 and 38.3, with
+// the window 27.5 and 29.6, all of 12 over 4096 54.0 and 55.3; 11 nodes (33 rows) 33.9 and 36.5; one over 1000 11.0 and 11.5.
+// With 128 columns memory is the bound and it makes no difference (52.9 and 52.9).  E4M3 has none, as its softmax warps hold
+// 32 rows: with 16 they would be twelve beside eight that convert.
 inline int tree_row_tile(int D, int G, int n, bool e4m3) {
   const int nr = row_tile(D, G, n);
   if (D == 256 && nr == 64) return kWideRows;

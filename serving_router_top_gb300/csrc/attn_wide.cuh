@@ -13,11 +13,12 @@
 //
 // attn.cuh's form takes these rows 64 at a time, reads keys and values as often, and has no slot to spare beside a key
 // and a value tile.  16 trees of up to 32 nodes of 8 heads over 512 to 32768 tokens (22 rows' worth of nodes on average):
-// bf16 63.7 us, E4M3 69.4 with the join; in 64-row tiles 96 and 111.
+// bf16 64.1 us, E4M3 69.7 with the join; in 64-row tiles 96 and 111.
 //
 // What bounds it: memory's way.  Without the conversions E4M3 takes 61 us, without exponentials or maxima, or with half the
-// products, what it takes with them; bf16 over pages that the L2 holds 50.4 (of 63.7).  The join is 8 to 12 us of either:
-// each of 152 runs leaves one or two pieces of 128 x 256 sums.
+// products, what it takes with them; bf16 over pages that the L2 holds 50.4.  The join is 8 to 12 us of either: each of 152
+// runs leaves one or two pieces of 128 x 256 sums.  In E4M3, with 96 registers a thread at launch, 228 bytes a thread of the
+// softmax are spilled.
 #pragma once
 
 #include "attn_chunk.cuh"

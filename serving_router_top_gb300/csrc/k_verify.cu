@@ -19,7 +19,7 @@
 //
 // What bounds it: a chain of trips to memory (requests; parents and tokens; the nodes' values; the rows) and of the
 // cluster's barriers, launch beside them.  A chain of 6 drawn nodes over 131072 tokens 8.2 us on sixteen CTAs; 64 picked trees
-// of up to 16 nodes over 100001 tokens 16.5 us, 1.5 TB/s of the last nodes' rows, and 64 drawn chains over 131072 29.4 us, 2.3
+// of up to 16 nodes over 100001 tokens 16.3 us, 1.6 TB/s of the last nodes' rows, and 64 drawn chains over 131072 29.4 us, 2.3
 // TB/s.  Eight CTAs of 256 threads, which read the drawn group again, took 16.8 us for the first and 30.3 for the second.
 #include "paged.cuh"
 
@@ -431,7 +431,8 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
   const struct {
     const void* p;
     long long n;
-  } out[3] = {{path, B * path_stride}, {count, B}, {token, B}}, in[5] = {{b->q_start, B + 1}, {d->token, T}, {d->parent, T}, {d->u, T}, {d->u_last, B}};
+  } out[3] = {{path, B * path_stride}, {count, B}, {token, B}},
+    in[5] = {{b->q_start, B + 1}, {d->token, T}, {d->parent, T}, {d->u, T}, {d->u_last, B}};
   for (int i = 0; i < 3; ++i) {
     for (const auto& x : in)
       if (!apart(out[i].p, out[i].n, x.p, x.n)) return MOE_EINVAL;
@@ -440,16 +441,19 @@ extern "C" int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d
   }
   verify::Args a = {b->q_start, d->target, d->draft, b->T > 1 ? d->target_stride : d->V, b->T > 1 ? d->draft_stride : d->V,
                     d->token, d->parent, d->u, d->u_last, d->V, b->T, path, count, token, path_stride, err_dev};
-  // CTAs of a request: up to two an SM in all, and no more than have four lines of 128 values a warp to read.  Up to four
-  // an SM took 64 picked trees from 21.9 to 29.2 us (64 registers), as half of the requests then wait for the others.
+  // CTAs of a request: up to two an SM in all, and no more than have four lines of 128 values a warp to read.  With one, two,
+  // four and eight an SM 64 picked trees take 18.4, 16.3, 23.2 and 41.5 us and 64 drawn chains 30.9, 29.5, 35.8 and 55.8, as
+  // requests past the second wait for others to end; 32 drawn chains 19.1, 19.3, 32.0 and 32.0.
   const int sms = sm_count();
   if (sms < 1) return MOE_ECUDA;
   const int most = d->V / (128 * verify::kGroups * verify::kWarps) + 1;
   int ctas = verify::kMaxCtas;
   while (ctas > 1 && ((long long)b->B * ctas > 2 * sms || ctas >= 2 * most)) ctas /= 2;
   if ((long long)b->B * ctas > INT32_MAX) return MOE_EINVAL;
-  // Registers for one CTA an SM where there are no more, else for two: a drawn chain 8.2 us with 128 and 9.8 with 64, which
-  // spill; 64 picked trees 29.5 and 16.5
+  // Registers for one CTA an SM where there are no more, else for two, which spill where drafts are drawn.  With 128 and with
+  // 64: one drawn chain 8.2 and 9.2 us, four 9.3 and 12.1, eight drawn trees of 16 29.2 and 32.4, one picked chain 6.6 and
+  // 6.7; 64 picked trees 25.0 and 16.3.  Eight drawn chains are the exception, 16.5 and 13.6: at one CTA an SM seven
+  // clusters of sixteen find a place.
   const bool alone = (long long)b->B * ctas <= sms;
   auto* kernel = d->draft ? alone ? verify::k_verify<true, 1> : verify::k_verify<true, 2>
                           : alone ? verify::k_verify<false, 1> : verify::k_verify<false, 2>;
