@@ -626,8 +626,8 @@ typedef struct {
 /* Fills depth, above and below from parent, once for all layers of a step.  A parent
  * that is not below its node's index is taken as -1; so are all nodes of a request
  * past 32 * words, whose masks are empty; both record MOE_ERANGE in err_dev
- * (int32[1], may be NULL), as does q_start that decreases.  Rows outside [q_start[0], q_start[B]) are left as they
- * are.  Asynchronous on `stream`. */
+ * (int32[1], may be NULL), as does q_start that decreases.  Rows outside [q_start[0],
+ * q_start[B]) are left as they are.  Asynchronous on `stream`. */
 int moe_tree_prepare(const moe_kv_batch* b, const moe_tree* tree, int32_t* err_dev, moe_stream_t stream);
 
 /* Norms of each head's query and key rows: w * x / sqrt(mean(x^2) + eps) over D columns. */
@@ -703,12 +703,12 @@ int moe_verify_drafts(const moe_kv_batch* b, const moe_verify_desc* d, int32_t* 
  * int32 [B][path_stride] and count int32 [B] device, as moe_verify_drafts writes
  * them: indices rise and are below n_b, else MOE_ERANGE is recorded in err_dev
  * (int32[1], may be NULL), as does q_start that decreases, and the request's path ends
- * before the first that does not; count is cut to path_stride.  A place past the table or in a page outside
- * [0, npages) also records MOE_ERANGE and is neither read nor written.
- * kv_len_out int32 [B] device or NULL: base + the kept nodes, the request's
- * tokens from here on; apart from path, count and the batch's arrays.  A pool that several layers share, or a
- * layer's keys and values, is moved once; others do not overlap.  Two requests must
- * not share a page of their trees.  L <= 4096.  Asynchronous on `stream`. */
+ * before the first that does not; count is cut to path_stride.  A place past the table
+ * or in a page outside [0, npages) also records MOE_ERANGE and is neither read nor
+ * written.  kv_len_out int32 [B] device or NULL: base + the kept nodes, the request's
+ * tokens from here on; apart from path, count and the batch's arrays.  A pool that
+ * several layers share, or a layer's keys and values, is moved once; others do not
+ * overlap.  Two requests must not share a page of their trees.  L <= 4096.  Asynchronous on `stream`. */
 int moe_kv_compact(const moe_kv_pages* kv, int L, const moe_kv_batch* b, const int32_t* path, int path_stride,
                    const int32_t* count, int32_t* kv_len_out, int32_t* err_dev, moe_stream_t stream);
 
